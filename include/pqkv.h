@@ -317,6 +317,83 @@ int pqkv_paged_attention_noalloc(const void* q, void* out, const void* pages, in
                                  const float* v_scale, int32_t scale_per_head, int32_t num_splits,
                                  int32_t max_seq_len, int32_t* status, void* stream);
 
+/*
+ * pqkv_extend_block_tables -- grow every request by its new tokens: take the
+ * pages it needs from a stack of free pages, write them into its block-table
+ * row, and give every token its pool slot and its position, all on the device.
+ * (ReVolta v0.1.3 release note, "Known issues": 16-token kernel pages.  The
+ * pages leave the allocation to their serving engine; the stack is this
+ * library's choice.)
+ *
+ * With L = seq_lens[s], n = new_tokens[s], have = ceil(L/16),
+ * need = ceil((L+n)/16) - have, and upto the sum of need over requests 0..s:
+ *   - the request is SERVED when need == 0 or upto <= free_count; its j-th new
+ *     page is free_pages[free_count - 1 - (upto - need + j)] (the stack's top
+ *     first), written to block_table[s][have + j];
+ *   - its tokens follow those of the requests before it in slot_mapping:
+ *     token i sits at position pos = L + i in slot
+ *     block_table[s][pos/16]*16 + pos%16;
+ *   - seq_lens_out[s] = L + n.
+ * A request that is not served keeps its length, takes no page, and its n
+ * tokens get slot -1 (which pqkv_kv_append_quant skips) and position -1.  It
+ * is not served
+ *   - when the stack runs out (PQKV_DEV_SLOT_RANGE); no later request gets
+ *     pages then, while requests that need none are still served;
+ *   - when L or n is negative, L + n exceeds max_pages_per_seq*16, or its
+ *     tokens end beyond num_tokens (PQKV_DEV_SEQ_RANGE).
+ * A token whose page id is outside [0, num_pages) gets slot and position -1
+ * (PQKV_DEV_PAGE_RANGE).
+ *
+ *   seq_lens, new_tokens  int32 [num_seqs].
+ *   block_table    int32 [num_seqs][max_pages_per_seq]; only new entries are written.
+ *   free_pages     int32 [max_free_pages], the stack; entries 0..free_count-1
+ *                  are free pages.  Not written.
+ *   free_count     int32 [1]; outside [0, max_free_pages] it is clamped
+ *                  (PQKV_DEV_SLOT_RANGE).
+ *   seq_lens_out   int32 [num_seqs], free_count_out int32 [1]: the state after
+ *                  the call; either may be the input itself (in place).
+ *   slot_mapping   int64 [num_tokens]: one entry per token of the step's batch;
+ *                  entries behind the last request's tokens become -1.
+ *   positions      int32 [num_tokens] or NULL, -1 where the slot is.
+ *   token_offsets  int32 [num_seqs+1] or NULL: each request's first token (and
+ *                  the end), at most num_tokens.
+ * The other outputs must not overlap the inputs.  num_seqs <= 2048,
+ * page_size == 16.  Stateless: no workspace.
+ */
+int pqkv_extend_block_tables(const int32_t* seq_lens, const int32_t* new_tokens, int32_t num_seqs,
+                             int32_t* block_table, int32_t max_pages_per_seq,
+                             const int32_t* free_pages, const int32_t* free_count,
+                             int32_t max_free_pages, int64_t num_pages, int32_t page_size,
+                             int32_t* seq_lens_out, int32_t* free_count_out, int64_t* slot_mapping,
+                             int32_t* positions, int32_t num_tokens, int32_t* token_offsets,
+                             int32_t* status, void* stream);
+
+/*
+ * pqkv_truncate_block_tables -- shorten requests and push their pages back on
+ * the stack: draft tokens that a verify step rejected, or whole requests that
+ * have ended.  (ReVolta README, "Quick start": MTP verify of 4 draft tokens,
+ * of which any number may be rejected.)
+ *
+ * Request s keeps its first keep_lens[s] tokens.  The pages with index in
+ * [max(ceil(keep/16), owned_pages[s]), ceil(seq_lens[s]/16)) of its row are
+ * pushed, requests in order, pages in order, from free_pages[free_count] on.
+ * The row itself is left as it is.
+ * A request with keep < 0, keep > seq_lens[s], or seq_lens[s] beyond its row
+ * is left as it is (PQKV_DEV_SEQ_RANGE).  Pages that find no room on the stack
+ * (free_count would exceed max_free_pages) are dropped (PQKV_DEV_SLOT_RANGE).
+ *
+ *   owned_pages  int32 [num_seqs] or NULL (all 0): the row's first page that
+ *                belongs to this request; the pages before it are another's
+ *                (a shared prefix) and are never pushed.
+ *   seq_lens_out, free_count_out  as in pqkv_extend_block_tables.
+ */
+int pqkv_truncate_block_tables(const int32_t* seq_lens, const int32_t* keep_lens,
+                               const int32_t* owned_pages, int32_t num_seqs,
+                               const int32_t* block_table, int32_t max_pages_per_seq,
+                               int32_t* free_pages, const int32_t* free_count,
+                               int32_t max_free_pages, int32_t page_size, int32_t* seq_lens_out,
+                               int32_t* free_count_out, int32_t* status, void* stream);
+
 /* Bytes at the start of the workspace that hold merge counters. */
 #define PQKV_COUNTER_BYTES(num_seqs, num_kv_heads) \
   ((((size_t)(num_seqs) * (size_t)(num_kv_heads) * 4u) + 255u) & ~(size_t)255u)

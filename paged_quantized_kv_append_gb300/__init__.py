@@ -85,6 +85,13 @@ def load_library(path: str | None = None):
                                                      c_vp, c_vp, c_sz, c_vp, c_vp]
         lib.pqkv_lse_merge.restype = ctypes.c_int
         lib.pqkv_lse_merge.argtypes = [c_vp, c_vp, c_i32, c_i64, c_i32, c_vp, c_vp, c_vp]
+        lib.pqkv_extend_block_tables.restype = ctypes.c_int
+        lib.pqkv_extend_block_tables.argtypes = [c_vp, c_vp, c_i32, c_vp, c_i32, c_vp, c_vp, c_i32,
+                                                 c_i64, c_i32, c_vp, c_vp, c_vp, c_vp, c_i32, c_vp,
+                                                 c_vp, c_vp]
+        lib.pqkv_truncate_block_tables.restype = ctypes.c_int
+        lib.pqkv_truncate_block_tables.argtypes = [c_vp, c_vp, c_vp, c_i32, c_vp, c_i32, c_vp,
+                                                   c_vp, c_i32, c_i32, c_vp, c_vp, c_vp, c_vp]
         lib.pqkv_status_string.restype = ctypes.c_char_p
         lib.pqkv_status_string.argtypes = [ctypes.c_int]
         lib.pqkv_version.restype = ctypes.c_char_p
@@ -405,6 +412,90 @@ def lse_merge(parts_o, parts_lse, out, out_lse=None, stream=None):
                                 _ptr(out_lse), _stream(out, stream))
     _check(rc, "lse_merge")
     return out
+
+
+def _int_tensor(name, x, dtype, shape, dev):
+    """A contiguous integer CUDA tensor of this shape (None: any length) on dev."""
+    if x.dtype != dtype or x.dim() != len(shape) or not x.is_contiguous() or x.device != dev or \
+            any(n is not None and m != n for m, n in zip(x.shape, shape)):
+        raise ValueError("%s must be a contiguous %s tensor %s on %s, got %s %s on %s" % (
+            name, dtype, list(shape), dev, x.dtype, list(x.shape), x.device))
+
+
+def _table_args(seq_lens, block_table, free_pages, free_count, seq_lens_out, free_count_out,
+                status):
+    dev = block_table.device
+    if dev.type != "cuda":
+        raise ValueError("block_table must be a CUDA tensor")
+    i32 = torch.int32
+    _int_tensor("block_table", block_table, i32, (None, None), dev)
+    B = block_table.shape[0]
+    _int_tensor("seq_lens", seq_lens, i32, (B,), dev)
+    _int_tensor("seq_lens_out", seq_lens_out, i32, (B,), dev)
+    _int_tensor("free_pages", free_pages, i32, (None,), dev)
+    _int_tensor("free_count", free_count, i32, (1,), dev)
+    _int_tensor("free_count_out", free_count_out, i32, (1,), dev)
+    _check_status(status, dev)
+    return dev, B
+
+
+def extend_block_tables(seq_lens, new_tokens, block_table, free_pages, free_count, num_pages,
+                        seq_lens_out, free_count_out, slot_mapping, positions=None,
+                        token_offsets=None, status=None, stream=None):
+    """Grow every request by ``new_tokens[s]`` tokens (int32 [B]): take pages
+    from the top of the stack ``free_pages[:free_count]``, write them into
+    ``block_table`` (int32 [B, max_pages_per_seq]), and fill ``slot_mapping``
+    (int64 [T]: the tokens of request 0, then of request 1, ..., then -1) for
+    kv_append_quant, with each token's position in its request and each
+    request's first token if asked for.  ``num_pages`` is the pool's size.
+
+    A request that finds no pages, or whose tokens fit neither its row nor
+    ``slot_mapping``, keeps its length, and its tokens get slot -1 (reported in
+    ``status``).  ``seq_lens_out`` / ``free_count_out`` may be the inputs
+    themselves.  Returns slot_mapping."""
+    dev, B = _table_args(seq_lens, block_table, free_pages, free_count, seq_lens_out,
+                         free_count_out, status)
+    _int_tensor("new_tokens", new_tokens, torch.int32, (B,), dev)
+    _int_tensor("slot_mapping", slot_mapping, torch.int64, (None,), dev)
+    T = slot_mapping.shape[0]
+    if positions is not None:
+        _int_tensor("positions", positions, torch.int32, (T,), dev)
+    if token_offsets is not None:
+        _int_tensor("token_offsets", token_offsets, torch.int32, (B + 1,), dev)
+    lib = load_library()
+    with torch.cuda.device(dev):
+        rc = lib.pqkv_extend_block_tables(
+            _ptr(seq_lens), _ptr(new_tokens), B, _ptr(block_table), block_table.shape[1],
+            _ptr(free_pages), _ptr(free_count), free_pages.shape[0], num_pages, PAGE_SIZE,
+            _ptr(seq_lens_out), _ptr(free_count_out), _ptr(slot_mapping), _ptr(positions), T,
+            _ptr(token_offsets), _ptr(status), _stream(block_table, stream))
+    _check(rc, "extend_block_tables")
+    return slot_mapping
+
+
+def truncate_block_tables(seq_lens, keep_lens, block_table, free_pages, free_count, seq_lens_out,
+                          free_count_out, owned_pages=None, status=None, stream=None):
+    """Shorten every request to its first ``keep_lens[s]`` tokens and push the
+    pages it no longer needs on the stack ``free_pages`` (from entry
+    ``free_count`` on): rejected draft tokens, or ended requests (keep 0).
+    Pages before ``owned_pages[s]`` (int32 [B], default all 0) belong to
+    another request -- a shared prefix -- and stay.  The block table is not
+    changed.  ``seq_lens_out`` / ``free_count_out`` may be the inputs
+    themselves.  Returns seq_lens_out."""
+    dev, B = _table_args(seq_lens, block_table, free_pages, free_count, seq_lens_out,
+                         free_count_out, status)
+    _int_tensor("keep_lens", keep_lens, torch.int32, (B,), dev)
+    if owned_pages is not None:
+        _int_tensor("owned_pages", owned_pages, torch.int32, (B,), dev)
+    lib = load_library()
+    with torch.cuda.device(dev):
+        rc = lib.pqkv_truncate_block_tables(
+            _ptr(seq_lens), _ptr(keep_lens), _ptr(owned_pages), B, _ptr(block_table),
+            block_table.shape[1], _ptr(free_pages), _ptr(free_count), free_pages.shape[0],
+            PAGE_SIZE, _ptr(seq_lens_out), _ptr(free_count_out), _ptr(status),
+            _stream(block_table, stream))
+    _check(rc, "truncate_block_tables")
+    return seq_lens_out
 
 
 NOALLOC_SCRATCH_BYTES = 16 << 20

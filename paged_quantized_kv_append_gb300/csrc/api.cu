@@ -125,6 +125,20 @@ int validate_heads(int32_t num_seqs, int32_t q_len, int32_t hq, int32_t hkv) {
   return PQKV_OK;
 }
 
+int check_table_args(int32_t num_seqs, int32_t max_pages_per_seq, int32_t max_free_pages,
+                     int32_t page_size, const void* free_pages, const void* free_count,
+                     const void* free_count_out, const void* status) {
+  if (num_seqs < 0 || max_pages_per_seq < 1 || max_free_pages < 0) return PQKV_EINVAL;
+  if (page_size != kPageSize) return PQKV_EUNSUPPORTED;
+  if (num_seqs > PQKV_MAX_SEQS) return PQKV_ERANGE;
+  if ((int64_t)max_pages_per_seq * page_size > PQKV_MAX_SEQ_LEN + page_size) return PQKV_ERANGE;
+  if (!free_count || !free_count_out || (max_free_pages > 0 && !free_pages)) return PQKV_EINVAL;
+  if (!aligned(free_count, 4) || !aligned(free_count_out, 4) || !aligned(free_pages, 4) ||
+      !aligned(status, 4))
+    return PQKV_EINVAL;
+  return PQKV_OK;
+}
+
 }  // namespace
 }  // namespace pqkv
 
@@ -446,6 +460,87 @@ extern "C" int pqkv_lse_merge(const float* part_o, const float* part_lse, int32_
                                          static_cast<uint16_t*>(out), out_lse,
                                          static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? PQKV_OK : PQKV_ECUDA;
+}
+
+extern "C" int pqkv_extend_block_tables(const int32_t* seq_lens, const int32_t* new_tokens,
+                                        int32_t num_seqs, int32_t* block_table,
+                                        int32_t max_pages_per_seq, const int32_t* free_pages,
+                                        const int32_t* free_count, int32_t max_free_pages,
+                                        int64_t num_pages, int32_t page_size,
+                                        int32_t* seq_lens_out, int32_t* free_count_out,
+                                        int64_t* slot_mapping, int32_t* positions,
+                                        int32_t num_tokens, int32_t* token_offsets,
+                                        int32_t* status, void* stream) {
+  int rc = check_table_args(num_seqs, max_pages_per_seq, max_free_pages, page_size, free_pages,
+                            free_count, free_count_out, status);
+  if (rc) return rc;
+  if (num_tokens < 0 || num_pages < 0 || num_pages > INT32_MAX) return PQKV_EINVAL;
+  if (num_seqs > 0 && (!seq_lens || !new_tokens || !block_table || !seq_lens_out))
+    return PQKV_EINVAL;
+  if (num_tokens > 0 && !slot_mapping) return PQKV_EINVAL;
+  if (!aligned(seq_lens, 4) || !aligned(new_tokens, 4) || !aligned(block_table, 4) ||
+      !aligned(seq_lens_out, 4) || !aligned(slot_mapping, 8) || !aligned(positions, 4) ||
+      !aligned(token_offsets, 4))
+    return PQKV_EINVAL;
+  int sms = 0;
+  rc = current_device_sms(&sms);
+  if (rc) return rc;
+  ExtendParams p = {};
+  p.seq_lens = seq_lens;
+  p.new_tokens = new_tokens;
+  p.block_table = block_table;
+  p.free_pages = free_pages;
+  p.free_count = free_count;
+  p.seq_lens_out = seq_lens_out;
+  p.free_count_out = free_count_out;
+  p.slot_mapping = slot_mapping;
+  p.positions = positions;
+  p.token_offsets = token_offsets;
+  p.status = status;
+  p.num_pages = num_pages;
+  p.num_seqs = num_seqs;
+  p.max_pages_per_seq = max_pages_per_seq;
+  p.max_free = max_free_pages;
+  p.num_tokens = num_tokens;
+  return launch_extend_tables(p, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? PQKV_OK
+             : PQKV_ECUDA;
+}
+
+extern "C" int pqkv_truncate_block_tables(const int32_t* seq_lens, const int32_t* keep_lens,
+                                          const int32_t* owned_pages, int32_t num_seqs,
+                                          const int32_t* block_table, int32_t max_pages_per_seq,
+                                          int32_t* free_pages, const int32_t* free_count,
+                                          int32_t max_free_pages, int32_t page_size,
+                                          int32_t* seq_lens_out, int32_t* free_count_out,
+                                          int32_t* status, void* stream) {
+  int rc = check_table_args(num_seqs, max_pages_per_seq, max_free_pages, page_size, free_pages,
+                            free_count, free_count_out, status);
+  if (rc) return rc;
+  if (num_seqs > 0 && (!seq_lens || !keep_lens || !block_table || !seq_lens_out))
+    return PQKV_EINVAL;
+  if (!aligned(seq_lens, 4) || !aligned(keep_lens, 4) || !aligned(owned_pages, 4) ||
+      !aligned(block_table, 4) || !aligned(seq_lens_out, 4))
+    return PQKV_EINVAL;
+  int sms = 0;
+  rc = current_device_sms(&sms);
+  if (rc) return rc;
+  TruncateParams p = {};
+  p.seq_lens = seq_lens;
+  p.keep_lens = keep_lens;
+  p.owned_pages = owned_pages;
+  p.block_table = block_table;
+  p.free_pages = free_pages;
+  p.free_count = free_count;
+  p.seq_lens_out = seq_lens_out;
+  p.free_count_out = free_count_out;
+  p.status = status;
+  p.num_seqs = num_seqs;
+  p.max_pages_per_seq = max_pages_per_seq;
+  p.max_free = max_free_pages;
+  return launch_truncate_tables(p, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? PQKV_OK
+             : PQKV_ECUDA;
 }
 
 namespace pqkv {

@@ -131,6 +131,48 @@ constexpr int kAppendUnroll = 1;
 cudaError_t launch_append(const AppendParams& p, int kv_dtype, int grid, cudaStream_t stream);
 int append_blocks_per_sm(int kv_dtype);
 
+// Block tables grown (extend) and shortened (truncate) on the device.
+struct ExtendParams {
+  const int32_t* seq_lens;
+  const int32_t* new_tokens;
+  int32_t* block_table;
+  const int32_t* free_pages;
+  const int32_t* free_count;
+  int32_t* seq_lens_out;
+  int32_t* free_count_out;
+  int64_t* slot_mapping;
+  int32_t* positions;       // may be null
+  int32_t* token_offsets;   // may be null
+  int32_t* status;
+  int64_t num_pages;
+  int32_t num_seqs;
+  int32_t max_pages_per_seq;
+  int32_t max_free;
+  int32_t num_tokens;
+  int32_t write_tokens;     // this launch writes slots, positions, offsets and table entries
+  int32_t write_state;      // this launch writes seq_lens_out and free_count_out
+};
+
+struct TruncateParams {
+  const int32_t* seq_lens;
+  const int32_t* keep_lens;
+  const int32_t* owned_pages;   // may be null
+  const int32_t* block_table;
+  int32_t* free_pages;
+  const int32_t* free_count;
+  int32_t* seq_lens_out;
+  int32_t* free_count_out;
+  int32_t* status;
+  int32_t num_seqs;
+  int32_t max_pages_per_seq;
+  int32_t max_free;
+  int32_t write_pages;      // this launch writes the free stack
+  int32_t write_state;      // this launch writes seq_lens_out and free_count_out
+};
+
+cudaError_t launch_extend_tables(ExtendParams p, int sms, cudaStream_t stream);
+cudaError_t launch_truncate_tables(TruncateParams p, int sms, cudaStream_t stream);
+
 // The arguments of one attention call (the shared part of the entry points).
 struct AttnArgs {
   const void* q;
