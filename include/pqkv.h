@@ -318,6 +318,54 @@ int pqkv_paged_attention_noalloc(const void* q, void* out, const void* pages, in
                                  int32_t max_seq_len, int32_t* status, void* stream);
 
 /*
+ * pqkv_paged_attention_shared_prefix -- pqkv_paged_attention for a batch whose
+ * sequences share prefixes (a system prompt, a long document): the keys of a
+ * shared prefix are read once for all the sequences that share it, instead of
+ * once per sequence.  (ReVolta README, "Quick start": 8 concurrent requests
+ * with prefix caching; the pages describe no kernel for it.)
+ *
+ * The sequences come in groups of neighbours: group g holds sequences
+ * group_offsets[g] .. group_offsets[g+1]-1, whose first prefix_lens[g] tokens
+ * are the same tokens IN THE SAME POOL PAGES, so their block-table rows agree
+ * over the first floor(prefix_lens[g]/16) entries; the entries of the group's
+ * first row are the ones read.  The result is that of pqkv_paged_attention on
+ * the same arguments (up to the order of the sums).  Shared are the whole pages
+ * of min(prefix_lens[g], min over the group of seq_lens[s] - q_len): a prefix
+ * that ends inside a page, and the q_len new tokens, stay private.
+ * prefix_lens[g] < 16 shares nothing; groups may be empty.
+ *
+ *   q, out, pages, block_table, seq_lens, k_scale, v_scale, status and the
+ *   size arguments as in pqkv_paged_attention.
+ *   group_offsets   int32 [num_groups+1] (device), from 0 to num_seqs, not
+ *                   falling; otherwise PQKV_DEV_SEQ_RANGE, and nothing is shared
+ *                   (the result is still right).
+ *   prefix_lens     int32 [num_groups] (device); negative, or longer than a
+ *                   sequence of the group: PQKV_DEV_SEQ_RANGE, and clamped.
+ *   max_seq_len, max_prefix_len  upper bounds of seq_lens and prefix_lens that
+ *                   size the launches (0: unknown).  They change speed only.
+ *   workspace       device scratch of at least
+ *                   pqkv_paged_attention_shared_prefix_workspace_size() bytes,
+ *                   256-byte aligned.  It needs no initial value and keeps
+ *                   nothing between calls.  Calls that share a workspace must
+ *                   not overlap on the device.
+ * 1 <= num_groups <= 2048.  Bitwise reproducible run to run on one device.
+ */
+int pqkv_paged_attention_shared_prefix(
+    const void* q, void* out, const void* pages, int64_t num_pages, const int32_t* block_table,
+    int32_t max_pages_per_seq, const int32_t* seq_lens, int32_t num_seqs,
+    const int32_t* group_offsets, const int32_t* prefix_lens, int32_t num_groups, int32_t q_len,
+    int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, int32_t page_size,
+    int32_t kv_dtype, const float* k_scale, const float* v_scale, int32_t scale_per_head,
+    int32_t max_seq_len, int32_t max_prefix_len, void* workspace, size_t workspace_bytes,
+    int32_t* status, void* stream);
+
+/* Bytes of workspace of pqkv_paged_attention_shared_prefix for these sizes (0
+ * for sizes it refuses).  Pure host function. */
+size_t pqkv_paged_attention_shared_prefix_workspace_size(int32_t num_seqs, int32_t num_groups,
+                                                         int32_t q_len, int32_t num_q_heads,
+                                                         int32_t num_kv_heads, int32_t head_dim);
+
+/*
  * pqkv_extend_block_tables -- grow every request by its new tokens: take the
  * pages it needs from a stack of free pages, write them into its block-table
  * row, and give every token its pool slot and its position, all on the device.

@@ -85,6 +85,12 @@ def load_library(path: str | None = None):
                                                      c_vp, c_vp, c_sz, c_vp, c_vp]
         lib.pqkv_lse_merge.restype = ctypes.c_int
         lib.pqkv_lse_merge.argtypes = [c_vp, c_vp, c_i32, c_i64, c_i32, c_vp, c_vp, c_vp]
+        lib.pqkv_paged_attention_shared_prefix_workspace_size.restype = c_sz
+        lib.pqkv_paged_attention_shared_prefix_workspace_size.argtypes = [c_i32] * 6
+        lib.pqkv_paged_attention_shared_prefix.restype = ctypes.c_int
+        lib.pqkv_paged_attention_shared_prefix.argtypes = [
+            c_vp, c_vp, c_vp, c_i64, c_vp, c_i32, c_vp, c_i32, c_vp, c_vp, c_i32, c_i32, c_i32,
+            c_i32, c_i32, c_i32, c_i32, c_vp, c_vp, c_i32, c_i32, c_i32, c_vp, c_sz, c_vp, c_vp]
         lib.pqkv_extend_block_tables.restype = ctypes.c_int
         lib.pqkv_extend_block_tables.argtypes = [c_vp, c_vp, c_i32, c_vp, c_i32, c_vp, c_vp, c_i32,
                                                  c_i64, c_i32, c_vp, c_vp, c_vp, c_vp, c_i32, c_vp,
@@ -411,6 +417,70 @@ def lse_merge(parts_o, parts_lse, out, out_lse=None, stream=None):
         rc = lib.pqkv_lse_merge(_ptr(parts_o), _ptr(parts_lse), P, rows, HEAD_DIM, _ptr(out),
                                 _ptr(out_lse), _stream(out, stream))
     _check(rc, "lse_merge")
+    return out
+
+
+def shared_prefix_workspace_size(num_seqs, num_groups, q_len, num_q_heads, num_kv_heads) -> int:
+    """Bytes of workspace of paged_attention_shared_prefix (0: sizes it refuses)."""
+    return int(load_library().pqkv_paged_attention_shared_prefix_workspace_size(
+        num_seqs, num_groups, q_len, num_q_heads, num_kv_heads, HEAD_DIM))
+
+
+def paged_attention_shared_prefix(q, pages, block_table, seq_lens, group_offsets, prefix_lens,
+                                  q_len, kv_dtype, k_scale, v_scale, out, max_seq_len=0,
+                                  max_prefix_len=0, workspace=None, status=None, stream=None):
+    """paged_attention of a batch whose sequences share prefixes, each prefix's
+    keys read once for all the sequences that share it.
+
+    Sequences ``group_offsets[g]`` .. ``group_offsets[g + 1] - 1`` (int32
+    [num_groups + 1]) start with the same ``prefix_lens[g]`` tokens (int32
+    [num_groups]) in the same pool pages: their ``block_table`` rows agree over
+    the whole pages of that length.  Everything else, and the result, as in
+    paged_attention.  ``max_seq_len`` / ``max_prefix_len`` are upper bounds of
+    the lengths (0: unknown) that only size the launches.  The default
+    workspace is taken from the caching allocator for the call; a uint8 tensor
+    of shared_prefix_workspace_size() bytes may be given instead."""
+    kd = _dtype_id(kv_dtype)
+    _check_pages(pages, kd)
+    H = pages.shape[1]
+    dev = pages.device
+    if q.dtype != torch.float16 or q.dim() != 3 or q.shape[2] != HEAD_DIM or not q.is_contiguous():
+        raise ValueError("q must be contiguous fp16 [num_seqs*q_len, Hq, 128]")
+    if out.shape != q.shape or out.dtype != torch.float16 or not out.is_contiguous():
+        raise ValueError("out must be contiguous fp16 shaped like q")
+    i32 = torch.int32
+    _int_tensor("seq_lens", seq_lens, i32, (None,), dev)
+    B = seq_lens.shape[0]
+    _int_tensor("block_table", block_table, i32, (B, None), dev)
+    _int_tensor("prefix_lens", prefix_lens, i32, (None,), dev)
+    M = prefix_lens.shape[0]
+    _int_tensor("group_offsets", group_offsets, i32, (M + 1,), dev)
+    if q.shape[0] != B * q_len:
+        raise ValueError("q has %d rows, expected num_seqs*q_len = %d" % (q.shape[0], B * q_len))
+    Hq = q.shape[1]
+    sph = 0
+    if kd in _SCALED:
+        sph = _check_scale(k_scale, H, "k_scale")
+        if _check_scale(v_scale, H, "v_scale") != sph:
+            raise ValueError("k_scale and v_scale must have the same shape")
+        _on_device(dev, k_scale=k_scale, v_scale=v_scale)
+    else:
+        k_scale = v_scale = None
+    _on_device(dev, q=q, out=out, workspace=workspace)
+    _check_status(status, dev)
+    lib = load_library()
+    with torch.cuda.device(dev):
+        if workspace is None:
+            need = shared_prefix_workspace_size(B, M, q_len, Hq, H)
+            with torch.cuda.stream(stream):
+                workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        rc = lib.pqkv_paged_attention_shared_prefix(
+            _ptr(q), _ptr(out), _ptr(pages), pages.shape[0], _ptr(block_table),
+            block_table.shape[1], _ptr(seq_lens), B, _ptr(group_offsets), _ptr(prefix_lens), M,
+            q_len, Hq, H, HEAD_DIM, PAGE_SIZE, kd, _ptr(k_scale), _ptr(v_scale), sph, max_seq_len,
+            max_prefix_len, _ptr(workspace), workspace.numel() * workspace.element_size(),
+            _ptr(status), _stream(q, stream))
+    _check(rc, "paged_attention_shared_prefix")
     return out
 
 

@@ -207,7 +207,7 @@ extern "C" size_t pqkv_paged_attention_workspace_size(int32_t num_seqs, int32_t 
 
 namespace pqkv {
 
-int plan_attention_launch(const AttnArgs& a, AttnLaunch* L) {
+int check_attention_args(const AttnArgs& a) {
   int rc = validate_common(a.head_dim, a.page_size, a.kv_dtype);
   if (rc) return rc;
   rc = validate_heads(a.num_seqs, a.q_len, a.num_q_heads, a.num_kv_heads);
@@ -223,6 +223,12 @@ int plan_attention_launch(const AttnArgs& a, AttnLaunch* L) {
   if (!aligned(a.q, 16) || !aligned(a.pages, 16) || !aligned(a.block_table, 4) ||
       !aligned(a.seq_lens, 4))
     return PQKV_EINVAL;
+  return PQKV_OK;
+}
+
+int plan_attention_launch(const AttnArgs& a, AttnLaunch* L) {
+  int rc = check_attention_args(a);
+  if (rc || a.num_seqs == 0) return rc;
   int sms = 0;
   rc = current_device_sms(&sms);
   if (rc) return rc;
@@ -261,15 +267,8 @@ int plan_attention_launch(const AttnArgs& a, AttnLaunch* L) {
   return PQKV_OK;
 }
 
-int bind_attention(const AttnArgs& a, const AttnLaunch& L, void* workspace,
-                   size_t workspace_bytes, int32_t* status, AttnParams* pp, CUtensorMap* mapp) {
-  const AttnPlan& pl = L.pl;
-  if (pl.total > 0) {
-    if (!workspace) return PQKV_EWORKSPACE;
-    if (!aligned(workspace, 256) || workspace_bytes < pl.total) return PQKV_EWORKSPACE;
-  }
-
-  // TMA map over the pool: [num_pages][Hkv][lines][128 bytes]
+// TMA map over the pool: [num_pages][Hkv][lines][128 bytes]
+int encode_pool_map(const AttnArgs& a, CUtensorMap* mapp) {
   PFN_cuTensorMapEncodeTiled_v12000 enc = encoder();
   if (!enc) return PQKV_ECUDA;
   const int eb = elem_bytes(a.kv_dtype);
@@ -287,6 +286,19 @@ int bind_attention(const AttnArgs& a, const AttnLaunch& L, void* workspace,
                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (cr != CUDA_SUCCESS) return PQKV_ECUDA;
+  return PQKV_OK;
+}
+
+int bind_attention(const AttnArgs& a, const AttnLaunch& L, void* workspace,
+                   size_t workspace_bytes, int32_t* status, AttnParams* pp, CUtensorMap* mapp) {
+  const AttnPlan& pl = L.pl;
+  if (pl.total > 0) {
+    if (!workspace) return PQKV_EWORKSPACE;
+    if (!aligned(workspace, 256) || workspace_bytes < pl.total) return PQKV_EWORKSPACE;
+  }
+
+  const int rc = encode_pool_map(a, mapp);
+  if (rc) return rc;
 
   AttnParams& p = *pp;
   p.q = static_cast<const uint16_t*>(a.q);
@@ -460,6 +472,54 @@ extern "C" int pqkv_lse_merge(const float* part_o, const float* part_lse, int32_
                                          static_cast<uint16_t*>(out), out_lse,
                                          static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? PQKV_OK : PQKV_ECUDA;
+}
+
+extern "C" size_t pqkv_paged_attention_shared_prefix_workspace_size(
+    int32_t num_seqs, int32_t num_groups, int32_t q_len, int32_t num_q_heads, int32_t num_kv_heads,
+    int32_t head_dim) {
+  if (head_dim != kHeadDim || num_groups < 1 || num_groups > PQKV_MAX_SEQS) return 0;
+  if (num_seqs < 1 || validate_heads(num_seqs, q_len, num_q_heads, num_kv_heads)) return 0;
+  return shared_prefix_workspace(num_seqs, num_groups, q_len, num_q_heads, num_kv_heads);
+}
+
+extern "C" int pqkv_paged_attention_shared_prefix(
+    const void* q, void* out, const void* pages, int64_t num_pages, const int32_t* block_table,
+    int32_t max_pages_per_seq, const int32_t* seq_lens, int32_t num_seqs,
+    const int32_t* group_offsets, const int32_t* prefix_lens, int32_t num_groups, int32_t q_len,
+    int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, int32_t page_size,
+    int32_t kv_dtype, const float* k_scale, const float* v_scale, int32_t scale_per_head,
+    int32_t max_seq_len, int32_t max_prefix_len, void* workspace, size_t workspace_bytes,
+    int32_t* status, void* stream) {
+  AttnArgs a{q, pages, num_pages, block_table, max_pages_per_seq, seq_lens, num_seqs, q_len,
+             num_q_heads, num_kv_heads, head_dim, page_size, kv_dtype, k_scale, v_scale,
+             scale_per_head, 0, max_seq_len};
+  int rc = check_output_args(a, !out || !aligned(out, 16));
+  if (rc) return rc;
+  rc = check_attention_args(a);
+  if (rc) return rc;
+  if (max_prefix_len < 0) return PQKV_EINVAL;
+  if (num_seqs == 0) return PQKV_OK;
+  if (num_groups < 1 || !group_offsets || !prefix_lens || !aligned(group_offsets, 4) ||
+      !aligned(prefix_lens, 4) || !aligned(status, 4))
+    return PQKV_EINVAL;
+  if (num_groups > PQKV_MAX_SEQS) return PQKV_ERANGE;
+  const size_t need =
+      shared_prefix_workspace(num_seqs, num_groups, q_len, num_q_heads, num_kv_heads);
+  if (!workspace || !aligned(workspace, 256) || workspace_bytes < need) return PQKV_EWORKSPACE;
+  int sms = 0;
+  rc = current_device_sms(&sms);
+  if (rc) return rc;
+  CUtensorMap map;
+  rc = encode_pool_map(a, &map);
+  if (rc) return rc;
+  if (kv_dtype == PQKV_KV_INT8_ROW)   // as in the other attention calls: the scale area
+    a.k_scale = reinterpret_cast<const float*>(
+        row_scale_area(const_cast<void*>(pages), num_pages, num_kv_heads));
+  const SharedArgs sa{group_offsets, prefix_lens, num_groups, max_prefix_len};
+  return launch_shared_prefix(a, sa, out, map, workspace, sms, status,
+                              static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? PQKV_OK
+             : PQKV_ECUDA;
 }
 
 extern "C" int pqkv_extend_block_tables(const int32_t* seq_lens, const int32_t* new_tokens,

@@ -204,6 +204,11 @@ struct AttnLaunch {
   AttnPlan pl;
 };
 
+// Validate the arguments of an attention call on the host (all but the
+// outputs and the workspace).  Queues nothing.
+int check_attention_args(const AttnArgs& a);
+// Encode the TMA map over the pool.
+int encode_pool_map(const AttnArgs& a, CUtensorMap* map);
 // Validate the arguments and size the launch (grid and workspace need) on the
 // current device.  Queues nothing.  num_seqs == 0 returns PQKV_OK with an
 // empty launch.
@@ -218,6 +223,23 @@ cudaError_t launch_attention(int kv_dtype, const AttnParams& p, const CUtensorMa
 // PQKV_EINVAL (after the size checks) when num_seqs > 0 and an output
 // argument is missing or misaligned.
 int check_output_args(const AttnArgs& a, bool bad_outputs);
+
+// Shared-prefix attention (shared_prefix.cuh): the arguments of one call beside
+// the attention's own, and its workspace.
+struct SharedArgs {
+  const int32_t* group_offsets;
+  const int32_t* prefix_lens;
+  int32_t num_groups;
+  int32_t max_prefix_len;
+};
+
+// Bytes of workspace of a shared-prefix call of these (valid) sizes.
+size_t shared_prefix_workspace(int32_t num_seqs, int32_t num_groups, int32_t q_len, int32_t hq,
+                               int32_t hkv);
+// Queue the kernels of one validated call.
+cudaError_t launch_shared_prefix(const AttnArgs& a, const SharedArgs& sa, void* out,
+                                 const CUtensorMap& map, void* workspace, int sms,
+                                 int32_t* status, cudaStream_t stream);
 
 inline int rows_padded(int rows) { return ((rows + 7) / 8) * 8; }
 

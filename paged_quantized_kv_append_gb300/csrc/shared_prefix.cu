@@ -1,0 +1,314 @@
+// Shared-prefix attention: the plan (which keys are shared, who has how many
+// pages), the merge of the partial results, and the launch of one call.  The
+// attention over the prefix and over the private keys is in shared_prefix.cuh.
+#include <algorithm>
+#include <cmath>
+
+#include "shared_prefix.cuh"
+
+namespace pqkv {
+namespace {
+
+constexpr int kPlanThreads = 512;
+constexpr int kPlanEach = PQKV_MAX_SEQS / kPlanThreads;
+
+__device__ __forceinline__ int last_at_most(const int* a, int n, int x) {
+  int lo = 0, hi = n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (a[mid] <= x) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
+
+// exclusive sum over the block's threads; `total` gets the sum
+__device__ __forceinline__ int block_scan(int v, int& total) {
+  __shared__ int w[kPlanThreads / 32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += u;
+  }
+  __syncthreads();
+  if (lane == 31) w[warp] = x;
+  __syncthreads();
+  int before = 0;
+  total = 0;
+#pragma unroll
+  for (int i = 0; i < kPlanThreads / 32; ++i) {
+    if (i == warp) before = total;
+    total += w[i];
+  }
+  return before + x - v;
+}
+
+// One block.  The shared pages of group g are the whole pages of
+// min(prefix_lens[g], min_s(L_s - q_len)): keys before every query of the
+// group, so no row needs a mask in the prefix, and every sequence keeps at
+// least its q_len new tokens private.
+__global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedParams p) {
+  __shared__ int s_off[PQKV_MAX_SEQS + 1];
+  __shared__ int s_min[PQKV_MAX_SEQS];
+  grid_dependency_wait();
+  grid_dependents_launch();
+  const int tid = threadIdx.x, B = p.num_seqs, M = p.num_groups;
+  // -- the groups: contiguous, in order, every sequence in one.  Offsets that
+  //    are not are reported, and nothing is shared then
+  bool ok = true;
+  for (int g = tid; g <= M; g += kPlanThreads) {
+    const int v = p.group_offsets[g];
+    const int prev = g > 0 ? p.group_offsets[g - 1] : 0;
+    ok = ok && (g > 0 ? v >= prev : v == 0) && (g < M || v == B);
+    s_off[g] = v;
+    if (g < M) s_min[g] = 0x7fffffff;
+  }
+  ok = __syncthreads_and(ok);
+  if (!ok) {
+    if (tid == 0) report(p.status, PQKV_DEV_SEQ_RANGE);
+    for (int g = tid; g <= M; g += kPlanThreads) s_off[g] = g == 0 ? 0 : B;
+  }
+  __syncthreads();
+  // -- the sequences' lengths, and the shortest of each group
+  const int per = (B + kPlanThreads - 1) / kPlanThreads;
+  int len[kPlanEach], grp[kPlanEach];
+#pragma unroll
+  for (int i = 0; i < kPlanEach; ++i) {
+    const int s = tid * per + i;
+    len[i] = grp[i] = 0;
+    if (i >= per || s >= B) continue;
+    int L = p.seq_lens[s];
+    const int Lmax = p.bt_stride * kPageSize;
+    if (L < p.q_len || L > Lmax) {
+      report(p.status, PQKV_DEV_SEQ_RANGE);
+      L = max(p.q_len, min(L, Lmax));
+    }
+    len[i] = L;
+    grp[i] = last_at_most(s_off, M, s);
+    atomicMin(&s_min[grp[i]], L - p.q_len);
+  }
+  __syncthreads();
+  // -- the groups' shared pages, row tiles and (tile, page) pairs
+  const int gper = (M + kPlanThreads - 1) / kPlanThreads;
+  int tiles[kPlanEach], pairs[kPlanEach], tsum = 0, psum = 0;
+#pragma unroll
+  for (int i = 0; i < kPlanEach; ++i) {
+    const int g = tid * gper + i;
+    tiles[i] = pairs[i] = 0;
+    if (i >= gper || g >= M) continue;
+    const int n = s_off[g + 1] - s_off[g], want = p.prefix_lens[g];
+    int pages = 0;
+    if (n > 0 && ok) {
+      if (want < 0 || want > s_min[g] + p.q_len) report(p.status, PQKV_DEV_SEQ_RANGE);
+      pages = max(0, min(want, s_min[g])) / kPageSize;
+    }
+    p.plan.gpages[g] = pages;
+    p.plan.goff[g] = s_off[g];
+    tiles[i] = pages > 0 ? (n * p.rows + p.tile_rows - 1) / p.tile_rows : 0;
+    pairs[i] = tiles[i] * pages;
+    tsum += tiles[i];
+    psum += pairs[i];
+    s_min[g] = pages;
+  }
+  int total_t, total_p;
+  int at_t = block_scan(tsum, total_t), at_p = block_scan(psum, total_p);
+#pragma unroll
+  for (int i = 0; i < kPlanEach; ++i) {
+    const int g = tid * gper + i;
+    if (i >= gper || g >= M) continue;
+    p.plan.gtiles[g] = at_t;
+    p.plan.gpre[g] = at_p;
+    at_t += tiles[i];
+    at_p += pairs[i];
+  }
+  if (tid == 0) {
+    p.plan.gtiles[M] = total_t;
+    p.plan.gpre[M] = total_p;
+    p.plan.goff[M] = B;
+  }
+  __syncthreads();
+  // -- the private pages
+  int own = 0, total_s;
+#pragma unroll
+  for (int i = 0; i < kPlanEach; ++i) {
+    const int s = tid * per + i;
+    if (i >= per || s >= B) continue;
+    own += (len[i] + kPageSize - 1) / kPageSize - s_min[grp[i]];
+  }
+  int at = block_scan(own, total_s);
+#pragma unroll
+  for (int i = 0; i < kPlanEach; ++i) {
+    const int s = tid * per + i;
+    if (i >= per || s >= B) continue;
+    p.plan.len[s] = len[i];
+    p.plan.group[s] = grp[i];
+    p.plan.page0[s] = s_min[grp[i]];
+    p.plan.spre[s] = at;
+    at += (len[i] + kPageSize - 1) / kPageSize - s_min[grp[i]];
+  }
+  if (tid == 0) p.plan.spre[B] = total_s;
+}
+
+// One warp per output row: the row's fragments, prefix first, folded in with a
+// running maximum (a fixed order, so the result is deterministic).
+__global__ void __launch_bounds__(256) shared_merge_kernel(const SharedParams p, int scaled) {
+  grid_dependency_wait();
+  grid_dependents_launch();
+  const int lane = threadIdx.x & 31;
+  const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int H = p.num_kv_heads;
+  if (row >= (int64_t)p.num_seqs * p.q_len * p.num_q_heads) return;
+  const int hq = (int)(row % p.num_q_heads);
+  const int tok = (int)(row / p.num_q_heads);
+  const int s = tok / p.q_len, i = tok % p.q_len, h = hq / p.group, gq = hq % p.group;
+  const int g = p.plan.group[s];
+  float M = kNoScore, l = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  auto fold = [&](const float* o, const float* ml, int RP, int64_t seg, const Shares& sh,
+                  int64_t a, int64_t b, int r) {
+    const int w1 = sh.owner(b - 1);
+    for (int w = sh.owner(a); w <= w1; ++w) {
+      const int64_t slot = seg + w;
+      const float m = __ldg(ml + slot * 2 * RP + r), lw = __ldg(ml + slot * 2 * RP + RP + r);
+      const float4 v = __ldg(reinterpret_cast<const float4*>(o + (slot * RP + r) * kHeadDim) + lane);
+      const float Mn = fmaxf(M, m);
+      const float f0 = ex2(M - Mn), f1 = ex2(m - Mn);
+      l = l * f0 + lw * f1;
+      acc.x = acc.x * f0 + v.x * f1;
+      acc.y = acc.y * f0 + v.y * f1;
+      acc.z = acc.z * f0 + v.z * f1;
+      acc.w = acc.w * f0 + v.w * f1;
+      M = Mn;
+    }
+  };
+  const int np = p.plan.gpages[g];
+  if (np > 0) {
+    const int R = (s - p.plan.goff[g]) * p.rows + i * p.group + gq;
+    const int nt = p.plan.gtiles[g + 1] - p.plan.gtiles[g];
+    const int seg = h * nt + R / p.tile_rows;
+    const int64_t a = (int64_t)p.plan.gpre[g] * H + (int64_t)seg * np;
+    fold(p.pre_o, p.pre_ml, p.pre_rp, (int64_t)p.plan.gtiles[g] * H + seg,
+         Shares((int64_t)p.plan.gpre[p.num_groups] * H, p.pre_workers), a, a + np,
+         R % p.tile_rows);
+  }
+  const int a0 = p.plan.spre[s], n = p.plan.spre[s + 1] - a0;
+  const int64_t a = (int64_t)a0 * H + (int64_t)h * n;
+  fold(p.suf_o, p.suf_ml, p.suf_rp, (int64_t)s * H + h,
+       Shares((int64_t)p.plan.spre[p.num_seqs] * H, p.suf_workers), a, a + n, i * p.group + gq);
+  float inv = l > 0.f ? 1.f / l : 0.f;
+  if (scaled) inv *= __ldg(p.v_scale + (p.scale_per_head ? h : 0));
+  __half2 h01 = __floats2half2_rn(acc.x * inv, acc.y * inv);
+  __half2 h23 = __floats2half2_rn(acc.z * inv, acc.w * inv);
+  uint2 pk;
+  pk.x = *reinterpret_cast<uint32_t*>(&h01);
+  pk.y = *reinterpret_cast<uint32_t*>(&h23);
+  *reinterpret_cast<uint2*>(p.out + row * kHeadDim + 4 * lane) = pk;
+}
+
+constexpr int kMaxSms = 160;   // the workspace holds the partial results of this many SMs
+
+size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
+
+// Sizes of a call, and where its arrays lie in the workspace.
+struct SharedLayout {
+  int tile_rows, pre_rp, suf_rp, pre_workers, suf_workers;
+  size_t pre_o, pre_ml, suf_o, suf_ml, total;   // offsets
+
+  SharedLayout(int B, int M, int q_len, int hq, int hkv, int sms = kMaxSms) {
+    const int rows = hq / hkv * q_len;
+    tile_rows = pre_rp = (int)std::min<int64_t>(32, ((int64_t)B * rows + 7) / 8 * 8);
+    suf_rp = rows_padded(rows);
+    sms = std::min(sms, kMaxSms);
+    pre_workers = sms * shared_blocks_per_sm(pre_rp / 8) * 8;
+    suf_workers = sms * shared_blocks_per_sm(suf_rp / 8) * 8;
+    const int64_t pre_slots =
+        (((int64_t)B * rows + tile_rows - 1) / tile_rows + M) * hkv + pre_workers;
+    const int64_t suf_slots = (int64_t)B * hkv + suf_workers;
+    size_t at = up256((size_t)(4 * (B + 1) + 4 * (M + 1)) * 4);
+    auto take = [&](size_t bytes) {
+      const size_t here = at;
+      at += up256(bytes);
+      return here;
+    };
+    pre_o = take((size_t)pre_slots * pre_rp * kHeadDim * 4);
+    pre_ml = take((size_t)pre_slots * 2 * pre_rp * 4);
+    suf_o = take((size_t)suf_slots * suf_rp * kHeadDim * 4);
+    suf_ml = take((size_t)suf_slots * 2 * suf_rp * 4);
+    total = at;
+  }
+};
+
+}  // namespace
+
+size_t shared_prefix_workspace(int32_t num_seqs, int32_t num_groups, int32_t q_len, int32_t hq,
+                               int32_t hkv) {
+  return SharedLayout(num_seqs, num_groups, q_len, hq, hkv).total;
+}
+
+cudaError_t launch_shared_prefix(const AttnArgs& a, const SharedArgs& sa, void* out,
+                                 const CUtensorMap& map, void* workspace, int sms,
+                                 int32_t* status, cudaStream_t stream) {
+  const int B = a.num_seqs, M = sa.num_groups;
+  const SharedLayout lay(B, M, a.q_len, a.num_q_heads, a.num_kv_heads, sms);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  SharedParams p = {};
+  p.q = static_cast<const uint16_t*>(a.q);
+  p.out = static_cast<uint16_t*>(out);
+  p.block_table = a.block_table;
+  p.seq_lens = a.seq_lens;
+  p.group_offsets = sa.group_offsets;
+  p.prefix_lens = sa.prefix_lens;
+  p.k_scale = a.k_scale;
+  p.v_scale = a.v_scale;
+  p.status = status;
+  int32_t* at = reinterpret_cast<int32_t*>(ws);
+  auto take = [&](int n) {
+    int32_t* here = at;
+    at += n;
+    return here;
+  };
+  p.plan.len = take(B);
+  p.plan.group = take(B);
+  p.plan.page0 = take(B);
+  p.plan.spre = take(B + 1);
+  p.plan.goff = take(M + 1);
+  p.plan.gpages = take(M);
+  p.plan.gtiles = take(M + 1);
+  p.plan.gpre = take(M + 1);
+  p.pre_o = reinterpret_cast<float*>(ws + lay.pre_o);
+  p.pre_ml = reinterpret_cast<float*>(ws + lay.pre_ml);
+  p.suf_o = reinterpret_cast<float*>(ws + lay.suf_o);
+  p.suf_ml = reinterpret_cast<float*>(ws + lay.suf_ml);
+  p.num_pages = a.num_pages;
+  p.bt_stride = a.max_pages_per_seq;
+  p.num_seqs = B;
+  p.num_groups = M;
+  p.q_len = a.q_len;
+  p.num_q_heads = a.num_q_heads;
+  p.num_kv_heads = a.num_kv_heads;
+  p.group = a.num_q_heads / a.num_kv_heads;
+  p.rows = p.group * a.q_len;
+  p.scale_per_head = a.scale_per_head ? 1 : 0;
+  p.tile_rows = lay.tile_rows;
+  p.pre_rp = lay.pre_rp;
+  p.suf_rp = lay.suf_rp;
+  p.pre_workers = lay.pre_workers;
+  p.suf_workers = lay.suf_workers;
+  p.sm_scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)a.head_dim));
+
+  cudaError_t e = launch_pdl(shared_plan_kernel, 1, kPlanThreads, 0, stream, p);
+  if (e != cudaSuccess) return e;
+  switch (a.kv_dtype) {
+    case PQKV_KV_FP16: e = launch_shared_fp16(p, map, stream); break;
+    case PQKV_KV_FP8_E4M3: e = launch_shared_e4m3(p, map, stream); break;
+    case PQKV_KV_INT8_ROW: e = launch_shared_int8_row(p, map, stream); break;
+    default: e = launch_shared_int8(p, map, stream); break;
+  }
+  if (e != cudaSuccess) return e;
+  const int64_t rows = (int64_t)B * a.q_len * a.num_q_heads;
+  const int scaled = a.kv_dtype == PQKV_KV_FP8_E4M3 || a.kv_dtype == PQKV_KV_INT8;
+  return launch_pdl(shared_merge_kernel, (unsigned)((rows + 7) / 8), 256, 0, stream, p, scaled);
+}
+
+}  // namespace pqkv
