@@ -289,6 +289,26 @@ int encode_pool_map(const AttnArgs& a, CUtensorMap* mapp) {
   return PQKV_OK;
 }
 
+// TMA map over the pool with a row's 128-byte parts as an axis of their own:
+// [num_pages][Hkv][K and V rows][parts][128 bytes]; a box is one part of 16 rows
+int encode_prefix_map(const AttnArgs& a, CUtensorMap* map) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc = encoder();
+  if (!enc) return PQKV_ECUDA;
+  const int eb = elem_bytes(a.kv_dtype);
+  const cuuint64_t row = (cuuint64_t)a.head_dim * eb, tile = 2 * a.page_size * row;
+  std::memset(map, 0, sizeof(*map));
+  const cuuint64_t dims[5] = {(cuuint64_t)(128 / eb), row / 128, (cuuint64_t)(2 * a.page_size),
+                              (cuuint64_t)a.num_kv_heads, (cuuint64_t)a.num_pages};
+  const cuuint64_t strides[4] = {128, row, tile, tile * a.num_kv_heads};
+  const cuuint32_t box[5] = {(cuuint32_t)(128 / eb), 1, (cuuint32_t)a.page_size, 1, 1};
+  const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+  const CUresult cr = enc(map, eb == 2 ? CU_TENSOR_MAP_DATA_TYPE_UINT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8,
+                          5, const_cast<void*>(a.pages), dims, strides, box, estr,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return cr == CUDA_SUCCESS ? PQKV_OK : PQKV_ECUDA;
+}
+
 int bind_attention(const AttnArgs& a, const AttnLaunch& L, void* workspace,
                    size_t workspace_bytes, int32_t* status, AttnParams* pp, CUtensorMap* mapp) {
   const AttnPlan& pl = L.pl;
@@ -509,14 +529,16 @@ extern "C" int pqkv_paged_attention_shared_prefix(
   int sms = 0;
   rc = current_device_sms(&sms);
   if (rc) return rc;
-  CUtensorMap map;
+  CUtensorMap map, prefix_map;
   rc = encode_pool_map(a, &map);
+  if (rc) return rc;
+  rc = encode_prefix_map(a, &prefix_map);
   if (rc) return rc;
   if (kv_dtype == PQKV_KV_INT8_ROW)   // as in the other attention calls: the scale area
     a.k_scale = reinterpret_cast<const float*>(
         row_scale_area(const_cast<void*>(pages), num_pages, num_kv_heads));
   const SharedArgs sa{group_offsets, prefix_lens, num_groups, max_prefix_len};
-  return launch_shared_prefix(a, sa, out, map, workspace, sms, status,
+  return launch_shared_prefix(a, sa, out, prefix_map, map, workspace, sms, status,
                               static_cast<cudaStream_t>(stream)) == cudaSuccess
              ? PQKV_OK
              : PQKV_ECUDA;

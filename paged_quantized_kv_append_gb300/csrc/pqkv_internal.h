@@ -209,6 +209,8 @@ struct AttnLaunch {
 int check_attention_args(const AttnArgs& a);
 // Encode the TMA map over the pool.
 int encode_pool_map(const AttnArgs& a, CUtensorMap* map);
+// The map whose box is 128 bytes of each of a page's 16 K (or V) rows.
+int encode_prefix_map(const AttnArgs& a, CUtensorMap* map);
 // Validate the arguments and size the launch (grid and workspace need) on the
 // current device.  Queues nothing.  num_seqs == 0 returns PQKV_OK with an
 // empty launch.
@@ -238,8 +240,8 @@ size_t shared_prefix_workspace(int32_t num_seqs, int32_t num_groups, int32_t q_l
                                int32_t hkv);
 // Queue the kernels of one validated call.
 cudaError_t launch_shared_prefix(const AttnArgs& a, const SharedArgs& sa, void* out,
-                                 const CUtensorMap& map, void* workspace, int sms,
-                                 int32_t* status, cudaStream_t stream);
+                                 const CUtensorMap& prefix_map, const CUtensorMap& map,
+                                 void* workspace, int sms, int32_t* status, cudaStream_t stream);
 
 inline int rows_padded(int rows) { return ((rows + 7) / 8) * 8; }
 

@@ -1,11 +1,14 @@
 // Shared-prefix attention instantiations for one KV format (kept in its own
 // translation unit so the formats compile in parallel).
-#include "shared_prefix.cuh"
+#include "shared_umma.cuh"
 
 namespace pqkv {
 
-cudaError_t launch_shared_int8(const SharedParams& p, const CUtensorMap& map, cudaStream_t st) {
-  return launch_shared_dtype<PQKV_KV_INT8>(p, map, st);
+cudaError_t launch_shared_int8(const SharedParams& p, const CUtensorMap& prefix_map,
+                             const CUtensorMap& map, cudaStream_t st) {
+  const cudaError_t e = launch_shared_umma_t<PQKV_KV_INT8>(p, prefix_map, st);
+  if (e != cudaSuccess) return e;
+  return launch_private_dtype<PQKV_KV_INT8>(p, map, p.suf_rp / 8, st);
 }
 
 }  // namespace pqkv

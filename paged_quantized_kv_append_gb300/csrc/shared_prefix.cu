@@ -4,6 +4,7 @@
 #include <algorithm>
 #include <cmath>
 
+#include "attention_impl.cuh"
 #include "shared_prefix.cuh"
 
 namespace pqkv {
@@ -89,13 +90,13 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedP
     atomicMin(&s_min[grp[i]], L - p.q_len);
   }
   __syncthreads();
-  // -- the groups' shared pages, row tiles and (tile, page) pairs
+  // -- the groups' shared pages, row tiles and costs
   const int gper = (M + kPlanThreads - 1) / kPlanThreads;
-  int tiles[kPlanEach], pairs[kPlanEach], tsum = 0, psum = 0;
+  int tiles[kPlanEach], costs[kPlanEach], tsum = 0, psum = 0;
 #pragma unroll
   for (int i = 0; i < kPlanEach; ++i) {
     const int g = tid * gper + i;
-    tiles[i] = pairs[i] = 0;
+    tiles[i] = costs[i] = 0;
     if (i >= gper || g >= M) continue;
     const int n = s_off[g + 1] - s_off[g], want = p.prefix_lens[g];
     int pages = 0;
@@ -105,10 +106,10 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedP
     }
     p.plan.gpages[g] = pages;
     p.plan.goff[g] = s_off[g];
-    tiles[i] = pages > 0 ? (n * p.rows + p.tile_rows - 1) / p.tile_rows : 0;
-    pairs[i] = tiles[i] * pages;
+    tiles[i] = pages > 0 ? umma_tiles(n * p.rows) : 0;
+    costs[i] = umma_weight(n * p.rows) * ((pages + kUmmaPages - 1) / kUmmaPages);
     tsum += tiles[i];
-    psum += pairs[i];
+    psum += costs[i];
     s_min[g] = pages;
   }
   int total_t, total_p;
@@ -118,13 +119,13 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedP
     const int g = tid * gper + i;
     if (i >= gper || g >= M) continue;
     p.plan.gtiles[g] = at_t;
-    p.plan.gpre[g] = at_p;
+    p.plan.gcost[g] = at_p;
     at_t += tiles[i];
-    at_p += pairs[i];
+    at_p += costs[i];
   }
   if (tid == 0) {
     p.plan.gtiles[M] = total_t;
-    p.plan.gpre[M] = total_p;
+    p.plan.gcost[M] = total_p;
     p.plan.goff[M] = B;
   }
   __syncthreads();
@@ -165,37 +166,41 @@ __global__ void __launch_bounds__(256) shared_merge_kernel(const SharedParams p,
   const int g = p.plan.group[s];
   float M = kNoScore, l = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  auto fold = [&](const float* o, const float* ml, int RP, int64_t seg, const Shares& sh,
-                  int64_t a, int64_t b, int r) {
-    const int w1 = sh.owner(b - 1);
-    for (int w = sh.owner(a); w <= w1; ++w) {
-      const int64_t slot = seg + w;
-      const float m = __ldg(ml + slot * 2 * RP + r), lw = __ldg(ml + slot * 2 * RP + RP + r);
-      const float4 v = __ldg(reinterpret_cast<const float4*>(o + (slot * RP + r) * kHeadDim) + lane);
-      const float Mn = fmaxf(M, m);
-      const float f0 = ex2(M - Mn), f1 = ex2(m - Mn);
-      l = l * f0 + lw * f1;
-      acc.x = acc.x * f0 + v.x * f1;
-      acc.y = acc.y * f0 + v.y * f1;
-      acc.z = acc.z * f0 + v.z * f1;
-      acc.w = acc.w * f0 + v.w * f1;
-      M = Mn;
-    }
+  auto add = [&](const float* o, const float* ml, int RP, int64_t slot, int r) {
+    const float m = __ldg(ml + slot * 2 * RP + r), lw = __ldg(ml + slot * 2 * RP + RP + r);
+    const float4 v = __ldg(reinterpret_cast<const float4*>(o + (slot * RP + r) * kHeadDim) + lane);
+    const float Mn = fmaxf(M, m);
+    const float f0 = ex2(M - Mn), f1 = ex2(m - Mn);
+    l = l * f0 + lw * f1;
+    acc.x = acc.x * f0 + v.x * f1;
+    acc.y = acc.y * f0 + v.y * f1;
+    acc.z = acc.z * f0 + v.z * f1;
+    acc.w = acc.w * f0 + v.w * f1;
+    M = Mn;
   };
   const int np = p.plan.gpages[g];
   if (np > 0) {
+    const int nrows = (p.plan.goff[g + 1] - p.plan.goff[g]) * p.rows;
     const int R = (s - p.plan.goff[g]) * p.rows + i * p.group + gq;
-    const int nt = p.plan.gtiles[g + 1] - p.plan.gtiles[g];
-    const int seg = h * nt + R / p.tile_rows;
-    const int64_t a = (int64_t)p.plan.gpre[g] * H + (int64_t)seg * np;
-    fold(p.pre_o, p.pre_ml, p.pre_rp, (int64_t)p.plan.gtiles[g] * H + seg,
-         Shares((int64_t)p.plan.gpre[p.num_groups] * H, p.pre_workers), a, a + np,
-         R % p.tile_rows);
+    const int rt = R / kUmmaRows, r = R % kUmmaRows, T = (np + kUmmaPages - 1) / kUmmaPages;
+    const bool dual = nrows - rt * kUmmaRows > 128;
+    const int w = dual ? 2 : 1, nt = p.plan.gtiles[g + 1] - p.plan.gtiles[g];
+    const int64_t a = (int64_t)p.plan.gcost[g] * H +
+                      (int64_t)h * (p.plan.gcost[g + 1] - p.plan.gcost[g]) + (int64_t)rt * 2 * T;
+    const int64_t seg = (int64_t)p.plan.gtiles[g] * H + h * nt + rt;
+    const Shares sh((int64_t)p.plan.gcost[p.num_groups] * H, p.pre_workers);
+    const int c1 = sh.owner(a + (int64_t)w * (T - 1));
+    for (int c = sh.owner(a); c <= c1; ++c) {
+      add(p.pre_o, p.pre_ml, p.pre_rp, seg + c, r);
+      if (!dual) add(p.pre_o, p.pre_ml, p.pre_rp, seg + c, r + p.pre_rp / 2);
+    }
   }
   const int a0 = p.plan.spre[s], n = p.plan.spre[s + 1] - a0;
   const int64_t a = (int64_t)a0 * H + (int64_t)h * n;
-  fold(p.suf_o, p.suf_ml, p.suf_rp, (int64_t)s * H + h,
-       Shares((int64_t)p.plan.spre[p.num_seqs] * H, p.suf_workers), a, a + n, i * p.group + gq);
+  const Shares sh((int64_t)p.plan.spre[p.num_seqs] * H, p.suf_workers);
+  const int w1 = sh.owner(a + n - 1);
+  for (int w = sh.owner(a); w <= w1; ++w)
+    add(p.suf_o, p.suf_ml, p.suf_rp, (int64_t)s * H + h + w, i * p.group + gq);
   float inv = l > 0.f ? 1.f / l : 0.f;
   if (scaled) inv *= __ldg(p.v_scale + (p.scale_per_head ? h : 0));
   __half2 h01 = __floats2half2_rn(acc.x * inv, acc.y * inv);
@@ -212,18 +217,18 @@ size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
 
 // Sizes of a call, and where its arrays lie in the workspace.
 struct SharedLayout {
-  int tile_rows, pre_rp, suf_rp, pre_workers, suf_workers;
+  int pre_rp, suf_rp, pre_workers, suf_workers;
   size_t pre_o, pre_ml, suf_o, suf_ml, total;   // offsets
 
   SharedLayout(int B, int M, int q_len, int hq, int hkv, int sms = kMaxSms) {
     const int rows = hq / hkv * q_len;
-    tile_rows = pre_rp = (int)std::min<int64_t>(32, ((int64_t)B * rows + 7) / 8 * 8);
+    // a slot holds a row tile, or twice a tile of at most 128 rows
+    pre_rp = (int)std::min<int64_t>(kUmmaRows, 2 * (((int64_t)B * rows + 7) / 8 * 8));
     suf_rp = rows_padded(rows);
     sms = std::min(sms, kMaxSms);
-    pre_workers = sms * shared_blocks_per_sm(pre_rp / 8) * 8;
-    suf_workers = sms * shared_blocks_per_sm(suf_rp / 8) * 8;
-    const int64_t pre_slots =
-        (((int64_t)B * rows + tile_rows - 1) / tile_rows + M) * hkv + pre_workers;
+    pre_workers = sms;
+    suf_workers = sms * private_blocks_per_sm(suf_rp / 8) * 8;
+    const int64_t pre_slots = (int64_t)(umma_tiles(B * rows) + M) * hkv + pre_workers;
     const int64_t suf_slots = (int64_t)B * hkv + suf_workers;
     size_t at = up256((size_t)(4 * (B + 1) + 4 * (M + 1)) * 4);
     auto take = [&](size_t bytes) {
@@ -247,7 +252,8 @@ size_t shared_prefix_workspace(int32_t num_seqs, int32_t num_groups, int32_t q_l
 }
 
 cudaError_t launch_shared_prefix(const AttnArgs& a, const SharedArgs& sa, void* out,
-                                 const CUtensorMap& map, void* workspace, int sms,
+                                 const CUtensorMap& prefix_map, const CUtensorMap& map,
+                                 void* workspace, int sms,
                                  int32_t* status, cudaStream_t stream) {
   const int B = a.num_seqs, M = sa.num_groups;
   const SharedLayout lay(B, M, a.q_len, a.num_q_heads, a.num_kv_heads, sms);
@@ -275,7 +281,7 @@ cudaError_t launch_shared_prefix(const AttnArgs& a, const SharedArgs& sa, void* 
   p.plan.goff = take(M + 1);
   p.plan.gpages = take(M);
   p.plan.gtiles = take(M + 1);
-  p.plan.gpre = take(M + 1);
+  p.plan.gcost = take(M + 1);
   p.pre_o = reinterpret_cast<float*>(ws + lay.pre_o);
   p.pre_ml = reinterpret_cast<float*>(ws + lay.pre_ml);
   p.suf_o = reinterpret_cast<float*>(ws + lay.suf_o);
@@ -290,7 +296,6 @@ cudaError_t launch_shared_prefix(const AttnArgs& a, const SharedArgs& sa, void* 
   p.group = a.num_q_heads / a.num_kv_heads;
   p.rows = p.group * a.q_len;
   p.scale_per_head = a.scale_per_head ? 1 : 0;
-  p.tile_rows = lay.tile_rows;
   p.pre_rp = lay.pre_rp;
   p.suf_rp = lay.suf_rp;
   p.pre_workers = lay.pre_workers;
@@ -300,10 +305,10 @@ cudaError_t launch_shared_prefix(const AttnArgs& a, const SharedArgs& sa, void* 
   cudaError_t e = launch_pdl(shared_plan_kernel, 1, kPlanThreads, 0, stream, p);
   if (e != cudaSuccess) return e;
   switch (a.kv_dtype) {
-    case PQKV_KV_FP16: e = launch_shared_fp16(p, map, stream); break;
-    case PQKV_KV_FP8_E4M3: e = launch_shared_e4m3(p, map, stream); break;
-    case PQKV_KV_INT8_ROW: e = launch_shared_int8_row(p, map, stream); break;
-    default: e = launch_shared_int8(p, map, stream); break;
+    case PQKV_KV_FP16: e = launch_shared_fp16(p, prefix_map, map, stream); break;
+    case PQKV_KV_FP8_E4M3: e = launch_shared_e4m3(p, prefix_map, map, stream); break;
+    case PQKV_KV_INT8_ROW: e = launch_shared_int8_row(p, prefix_map, map, stream); break;
+    default: e = launch_shared_int8(p, prefix_map, map, stream); break;
   }
   if (e != cudaSuccess) return e;
   const int64_t rows = (int64_t)B * a.q_len * a.num_q_heads;
