@@ -104,8 +104,8 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedP
       if (want < 0 || want > s_min[g] + p.q_len) report(p.status, PQKV_DEV_SEQ_RANGE);
       pages = max(0, min(want, s_min[g])) / kPageSize;
     }
-    p.plan.gpages[g] = pages;
-    p.plan.goff[g] = s_off[g];
+    p.plan.gpages(M)[g] = pages;
+    p.plan.goff()[g] = s_off[g];
     tiles[i] = pages > 0 ? umma_tiles(n * p.rows) : 0;
     costs[i] = umma_weight(n * p.rows) * ((pages + kUmmaPages - 1) / kUmmaPages);
     tsum += tiles[i];
@@ -118,15 +118,15 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedP
   for (int i = 0; i < kPlanEach; ++i) {
     const int g = tid * gper + i;
     if (i >= gper || g >= M) continue;
-    p.plan.gtiles[g] = at_t;
-    p.plan.gcost[g] = at_p;
+    p.plan.gtiles(M)[g] = at_t;
+    p.plan.gcost(M)[g] = at_p;
     at_t += tiles[i];
     at_p += costs[i];
   }
   if (tid == 0) {
-    p.plan.gtiles[M] = total_t;
-    p.plan.gcost[M] = total_p;
-    p.plan.goff[M] = B;
+    p.plan.gtiles(M)[M] = total_t;
+    p.plan.gcost(M)[M] = total_p;
+    p.plan.goff()[M] = B;
   }
   __syncthreads();
   // -- the private pages
@@ -158,37 +158,37 @@ __global__ void __launch_bounds__(256) shared_merge_kernel(const SharedParams p,
   grid_dependents_launch();
   const int lane = threadIdx.x & 31;
   const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int H = p.num_kv_heads;
+  const int H = p.num_kv_heads, M = p.num_groups;
   if (row >= (int64_t)p.num_seqs * p.q_len * p.num_q_heads) return;
   const int hq = (int)(row % p.num_q_heads);
   const int tok = (int)(row / p.num_q_heads);
   const int s = tok / p.q_len, i = tok % p.q_len, h = hq / p.group, gq = hq % p.group;
   const int g = p.plan.group[s];
-  float M = kNoScore, l = 0.f;
+  float top = kNoScore, l = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   auto add = [&](const float* o, const float* ml, int RP, int64_t slot, int r) {
     const float m = __ldg(ml + slot * 2 * RP + r), lw = __ldg(ml + slot * 2 * RP + RP + r);
     const float4 v = __ldg(reinterpret_cast<const float4*>(o + (slot * RP + r) * kHeadDim) + lane);
-    const float Mn = fmaxf(M, m);
-    const float f0 = ex2(M - Mn), f1 = ex2(m - Mn);
+    const float Mn = fmaxf(top, m);
+    const float f0 = ex2(top - Mn), f1 = ex2(m - Mn);
     l = l * f0 + lw * f1;
     acc.x = acc.x * f0 + v.x * f1;
     acc.y = acc.y * f0 + v.y * f1;
     acc.z = acc.z * f0 + v.z * f1;
     acc.w = acc.w * f0 + v.w * f1;
-    M = Mn;
+    top = Mn;
   };
-  const int np = p.plan.gpages[g];
+  const int np = p.plan.gpages(M)[g];
   if (np > 0) {
-    const int nrows = (p.plan.goff[g + 1] - p.plan.goff[g]) * p.rows;
-    const int R = (s - p.plan.goff[g]) * p.rows + i * p.group + gq;
+    const int nrows = (p.plan.goff()[g + 1] - p.plan.goff()[g]) * p.rows;
+    const int R = (s - p.plan.goff()[g]) * p.rows + i * p.group + gq;
     const int rt = R / kUmmaRows, r = R % kUmmaRows, T = (np + kUmmaPages - 1) / kUmmaPages;
     const bool dual = nrows - rt * kUmmaRows > 128;
-    const int w = dual ? 2 : 1, nt = p.plan.gtiles[g + 1] - p.plan.gtiles[g];
-    const int64_t a = (int64_t)p.plan.gcost[g] * H +
-                      (int64_t)h * (p.plan.gcost[g + 1] - p.plan.gcost[g]) + (int64_t)rt * 2 * T;
-    const int64_t seg = (int64_t)p.plan.gtiles[g] * H + h * nt + rt;
-    const Shares sh((int64_t)p.plan.gcost[p.num_groups] * H, p.pre_workers);
+    const int w = dual ? 2 : 1, nt = p.plan.gtiles(M)[g + 1] - p.plan.gtiles(M)[g];
+    const int64_t a = (int64_t)p.plan.gcost(M)[g] * H +
+                      (int64_t)h * (p.plan.gcost(M)[g + 1] - p.plan.gcost(M)[g]) + (int64_t)rt * 2 * T;
+    const int64_t seg = (int64_t)p.plan.gtiles(M)[g] * H + h * nt + rt;
+    const Shares sh((int64_t)p.plan.gcost(M)[M] * H, p.pre_workers);
     const int c1 = sh.owner(a + (int64_t)w * (T - 1));
     for (int c = sh.owner(a); c <= c1; ++c) {
       add(p.pre_o, p.pre_ml, p.pre_rp, seg + c, r);
@@ -278,10 +278,7 @@ cudaError_t launch_shared_prefix(const AttnArgs& a, const SharedArgs& sa, void* 
   p.plan.group = take(B);
   p.plan.page0 = take(B);
   p.plan.spre = take(B + 1);
-  p.plan.goff = take(M + 1);
-  p.plan.gpages = take(M);
-  p.plan.gtiles = take(M + 1);
-  p.plan.gcost = take(M + 1);
+  p.plan.groups = take(4 * (M + 1));
   p.pre_o = reinterpret_cast<float*>(ws + lay.pre_o);
   p.pre_ml = reinterpret_cast<float*>(ws + lay.pre_ml);
   p.suf_o = reinterpret_cast<float*>(ws + lay.suf_o);

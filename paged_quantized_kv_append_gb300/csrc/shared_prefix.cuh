@@ -25,10 +25,13 @@ struct SharedPlan {
   int32_t* group;     // [N]     its group
   int32_t* page0;     // [N]     its first private page = its group's shared pages
   int32_t* spre;      // [N + 1] private pages of the sequences before it
-  int32_t* goff;      // [M + 1] first sequence of the group
-  int32_t* gpages;    // [M]     shared pages of the group
-  int32_t* gtiles;    // [M + 1] row tiles of a kv-head in the groups before it
-  int32_t* gcost;     // [M + 1] cost of a kv-head's tiles in the groups before it
+  // four rows of M + 1: the group's first sequence, its shared pages, the row
+  // tiles of a kv-head in the groups before it, and those tiles' cost
+  int32_t* groups;
+  __host__ __device__ int32_t* goff() const { return groups; }
+  __host__ __device__ int32_t* gpages(int M) const { return groups + (M + 1); }
+  __host__ __device__ int32_t* gtiles(int M) const { return groups + 2 * (M + 1); }
+  __host__ __device__ int32_t* gcost(int M) const { return groups + 3 * (M + 1); }
 };
 
 struct SharedParams {

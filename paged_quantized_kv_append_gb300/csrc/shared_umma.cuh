@@ -13,7 +13,7 @@
 //
 // Warps: 0-3 and 4-7 the softmax of stream 0 and 1 (a thread per row), 8-11
 // widen the 8-bit codes to fp16 (exact; TMA writes the fp16 pool's rows into
-// place itself), 12 issues the copies, 13 the products.
+// place itself), 12 issues the copies, 13 and 14 the products of a stream each.
 //
 // The running maximum of a row is only raised when a score passes it by more
 // than 8 (probabilities stay <= 2^8 in fp16), so O is rescaled rarely, by the
@@ -72,6 +72,17 @@ __device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, ui
       "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
       "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
       : "memory");
+}
+
+// True in one thread of a converged warp.  The products are issued under it from
+// warp-uniform control flow: their operands then stay in uniform registers
+// (issued by a lane of a divergent branch, an instruction cost about 100 cycles,
+// more than the 64 that its product takes).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred P;\n\telect.sync _|P, 0xffffffff;\n\tselp.u32 %0, 1, 0, P;\n\t}"
+               : "=r"(p));
+  return p != 0;
 }
 
 #define PQKV_R32(F) \
@@ -176,10 +187,22 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
   return r;
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
 __device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c,
                                        uint32_t d) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c),
                "r"(d)
+               : "memory");
+}
+// 32 bytes, a whole sector per lane
+__device__ __forceinline__ void stg256(float* dst, const uint32_t* v) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(v[0]),
+               "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
                : "memory");
 }
 __device__ __forceinline__ uint4 lds128u(uint32_t addr) {
@@ -217,36 +240,39 @@ struct UmmaFrag {
 // [a, a + w T) of its T key tiles (w = 2 or 1); key tile i belongs to the share
 // that holds cost a + w i.
 struct UmmaIter {
-  const int* gcost;   // [M + 1] cost of a kv-head in the groups before it
-  const int* gpages;  // [M]
-  const int* gtiles;  // [M + 1]
-  const int32_t* goff;
-  int M, H, rows;
+  const int* tab;     // the plan's rows of groups
+  int stride;         // entries per row
   int64_t x, e;
 
-  __device__ bool next(UmmaFrag& f) {
+  __device__ int goff(int g) const { return tab[g]; }
+  __device__ int gpages(int g) const { return tab[stride + g]; }
+  __device__ int gtiles(int g) const { return tab[2 * stride + g]; }
+  __device__ int gcost(int g) const { return tab[3 * stride + g]; }
+
+  // M groups, H kv-heads, `rows` rows of a (sequence, kv-head)
+  __device__ bool next(UmmaFrag& f, int M, int H, int rows) {
     while (x < e) {
       int lo = 0, hi = M - 1;
       while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if ((int64_t)gcost[mid] * H <= x) lo = mid; else hi = mid - 1;
+        if ((int64_t)gcost(mid) * H <= x) lo = mid; else hi = mid - 1;
       }
-      const int g = lo, C = gcost[g + 1] - gcost[g];
-      const int T = (gpages[g] + kUmmaPages - 1) / kUmmaPages;
-      const int64_t off = x - (int64_t)gcost[g] * H;
+      const int g = lo, C = gcost(g + 1) - gcost(g);
+      const int T = (gpages(g) + kUmmaPages - 1) / kUmmaPages;
+      const int64_t off = x - (int64_t)gcost(g) * H;
       f.g = g;
       f.h = (int)Shares::div(off, C);
       const int in = (int)(off - (int64_t)f.h * C);
       f.rt = in / (2 * T);
-      f.nrows = (goff[g + 1] - goff[g]) * rows;
+      f.nrows = (goff(g + 1) - goff(g)) * rows;
       f.row0 = f.rt * kUmmaRows;
       f.dual = f.nrows - f.row0 > 128;
       const int w = f.dual ? 2 : 1;
       const int64_t a = x - (in - f.rt * 2 * T);
       f.u0 = (int)((x - a + w - 1) / w);
       f.u1 = (int)min((int64_t)T, (e - a + w - 1) / w);
-      f.pages = gpages[g];
-      f.seg = gtiles[g] * H + f.h * (gtiles[g + 1] - gtiles[g]) + f.rt;
+      f.pages = gpages(g);
+      f.seg = gtiles(g) * H + f.h * (gtiles(g + 1) - gtiles(g)) + f.rt;
       x = min(e, a + (int64_t)w * T);
       if (f.u0 < f.u1) return true;
     }
@@ -268,6 +294,13 @@ struct UmmaCfg {
   static constexpr bool kWide = KVT == PQKV_KV_FP16;      // rows need no widening
   static constexpr bool kRowScaled = KVT == PQKV_KV_INT8_ROW;
   static constexpr int kThreads = 512;
+  static constexpr long long kWaitCycles = 1ll << 31;     // 1.04 s at 2.07 GHz
+  // A row's reference maximum is raised when a score passes it by more than
+  // this (log2): probabilities stay <= 2^14, within fp16's 2^16, and the fewer
+  // rescales of O the better (8 as in the decode kernel: 300 cycles a step on
+  // scores with outliers).  Row-scaled V: p times a scale of up to 2^8 has to
+  // fit too.
+  static constexpr float kRaise = kRowScaled ? 8.f : 14.f;
   static constexpr int kHalf = 128 * 128;                 // 16 KB: 128 rows of 64 values
   static constexpr int kTile = 2 * kHalf;
   static constexpr int kQOff = 0;                         // 2 streams
@@ -275,14 +308,14 @@ struct UmmaCfg {
   static constexpr int kVOff = kKOff + 2 * kTile;         // 2 stages
   static constexpr int kCodeOff = kVOff + 2 * kTile;      // staged codes: slabs of 128 rows
   static constexpr int kSlab = 128 * 128;
-  static constexpr int kSlabs = kWide ? 0 : (kRowScaled ? 1 : 2);
-  static constexpr int kScOff = kCodeOff + kSlabs * kSlab;  // row scales: 4 stages of K and V
-  static constexpr int kScBytes = kRowScaled ? 4 * 2 * 128 * 4 : 0;
+  static constexpr int kSlabs = kWide ? 0 : 2;
+  static constexpr int kScOff = kCodeOff + kSlabs * kSlab;  // fp16 row scales: 3 stages of K and V
+  static constexpr int kScBytes = kRowScaled ? 3 * 2 * 128 * 2 : 0;
   static constexpr int kBarOff = kScOff + kScBytes;
-  static constexpr int kBars = 4 + 8 + 8 + 1;
+  static constexpr int kBars = 4 + 8 + 10 + 2;
   // the plan of up to kTabGroups groups is copied to shared memory (more are
   // read from L2: a search per fragment)
-  static constexpr int kTabGroups = 48;
+  static constexpr int kTabGroups = kRowScaled ? 15 : 48;
   static constexpr int kTabOff = kBarOff + kBars * 8 + 8;
   static constexpr int kSmemBytes = kTabOff + 4 * (kTabGroups + 1) * 4 + 1024;
   static_assert(kSmemBytes <= 232448, "shared memory of a block");
@@ -312,9 +345,9 @@ __global__ void __launch_bounds__(512, 1)
   uint64_t* v_empty = bars + 10;
   uint64_t* q_ready = bars + 12;       // [stream] the fragment's query rows are in place
   uint64_t* s_full = bars + 14;        // [stream] scores in TMEM
-  uint64_t* p_ready = bars + 16;       // [stream] probabilities in TMEM, O rescaled
-  uint64_t* o_done = bars + 18;        // [stream] the product with V is done
-  uint64_t* drain = bars + 20;         // after a wait that ran out
+  uint64_t* p_ready = bars + 16;       // [stream][half] 64 keys' probabilities in TMEM, O rescaled
+  uint64_t* o_done = bars + 20;        // [stream] the product with V is done
+  uint64_t* drain = bars + 22;         // [stream] after a wait that ran out
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Cfg::kBarOff + Cfg::kBars * 8);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Cfg::kBarOff + Cfg::kBars * 8 + 4);
   const int M = p.num_groups, H = p.num_kv_heads;
@@ -325,15 +358,16 @@ __global__ void __launch_bounds__(512, 1)
       mbar_init(&code_full[i], 1);
       mbar_init(&code_empty[i], 4);
       mbar_init(&k_full[i], Cfg::kWide ? 1 : 4);
-      mbar_init(&k_empty[i], 1);
+      mbar_init(&k_empty[i], 2);
       mbar_init(&v_full[i], Cfg::kWide ? 1 : 4);
-      mbar_init(&v_empty[i], 1);
+      mbar_init(&v_empty[i], 2);
       mbar_init(&q_ready[i], 4);
       mbar_init(&s_full[i], 1);
       mbar_init(&p_ready[i], 4);
+      mbar_init(&p_ready[2 + i], 4);
       mbar_init(&o_done[i], 1);
+      mbar_init(&drain[i], 1);
     }
-    mbar_init(drain, 1);
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -342,33 +376,19 @@ __global__ void __launch_bounds__(512, 1)
   grid_dependency_wait();
   grid_dependents_launch();
   UmmaIter it;
-  it.gcost = p.plan.gcost;
-  it.gpages = p.plan.gpages;
-  it.gtiles = p.plan.gtiles;
-  it.goff = p.plan.goff;
+  it.tab = p.plan.groups;
+  it.stride = M + 1;
   if (M <= Cfg::kTabGroups) {
     int* tab = reinterpret_cast<int*>(smem + Cfg::kTabOff);
-    const int n = Cfg::kTabGroups + 1;
-    if (tid <= M) {
-      tab[tid] = it.gcost[tid];
-      tab[n + tid] = tid < M ? it.gpages[tid] : 0;
-      tab[2 * n + tid] = it.gtiles[tid];
-      tab[3 * n + tid] = it.goff[tid];
-    }
-    it.gcost = tab;
-    it.gpages = tab + n;
-    it.gtiles = tab + 2 * n;
-    it.goff = tab + 3 * n;
+    for (int i = tid; i < 4 * (M + 1); i += Cfg::kThreads) tab[i] = p.plan.groups[i];
+    it.tab = tab;
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  const Shares sh((int64_t)it.gcost[M] * H, p.pre_workers);
-  it.M = M;
-  it.H = H;
-  it.rows = p.rows;
+  const Shares sh((int64_t)it.gcost(M) * H, p.pre_workers);
   it.x = it.e = 0;
   if ((int)blockIdx.x < sh.n) {
     it.x = sh.start(blockIdx.x);
@@ -376,17 +396,20 @@ __global__ void __launch_bounds__(512, 1)
   }
   UmmaFrag f;
 
-  // Bounded wait (1 s).  When one runs out the whole CTA stops at its next waits.
+  // Bounded wait (about 1 s).  When one runs out the whole CTA stops at its next waits.
+  // Called by whole warps; every lane gets the same answer.
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-    if (mbar_try_wait(bar, parity)) return true;
-    const uint64_t t0 = globaltimer_ns();
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    const long long t0 = clock64();
     for (uint32_t n = 1;; ++n) {
-      if (mbar_try_wait(bar, parity)) return true;
+      if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
       if ((n & 63u) == 0) {
-        if (*abort_flag) return false;
-        if (globaltimer_ns() - t0 > kWaitLimitNs) {
-          *abort_flag = 1;
-          report(p.status, PQKV_DEV_TIMEOUT);
+        const bool late = clock64() - t0 > Cfg::kWaitCycles;
+        if (__any_sync(0xffffffffu, late || *abort_flag)) {
+          if (lane == 0) {
+            if (!*abort_flag) report(p.status, PQKV_DEV_TIMEOUT);
+            *abort_flag = 1;
+          }
           return false;
         }
       }
@@ -401,31 +424,32 @@ __global__ void __launch_bounds__(512, 1)
     const uint32_t tS = tmem + lane_sel + st * 128, tO = tmem + lane_sel + 256 + st * 128;
     uint32_t n_step = 0;             // steps of this stream so far (s_full, p_ready, o_done)
     uint32_t n_tile = 0;             // key tiles of the CTA so far (row scales' stages)
-    bool ok = true;
-    while (ok && it.next(f)) {
-      // ---- the row into shared memory
+    // the fragment's row of this thread, or -1; its query row into shared memory
+    auto load_row = [&]() -> int {
       const int row = f.row0 + (f.dual ? st * 128 : 0) + r;
+      const int steps = f.dual ? f.u1 - f.u0 : (f.u1 - f.u0 + 1 - st) / 2;
       const bool live = row < f.nrows;
-      const int nt = f.u1 - f.u0, steps = f.dual ? nt : (nt + 1 - st) / 2;
       if (steps > 0) {
-        const int64_t tok = (int64_t)it.goff[f.g] * p.q_len + row / p.group;
+        const int64_t tok = (int64_t)it.goff(f.g) * p.q_len + row / p.group;
         const uint4* src = reinterpret_cast<const uint4*>(
             p.q + (tok * p.num_q_heads + f.h * p.group + row % p.group) * kHeadDim);
         const uint32_t dst = sbase + Cfg::kQOff + st * Cfg::kTile + r * 128;
+        uint4 v[16];
 #pragma unroll
-        for (int c0 = 0; c0 < 16; c0 += 8) {
-          uint4 v[8];
+        for (int c = 0; c < 16; ++c) v[c] = live ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
 #pragma unroll
-          for (int c = 0; c < 8; ++c) v[c] = live ? __ldg(src + c0 + c) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-          for (int c = 0; c < 8; ++c)
-            sts128(dst + (c0 >> 3) * Cfg::kHalf + ((c ^ (r & 7)) << 4), v[c].x, v[c].y, v[c].z,
-                   v[c].w);
-        }
+        for (int c = 0; c < 16; ++c)
+          sts128(dst + (c >> 3) * Cfg::kHalf + (((c & 7) ^ (r & 7)) << 4), v[c].x, v[c].y, v[c].z,
+                 v[c].w);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&q_ready[st]);
       }
+      return live ? row : -1;
+    };
+    bool ok = it.next(f, M, H, p.rows);
+    int my_row = ok ? load_row() : -1;
+    while (ok) {
       float scale = p.sm_scale_log2;
       if constexpr (KVT == PQKV_KV_FP8_E4M3 || KVT == PQKV_KV_INT8) {
         const int hs = p.scale_per_head ? f.h : 0;
@@ -434,10 +458,17 @@ __global__ void __launch_bounds__(512, 1)
           report(p.status, PQKV_DEV_BAD_SCALE);
         scale *= ks;
       }
-      const bool warp_live = f.row0 + (f.dual ? st * 128 : 0) + wq * 32 < f.nrows;
+      const int nt = f.u1 - f.u0, steps = f.dual ? nt : (nt + 1 - st) / 2;
+      const int keys = f.pages * kPageSize - f.u0 * kUmmaKeys;     // of the fragment, and behind
+      const bool dual = f.dual;
+      const bool warp_live = __any_sync(0xffffffffu, my_row >= 0);
+      const int64_t slot = (int64_t)f.seg + blockIdx.x;
+      const int at = st * (p.pre_rp / 2) + r;
       float ref = kNoScore, l = 0.f;
       bool first = true;
-      for (int u = f.dual ? 0 : st; ok && u < nt; u += f.dual ? 1 : 2) {
+#pragma unroll 1
+      for (int i = 0; i < steps; ++i) {
+        const int u = dual ? i : 2 * i + st;
         if (!wait(&s_full[st], n_step & 1)) {
           ok = false;
           break;
@@ -450,29 +481,33 @@ __global__ void __launch_bounds__(512, 1)
           tmem_wait_ld();
 #pragma unroll
           for (int c = 0; c < 4; ++c) tmem_landed32(s + 32 * c);
+          const uint32_t sc = sbase + Cfg::kScOff + (n_tile + u) % 3 * 512;
           if constexpr (Cfg::kRowScaled) {
-            const uint32_t sc = sbase + Cfg::kScOff + ((n_tile + u) & 3) * 1024;
 #pragma unroll
-            for (int c = 0; c < 128; c += 4) {
-              const uint4 k4 = lds128u(sc + c * 4);
-              s[c] = __float_as_uint(__uint_as_float(s[c]) * __uint_as_float(k4.x));
-              s[c + 1] = __float_as_uint(__uint_as_float(s[c + 1]) * __uint_as_float(k4.y));
-              s[c + 2] = __float_as_uint(__uint_as_float(s[c + 2]) * __uint_as_float(k4.z));
-              s[c + 3] = __float_as_uint(__uint_as_float(s[c + 3]) * __uint_as_float(k4.w));
+            for (int c = 0; c < 128; c += 8) {
+              const uint4 k8 = lds128u(sc + c * 2);
+              const uint32_t kk[4] = {k8.x, k8.y, k8.z, k8.w};
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const float2 ks = __half22float2(*reinterpret_cast<const __half2*>(&kk[j]));
+                s[c + 2 * j] = __float_as_uint(__uint_as_float(s[c + 2 * j]) * ks.x);
+                s[c + 2 * j + 1] = __float_as_uint(__uint_as_float(s[c + 2 * j + 1]) * ks.y);
+              }
             }
           }
-          const int valid = f.pages * kPageSize - (f.u0 + u) * kUmmaKeys;
+          const int valid = keys - u * kUmmaKeys;
           if (valid < kUmmaKeys) {
 #pragma unroll
             for (int c = 0; c < 128; ++c)
               if (c >= valid) s[c] = 0xff800000u;              // -inf
           }
-          float mx = kNoScore;
+          float mx4[4] = {kNoScore, kNoScore, kNoScore, kNoScore};
 #pragma unroll
           for (int c = 0; c < 128; c += 2)
-            mx = fmaxf(fmaxf(mx, __uint_as_float(s[c])), __uint_as_float(s[c + 1]));
-          const float m2 = mx * scale;
-          const bool raise = m2 > ref + 8.f;
+            mx4[(c >> 1) & 3] = max3(mx4[(c >> 1) & 3], __uint_as_float(s[c]),
+                                     __uint_as_float(s[c + 1]));
+          const float m2 = max3(fmaxf(mx4[0], mx4[1]), mx4[2], mx4[3]) * scale;
+          const bool raise = m2 > ref + Cfg::kRaise;
           if (__any_sync(0xffffffffu, raise)) {
             const float nref = raise ? m2 : ref;
             const float fct = ex2(ref - nref);
@@ -497,51 +532,56 @@ __global__ void __launch_bounds__(512, 1)
           }
           first = false;
           const uint64_t scale2 = f2(scale, scale), ref2 = f2(-ref, -ref);
-          uint64_t sum = f2(0.f, 0.f);
+          uint64_t sum[4] = {0, 0, 0, 0};
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
             uint32_t ph[32];
 #pragma unroll
             for (int c = 0; c < 32; ++c) {
-              const int i = 64 * half + 2 * c;
+              const int k = 64 * half + 2 * c;
               float a, b;
-              unf2(fma2(f2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), scale2, ref2), a, b);
+              unf2(fma2(f2(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), scale2, ref2), a, b);
               a = ex2(a);
               b = ex2(b);
-              sum = add2(sum, f2(a, b));
-              if constexpr (Cfg::kRowScaled) {
-                const uint32_t sc = sbase + Cfg::kScOff + ((n_tile + u) & 3) * 1024 + 512;
-                float va, vb;
-                asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];"
-                             : "=f"(va), "=f"(vb)
-                             : "r"(sc + i * 4));
-                a *= va;
-                b *= vb;
-              }
+              sum[c & 3] = add2(sum[c & 3], f2(a, b));
               ph[c] = pack_half2(a, b);
+              if constexpr (Cfg::kRowScaled) {
+                // p * (V row scale), rounded once: the fp32 product
+                uint32_t w;
+                asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w) : "r"(sc + 256 + k * 2));
+                const float2 vs = __half22float2(*reinterpret_cast<const __half2*>(&w));
+                ph[c] = pack_half2(a * vs.x, b * vs.y);
+              }
             }
             tmem_st32(tS + 32 * half, ph);
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&p_ready[2 * st + half]);
           }
           float a, b;
-          unf2(sum, a, b);
+          unf2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), a, b);
           l += a + b;
-          tmem_wait_st();
+        } else if (lane == 0) {      // no row of this warp: its probabilities feed rows unread
+          mbar_arrive(&p_ready[2 * st]);
+          mbar_arrive(&p_ready[2 * st + 1]);
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&p_ready[st]);
         n_step += 1;
       }
       n_tile += nt;
+      if (!ok) break;
+      // ---- the next fragment's query row (this one's scores are done), so that
+      // its first product runs under what follows
+      const bool live = my_row >= 0;
+      ok = it.next(f, M, H, p.rows);
+      if (ok) my_row = load_row();
       // ---- O, m and l of the fragment
-      const int64_t slot = (int64_t)f.seg + blockIdx.x;
-      float* dst = p.pre_o + (slot * p.pre_rp + st * (p.pre_rp / 2) + r) * kHeadDim;
-      float* ml = p.pre_ml + slot * 2 * p.pre_rp + st * (p.pre_rp / 2) + r;
-      if (ok && steps > 0) {
-        ok = wait(&o_done[st], (n_step - 1) & 1);
+      if (steps > 0) {
+        if (!wait(&o_done[st], (n_step - 1) & 1)) break;
         tc_fence_after();
       }
-      if (ok && warp_live) {
+      if (warp_live) {
+        float* dst = p.pre_o + (slot * p.pre_rp + at) * kHeadDim;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           uint32_t o[32];
@@ -555,14 +595,12 @@ __global__ void __launch_bounds__(512, 1)
           }
           if (live) {
 #pragma unroll
-            for (int k = 0; k < 32; k += 4)
-              *reinterpret_cast<uint4*>(dst + 32 * c + k) =
-                  make_uint4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+            for (int k = 0; k < 32; k += 8) stg256(dst + 32 * c + k, o + k);
           }
         }
         if (live) {
-          ml[0] = ref;
-          ml[p.pre_rp] = l;
+          p.pre_ml[slot * 2 * p.pre_rp + at] = ref;
+          p.pre_ml[slot * 2 * p.pre_rp + p.pre_rp + at] = l;
         }
       }
       tc_fence_before();
@@ -574,31 +612,28 @@ __global__ void __launch_bounds__(512, 1)
       const int wt = tid - 256;
       uint32_t n_slab = 0, n_tile = 0;
       bool ok = true;
-      while (ok && it.next(f)) {
+      // INT8_ROW: K and V row scale (fp16 bits) of this thread's token of key
+      // tile u; 0 behind the prefix and for pages outside the pool
+      auto row_scale = [&](int u) -> ushort2 {
+        const int tok = u * kUmmaKeys + wt, pg = tok / kPageSize, rr = tok % kPageSize;
+        if (pg >= f.pages) return make_ushort2(0, 0);
+        const int id = __ldg(p.block_table + (int64_t)it.goff(f.g) * p.bt_stride + pg);
+        if (id < 0 || (int64_t)id >= p.num_pages) return make_ushort2(0, 0);
+        const uint16_t* src = reinterpret_cast<const uint16_t*>(p.k_scale) +
+                              (((int64_t)id * H + f.h) * 8 + (rr & 7)) * 4 + (rr >> 3);
+        return make_ushort2(__ldg(src), __ldg(src + 2));
+      };
+      ushort2 ahead = make_ushort2(0, 0);
+      while (ok && it.next(f, M, H, p.rows)) {
         for (int u = f.u0; ok && u < f.u1; ++u, ++n_tile) {
           if constexpr (Cfg::kRowScaled) {
-            // the tile's row scales as fp32, a token per thread (rows behind
-            // the prefix, and pages outside the pool: 0)
-            const int tok = u * kUmmaKeys + wt, pg = tok / kPageSize, rr = tok % kPageSize;
-            float ks = 0.f, vs = 0.f;
-            if (pg < f.pages) {
-              const int id = __ldg(p.block_table + (int64_t)it.goff[f.g] * p.bt_stride + pg);
-              if (id >= 0 && (int64_t)id < p.num_pages) {
-                const __half* src = reinterpret_cast<const __half*>(p.k_scale) +
-                                    (((int64_t)id * H + f.h) * 8 + (rr & 7)) * 4 + (rr >> 3);
-                ks = __half2float(src[0]);
-                vs = __half2float(src[2]);
-              }
-            }
-            float* dst = reinterpret_cast<float*>(smem + Cfg::kScOff + (n_tile & 3) * 1024);
-            // stage n_tile & 3 was last read by the softmax of tile n_tile - 4,
-            // which the K stage's release two tiles ago came after
-            if (n_tile >= 2 && !wait(&k_empty[n_tile & 1], ((n_tile >> 1) + 1) & 1)) {
-              ok = false;
-              break;
-            }
-            dst[wt] = ks;
-            dst[128 + wt] = vs;
+            // The tile's fp16 row scales, a token per thread, read a tile ahead.
+            // Stage n % 3 was last read by the softmax of tile n - 3, whose
+            // product with V the V stage's release for tile n - 1 came after.
+            uint16_t* dst = reinterpret_cast<uint16_t*>(smem + Cfg::kScOff + n_tile % 3 * 512);
+            dst[wt] = u == f.u0 ? row_scale(u).x : ahead.x;
+            dst[128 + wt] = u == f.u0 ? row_scale(u).y : ahead.y;
+            if (u + 1 < f.u1) ahead = row_scale(u + 1);
           }
 #pragma unroll 1
           for (int kv = 0; kv < 2; ++kv, ++n_slab) {
@@ -647,8 +682,8 @@ __global__ void __launch_bounds__(512, 1)
     // ================= copies =================
     uint32_t n = 0, n_tile = 0;      // copies (K or V of a key tile) and key tiles so far
     bool ok = true;
-    while (ok && it.next(f)) {
-      const int32_t* row = p.block_table + (int64_t)it.goff[f.g] * p.bt_stride;
+    while (ok && it.next(f, M, H, p.rows)) {
+      const int32_t* row = p.block_table + (int64_t)it.goff(f.g) * p.bt_stride;
       for (int u = f.u0; ok && u < f.u1; ++u, ++n_tile) {
         // lane = page of the tile; pages behind the prefix read as zeros
         // (a page id one past the pool: the copy's bounds fill them)
@@ -663,7 +698,6 @@ __global__ void __launch_bounds__(512, 1)
             const int stage = n_tile & 1;
             uint64_t* full = (kv ? v_full : k_full) + stage;
             ok = n_tile < 2 || wait((kv ? v_empty : k_empty) + stage, ((n_tile >> 1) + 1) & 1);
-            ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             if (lane == 0) mbar_arrive_expect_tx(full, Cfg::kTile);
             __syncwarp();
@@ -677,7 +711,6 @@ __global__ void __launch_bounds__(512, 1)
           } else {
             const int slot = n % Cfg::kSlabs;
             ok = n < Cfg::kSlabs || wait(&code_empty[slot], ((n / Cfg::kSlabs) + 1) & 1);
-            ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             if (lane == 0) mbar_arrive_expect_tx(&code_full[slot], Cfg::kSlab);
             __syncwarp();
@@ -700,55 +733,78 @@ __global__ void __launch_bounds__(512, 1)
           (void)mbar_wait(&code_full[i % Cfg::kSlabs], (i / Cfg::kSlabs) & 1);
       }
     }
-  } else if (warp == 13 && lane == 0) {
-    // ================= products =================
-    uint32_t n_tile = 0, n_q[2] = {0, 0}, n_step[2] = {0, 0};
+  } else if (warp < 15) {
+    // ================= products: a warp per stream =================
+    // The tensor pipe takes few products ahead of the one it works on, so a
+    // wait between two products of a warp leaves it idle; with a warp for each
+    // stream the other stream's products fill the gap.
+    const int st = warp - 13;
+    uint32_t n_tile = 0, n_q = 0, n_step = 0;
     bool ok = true;
-    const uint32_t q0 = sbase + Cfg::kQOff, k0 = sbase + Cfg::kKOff, v0 = sbase + Cfg::kVOff;
-    while (ok && it.next(f)) {
-      const int nt = f.u1 - f.u0, steps = f.dual ? 2 * nt : nt;
-      auto tile_of = [&](int i) { return n_tile + (f.dual ? i >> 1 : i); };
-      // S_t = Q_t K^T of step i
-      auto qk = [&](int i) -> bool {
-        const int t = i & 1;
-        const uint32_t tl = tile_of(i), stage = tl & 1;
-        if (i < 2 && !wait(&q_ready[t], n_q[t]++ & 1)) return false;
+    const uint64_t q_desc = tc_desc(sbase + Cfg::kQOff + st * Cfg::kTile, 16),
+                   k_desc = tc_desc(sbase + Cfg::kKOff, 16),
+                   v_desc = tc_desc(sbase + Cfg::kVOff, Cfg::kHalf);
+    const uint32_t tS = tmem + st * 128, tO = tmem + 256 + st * 128;
+    while (ok && it.next(f, M, H, p.rows)) {
+      const int nt = f.u1 - f.u0;
+      const bool dual = f.dual;
+      const int steps = dual ? nt : (nt + 1 - st) / 2;
+      // S = Q K^T on key tile tl.  A stage is free again when both streams are
+      // done with it, or after its one stream's second arrival.
+      auto qk = [&](uint32_t tl) -> bool {
+        const uint32_t stage = tl & 1;
         if (!wait(&k_full[stage], (tl >> 1) & 1)) return false;
         tc_fence_after();
-        const uint64_t a = tc_desc(q0 + t * Cfg::kTile, 16), b = tc_desc(k0 + stage * Cfg::kTile, 16);
+        if (elect_one()) {
+          const uint64_t b = k_desc + (uint64_t)(stage * (Cfg::kTile >> 4));
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const uint64_t off = (uint64_t)(((k >> 2) * Cfg::kHalf + (k & 3) * 32) >> 4);
-          tc_mma_ss(tmem + t * 128, a + off, b + off, kIdescQK, k > 0);
+          for (int k = 0; k < 8; ++k) {
+            const uint64_t off = (uint64_t)(((k >> 2) * Cfg::kHalf + (k & 3) * 32) >> 4);
+            tc_mma_ss(tS, q_desc + off, b + off, kIdescQK, k > 0);
+          }
+          tc_commit(&s_full[st]);
+          tc_commit(&k_empty[stage]);
+          if (!dual) tc_commit(&k_empty[stage]);
         }
-        tc_commit(&s_full[t]);
-        if (!f.dual || t == 1) tc_commit(&k_empty[stage]);
+        __syncwarp();
         return true;
       };
-      // O_t += P_t V of step i
-      auto pv = [&](int i) -> bool {
-        const int t = i & 1;
-        const uint32_t tl = tile_of(i), stage = tl & 1;
-        if (!wait(&p_ready[t], n_step[t] & 1)) return false;
-        if (!wait(&v_full[stage], (tl >> 1) & 1)) return false;
-        tc_fence_after();
-        const uint64_t b = tc_desc(v0 + stage * Cfg::kTile, Cfg::kHalf);
+      if (steps > 0) {
+        ok = wait(&q_ready[st], n_q & 1) && qk(n_tile + (dual ? 0 : st));
+        n_q += 1;
+      }
+#pragma unroll 1
+      for (int i = 0; ok && i < steps; ++i) {
+        // O += P V, in two halves of 64 keys
+        const uint32_t tl = n_tile + (dual ? i : 2 * i + st), stage = tl & 1;
+        const uint64_t b = v_desc + (uint64_t)(stage * (Cfg::kTile >> 4));
+        ok = wait(&v_full[stage], (tl >> 1) & 1);
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          tc_mma_ts(tmem + 256 + t * 128, tmem + t * 128 + k * 8, b + (uint64_t)(k * 2048 >> 4),
-                    kIdescPV, i >= 2 || k > 0);
-        tc_commit(&o_done[t]);
-        if (!f.dual || t == 1) tc_commit(&v_empty[stage]);
-        n_step[t] += 1;
-        return true;
-      };
-      ok = qk(0) && (steps < 2 || qk(1));
-      for (int i = 0; ok && i < steps; ++i) ok = pv(i) && (i + 2 >= steps || qk(i + 2));
+        for (int half = 0; half < 2; ++half) {
+          if (!ok || !(ok = wait(&p_ready[2 * st + half], n_step & 1))) break;
+          tc_fence_after();
+          if (elect_one()) {
+#pragma unroll
+            for (int k = 4 * half; k < 4 * half + 4; ++k)
+              tc_mma_ts(tO, tS + k * 8, b + (uint64_t)(k * 2048 >> 4), kIdescPV, i > 0 || k > 0);
+            if (half) {
+              tc_commit(&o_done[st]);
+              tc_commit(&v_empty[stage]);
+              if (!dual) tc_commit(&v_empty[stage]);
+            }
+          }
+          __syncwarp();
+        }
+        n_step += 1;
+        // the next scores go over this step's probabilities: products of one
+        // thread run in order
+        if (ok && i + 1 < steps) ok = qk(tl + (dual ? 1 : 2));
+      }
       n_tile += nt;
     }
     if (!ok) {                       // products in flight end before the TMEM is freed
-      tc_commit(drain);
-      (void)mbar_wait(drain, 0);
+      if (elect_one()) tc_commit(&drain[st]);
+      (void)mbar_wait(&drain[st], 0);
     }
   }
   }
