@@ -159,9 +159,10 @@ __device__ __forceinline__ uint64_t tc_desc(uint32_t addr, uint32_t half_stride)
          ((uint64_t)(1024 >> 4) << 32) | (uint64_t(1) << 46) | (uint64_t(2) << 61);
 }
 
-// kind::f16, fp16 A and B, fp32 D, M 128, N 128; B with its rows along K for V
-constexpr uint32_t kIdescQK = (1u << 4) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
-constexpr uint32_t kIdescPV = kIdescQK | (1u << 16);
+// kind::f16, fp16 A and B, fp32 D, M 128, N 64 (keys) and 128 (dims); B with
+// its rows along K for V
+constexpr uint32_t kIdescQK = (1u << 4) | ((64u >> 3) << 17) | ((128u >> 4) << 24);
+constexpr uint32_t kIdescPV = (1u << 4) | (1u << 16) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
 
 __device__ __forceinline__ uint64_t f2(float a, float b) {
   uint64_t r;
@@ -312,7 +313,7 @@ struct UmmaCfg {
   static constexpr int kScOff = kCodeOff + kSlabs * kSlab;  // fp16 row scales: 3 stages of K and V
   static constexpr int kScBytes = kRowScaled ? 3 * 2 * 128 * 2 : 0;
   static constexpr int kBarOff = kScOff + kScBytes;
-  static constexpr int kBars = 4 + 8 + 10 + 2;
+  static constexpr int kBars = 4 + 8 + 14 + 2;
   // the plan of up to kTabGroups groups is copied to shared memory (more are
   // read from L2: a search per fragment)
   static constexpr int kTabGroups = kRowScaled ? 15 : 48;
@@ -321,7 +322,7 @@ struct UmmaCfg {
   static_assert(kSmemBytes <= 232448, "shared memory of a block");
   // registers per thread of the softmax, widening and issuing warps, of the
   // 128 * 512 that the block is launched with
-  static constexpr int kRegSoftmax = 192, kRegWiden = 64, kRegIssue = 64;
+  static constexpr int kRegSoftmax = 152, kRegWiden = 120, kRegIssue = 88;
   static_assert(2 * kRegSoftmax + kRegWiden + kRegIssue <= 4 * 128, "registers of the launch");
 };
 
@@ -344,10 +345,11 @@ __global__ void __launch_bounds__(512, 1)
   uint64_t* v_full = bars + 8;
   uint64_t* v_empty = bars + 10;
   uint64_t* q_ready = bars + 12;       // [stream] the fragment's query rows are in place
-  uint64_t* s_full = bars + 14;        // [stream] scores in TMEM
-  uint64_t* p_ready = bars + 16;       // [stream][half] 64 keys' probabilities in TMEM, O rescaled
-  uint64_t* o_done = bars + 20;        // [stream] the product with V is done
-  uint64_t* drain = bars + 22;         // [stream] after a wait that ran out
+  uint64_t* s_full = bars + 14;        // [stream][half] 64 keys' scores in TMEM
+  uint64_t* p_ready = bars + 18;       // [stream][half] their probabilities, and O rescaled
+  uint64_t* o_done = bars + 22;        // [stream] their product with V is done
+  uint64_t* o_last = bars + 24;        // [stream] the fragment's last product with V is done
+  uint64_t* drain = bars + 26;         // [stream] after a wait that ran out
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Cfg::kBarOff + Cfg::kBars * 8);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Cfg::kBarOff + Cfg::kBars * 8 + 4);
   const int M = p.num_groups, H = p.num_kv_heads;
@@ -363,9 +365,11 @@ __global__ void __launch_bounds__(512, 1)
       mbar_init(&v_empty[i], 2);
       mbar_init(&q_ready[i], 4);
       mbar_init(&s_full[i], 1);
+      mbar_init(&s_full[2 + i], 1);
       mbar_init(&p_ready[i], 4);
       mbar_init(&p_ready[2 + i], 4);
       mbar_init(&o_done[i], 1);
+      mbar_init(&o_last[i], 1);
       mbar_init(&drain[i], 1);
     }
     *abort_flag = 0;
@@ -422,7 +426,8 @@ __global__ void __launch_bounds__(512, 1)
     const int st = warp >> 2, wq = warp & 3, r = wq * 32 + lane;
     const uint32_t lane_sel = (uint32_t)(wq * 32) << 16;
     const uint32_t tS = tmem + lane_sel + st * 128, tO = tmem + lane_sel + 256 + st * 128;
-    uint32_t n_step = 0;             // steps of this stream so far (s_full, p_ready, o_done)
+    uint32_t n_step = 0;             // steps of this stream so far (a key tile: two halves)
+    uint32_t n_frag = 0;             // its fragments with a step
     uint32_t n_tile = 0;             // key tiles of the CTA so far (row scales' stages)
     // the fragment's row of this thread, or -1; its query row into shared memory
     auto load_row = [&]() -> int {
@@ -465,106 +470,107 @@ __global__ void __launch_bounds__(512, 1)
       const int64_t slot = (int64_t)f.seg + blockIdx.x;
       const int at = st * (p.pre_rp / 2) + r;
       float ref = kNoScore, l = 0.f;
-      bool first = true;
 #pragma unroll 1
-      for (int i = 0; i < steps; ++i) {
+      for (int i = 0; ok && i < steps; ++i) {
         const int u = dual ? i : 2 * i + st;
-        if (!wait(&s_full[st], n_step & 1)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        if (warp_live) {
-          uint32_t s[128];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32 * c, s + 32 * c);
-          tmem_wait_ld();
-#pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_landed32(s + 32 * c);
-          const uint32_t sc = sbase + Cfg::kScOff + (n_tile + u) % 3 * 512;
-          if constexpr (Cfg::kRowScaled) {
-#pragma unroll
-            for (int c = 0; c < 128; c += 8) {
-              const uint4 k8 = lds128u(sc + c * 2);
-              const uint32_t kk[4] = {k8.x, k8.y, k8.z, k8.w};
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const float2 ks = __half22float2(*reinterpret_cast<const __half2*>(&kk[j]));
-                s[c + 2 * j] = __float_as_uint(__uint_as_float(s[c + 2 * j]) * ks.x);
-                s[c + 2 * j + 1] = __float_as_uint(__uint_as_float(s[c + 2 * j + 1]) * ks.y);
-              }
-            }
-          }
-          const int valid = keys - u * kUmmaKeys;
-          if (valid < kUmmaKeys) {
-#pragma unroll
-            for (int c = 0; c < 128; ++c)
-              if (c >= valid) s[c] = 0xff800000u;              // -inf
-          }
-          float mx4[4] = {kNoScore, kNoScore, kNoScore, kNoScore};
-#pragma unroll
-          for (int c = 0; c < 128; c += 2)
-            mx4[(c >> 1) & 3] = max3(mx4[(c >> 1) & 3], __uint_as_float(s[c]),
-                                     __uint_as_float(s[c + 1]));
-          const float m2 = max3(fmaxf(mx4[0], mx4[1]), mx4[2], mx4[3]) * scale;
-          const bool raise = m2 > ref + Cfg::kRaise;
-          if (__any_sync(0xffffffffu, raise)) {
-            const float nref = raise ? m2 : ref;
-            const float fct = ex2(ref - nref);
-            ref = nref;
-            l *= fct;
-            if (!first) {
-              if (!wait(&o_done[st], (n_step - 1) & 1)) {
-                ok = false;
-                break;
-              }
-              tc_fence_after();
+        const uint32_t sc = sbase + Cfg::kScOff + (n_tile + u) % 3 * 512;
 #pragma unroll 1
-              for (int c = 0; c < 128; c += 16) {
-                uint32_t o[16];
-                tmem_ld16_wait(tO + c, o);
+        for (int half = 0; half < 2; ++half) {
+          if (!wait(&s_full[2 * st + half], n_step & 1)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          if (warp_live) {
+            const uint32_t tH = tS + 64 * half;
+            uint32_t s[64];
+            tmem_ld32(tH, s);
+            tmem_ld32(tH + 32, s + 32);
+            tmem_wait_ld();
+            tmem_landed32(s);
+            tmem_landed32(s + 32);
+            const uint32_t sch = sc + 128 * half;          // 64 fp16 scales of K, of V 256 bytes on
+            if constexpr (Cfg::kRowScaled) {
 #pragma unroll
-                for (int k = 0; k < 16; ++k)
-                  o[k] = __float_as_uint(__uint_as_float(o[k]) * fct);
-                tmem_st16(tO + c, o);
+              for (int c = 0; c < 64; c += 8) {
+                const uint4 k8 = lds128u(sch + c * 2);
+                const uint32_t kk[4] = {k8.x, k8.y, k8.z, k8.w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  const float2 ks = __half22float2(*reinterpret_cast<const __half2*>(&kk[j]));
+                  s[c + 2 * j] = __float_as_uint(__uint_as_float(s[c + 2 * j]) * ks.x);
+                  s[c + 2 * j + 1] = __float_as_uint(__uint_as_float(s[c + 2 * j + 1]) * ks.y);
+                }
               }
             }
-          }
-          first = false;
-          const uint64_t scale2 = f2(scale, scale), ref2 = f2(-ref, -ref);
-          uint64_t sum[4] = {0, 0, 0, 0};
+            const int valid = keys - u * kUmmaKeys - 64 * half;
+            if (valid < 64) {
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
+              for (int c = 0; c < 64; ++c)
+                if (c >= valid) s[c] = 0xff800000u;            // -inf
+            }
+            float mx4[4] = {kNoScore, kNoScore, kNoScore, kNoScore};
+#pragma unroll
+            for (int c = 0; c < 64; c += 2)
+              mx4[(c >> 1) & 3] = max3(mx4[(c >> 1) & 3], __uint_as_float(s[c]),
+                                       __uint_as_float(s[c + 1]));
+            const float m2 = max3(fmaxf(mx4[0], mx4[1]), mx4[2], mx4[3]) * scale;
+            const bool raise = m2 > ref + Cfg::kRaise;
+            if (__any_sync(0xffffffffu, raise)) {
+              const float nref = raise ? m2 : ref;
+              const float fct = ex2(ref - nref);
+              ref = nref;
+              l *= fct;
+              if (i + half > 0) {                              // O holds something
+                // the half before this one (the one before that is done: this
+                // half's scores were issued behind its product)
+                if (!wait(&o_done[st], (half + 1) & 1)) {
+                  ok = false;
+                  break;
+                }
+                tc_fence_after();
+#pragma unroll 1
+                for (int c = 0; c < 128; c += 16) {
+                  uint32_t o[16];
+                  tmem_ld16_wait(tO + c, o);
+#pragma unroll
+                  for (int k = 0; k < 16; ++k)
+                    o[k] = __float_as_uint(__uint_as_float(o[k]) * fct);
+                  tmem_st16(tO + c, o);
+                }
+              }
+            }
+            const uint64_t scale2 = f2(scale, scale), ref2 = f2(-ref, -ref);
+            uint64_t sum[4] = {0, 0, 0, 0};
             uint32_t ph[32];
 #pragma unroll
             for (int c = 0; c < 32; ++c) {
-              const int k = 64 * half + 2 * c;
               float a, b;
-              unf2(fma2(f2(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), scale2, ref2), a, b);
+              unf2(fma2(f2(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1])), scale2, ref2),
+                   a, b);
               a = ex2(a);
               b = ex2(b);
               sum[c & 3] = add2(sum[c & 3], f2(a, b));
-              ph[c] = pack_half2(a, b);
               if constexpr (Cfg::kRowScaled) {
                 // p * (V row scale), rounded once: the fp32 product
                 uint32_t w;
-                asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w) : "r"(sc + 256 + k * 2));
+                asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w) : "r"(sch + 256 + c * 4));
                 const float2 vs = __half22float2(*reinterpret_cast<const __half2*>(&w));
-                ph[c] = pack_half2(a * vs.x, b * vs.y);
+                a *= vs.x;
+                b *= vs.y;
               }
+              ph[c] = pack_half2(a, b);
             }
-            tmem_st32(tS + 32 * half, ph);
+            tmem_st32(tH, ph);
+            float a, b;
+            unf2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), a, b);
+            l += a + b;
             tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&p_ready[2 * st + half]);
           }
-          float a, b;
-          unf2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), a, b);
-          l += a + b;
-        } else if (lane == 0) {      // no row of this warp: its probabilities feed rows unread
-          mbar_arrive(&p_ready[2 * st]);
-          mbar_arrive(&p_ready[2 * st + 1]);
+          // (a warp without a row: its probabilities feed rows that nobody reads)
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_ready[2 * st + half]);
         }
         n_step += 1;
       }
@@ -577,7 +583,8 @@ __global__ void __launch_bounds__(512, 1)
       if (ok) my_row = load_row();
       // ---- O, m and l of the fragment
       if (steps > 0) {
-        if (!wait(&o_done[st], (n_step - 1) & 1)) break;
+        if (!wait(&o_last[st], n_frag & 1)) break;
+        n_frag += 1;
         tc_fence_after();
       }
       if (warp_live) {
@@ -749,56 +756,65 @@ __global__ void __launch_bounds__(512, 1)
       const int nt = f.u1 - f.u0;
       const bool dual = f.dual;
       const int steps = dual ? nt : (nt + 1 - st) / 2;
-      // S = Q K^T on key tile tl.  A stage is free again when both streams are
-      // done with it, or after its one stream's second arrival.
-      auto qk = [&](uint32_t tl) -> bool {
+      // S = Q K^T on half a key tile.  A stage is free again when both streams
+      // are done with it, or after its one stream's second arrival.
+      auto qk = [&](uint32_t tl, int half) -> bool {
         const uint32_t stage = tl & 1;
-        if (!wait(&k_full[stage], (tl >> 1) & 1)) return false;
+        if (!half && !wait(&k_full[stage], (tl >> 1) & 1)) return false;
         tc_fence_after();
         if (elect_one()) {
-          const uint64_t b = k_desc + (uint64_t)(stage * (Cfg::kTile >> 4));
+          const uint64_t b = k_desc + (uint64_t)((stage * Cfg::kTile + half * 8192) >> 4);
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
             const uint64_t off = (uint64_t)(((k >> 2) * Cfg::kHalf + (k & 3) * 32) >> 4);
-            tc_mma_ss(tS, q_desc + off, b + off, kIdescQK, k > 0);
+            tc_mma_ss(tS + 64 * half, q_desc + off, b + off, kIdescQK, k > 0);
           }
-          tc_commit(&s_full[st]);
-          tc_commit(&k_empty[stage]);
-          if (!dual) tc_commit(&k_empty[stage]);
+          tc_commit(&s_full[2 * st + half]);
+          if (half) {
+            tc_commit(&k_empty[stage]);
+            if (!dual) tc_commit(&k_empty[stage]);
+          }
         }
         __syncwarp();
         return true;
       };
+      // O += P V on half a key tile
+      auto pv = [&](uint32_t tl, int half, bool acc, bool last) -> bool {
+        const uint32_t stage = tl & 1;
+        if (!half && !wait(&v_full[stage], (tl >> 1) & 1)) return false;
+        if (!wait(&p_ready[2 * st + half], n_step & 1)) return false;
+        tc_fence_after();
+        if (elect_one()) {
+          const uint64_t b = v_desc + (uint64_t)((stage * Cfg::kTile + half * 8192) >> 4);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            tc_mma_ts(tO, tS + 64 * half + k * 8, b + (uint64_t)(k * 2048 >> 4), kIdescPV,
+                      acc || k > 0);
+          tc_commit(&o_done[st]);
+          if (half) {
+            tc_commit(&v_empty[stage]);
+            if (!dual) tc_commit(&v_empty[stage]);
+            if (last) tc_commit(&o_last[st]);
+          }
+        }
+        __syncwarp();
+        return true;
+      };
+      // Half h's next scores go over its probabilities, right behind the product
+      // that reads them (products of one thread run in order), so that they are
+      // there when the softmax is done with the other half.
       if (steps > 0) {
-        ok = wait(&q_ready[st], n_q & 1) && qk(n_tile + (dual ? 0 : st));
+        const uint32_t tl = n_tile + (dual ? 0 : st);
+        ok = wait(&q_ready[st], n_q & 1) && qk(tl, 0) && qk(tl, 1);
         n_q += 1;
       }
 #pragma unroll 1
       for (int i = 0; ok && i < steps; ++i) {
-        // O += P V, in two halves of 64 keys
-        const uint32_t tl = n_tile + (dual ? i : 2 * i + st), stage = tl & 1;
-        const uint64_t b = v_desc + (uint64_t)(stage * (Cfg::kTile >> 4));
-        ok = wait(&v_full[stage], (tl >> 1) & 1);
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          if (!ok || !(ok = wait(&p_ready[2 * st + half], n_step & 1))) break;
-          tc_fence_after();
-          if (elect_one()) {
-#pragma unroll
-            for (int k = 4 * half; k < 4 * half + 4; ++k)
-              tc_mma_ts(tO, tS + k * 8, b + (uint64_t)(k * 2048 >> 4), kIdescPV, i > 0 || k > 0);
-            if (half) {
-              tc_commit(&o_done[st]);
-              tc_commit(&v_empty[stage]);
-              if (!dual) tc_commit(&v_empty[stage]);
-            }
-          }
-          __syncwarp();
-        }
+        const uint32_t tl = n_tile + (dual ? i : 2 * i + st), next = tl + (dual ? 1 : 2);
+        const bool more = i + 1 < steps;
+        ok = pv(tl, 0, i > 0, false) && (!more || qk(next, 0)) && pv(tl, 1, true, !more) &&
+             (!more || qk(next, 1));
         n_step += 1;
-        // the next scores go over this step's probabilities: products of one
-        // thread run in order
-        if (ok && i + 1 < steps) ok = qk(tl + (dual ? 1 : 2));
       }
       n_tile += nt;
     }
