@@ -166,8 +166,7 @@ __global__ void __launch_bounds__(256) shared_merge_kernel(const SharedParams p,
   const int g = p.plan.group[s];
   float top = kNoScore, l = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  auto add = [&](const float* o, const float* ml, int RP, int64_t slot, int r) {
-    const float m = __ldg(ml + slot * 2 * RP + r), lw = __ldg(ml + slot * 2 * RP + RP + r);
+  auto add = [&](const float* o, float m, float lw, int RP, int64_t slot, int r) {
     const float4 v = __ldg(reinterpret_cast<const float4*>(o + (slot * RP + r) * kHeadDim) + lane);
     const float Mn = fmaxf(top, m);
     const float f0 = ex2(top - Mn), f1 = ex2(m - Mn);
@@ -177,6 +176,14 @@ __global__ void __launch_bounds__(256) shared_merge_kernel(const SharedParams p,
     acc.z = acc.z * f0 + v.z * f1;
     acc.w = acc.w * f0 + v.w * f1;
     top = Mn;
+  };
+  auto add_prefix = [&](int64_t slot, int r) {
+    const float* ml = p.pre_ml + slot * 3 * p.pre_rp + r;
+    add(p.pre_o, __ldg(ml), __ldg(ml + p.pre_rp) + __ldg(ml + 2 * p.pre_rp), p.pre_rp, slot, r);
+  };
+  auto add_private = [&](int64_t slot, int r) {
+    const float* ml = p.suf_ml + slot * 2 * p.suf_rp + r;
+    add(p.suf_o, __ldg(ml), __ldg(ml + p.suf_rp), p.suf_rp, slot, r);
   };
   const int np = p.plan.gpages(M)[g];
   if (np > 0) {
@@ -191,8 +198,8 @@ __global__ void __launch_bounds__(256) shared_merge_kernel(const SharedParams p,
     const Shares sh((int64_t)p.plan.gcost(M)[M] * H, p.pre_workers);
     const int c1 = sh.owner(a + (int64_t)w * (T - 1));
     for (int c = sh.owner(a); c <= c1; ++c) {
-      add(p.pre_o, p.pre_ml, p.pre_rp, seg + c, r);
-      if (!dual) add(p.pre_o, p.pre_ml, p.pre_rp, seg + c, r + p.pre_rp / 2);
+      add_prefix(seg + c, r);
+      if (!dual) add_prefix(seg + c, r + p.pre_rp / 2);
     }
   }
   const int a0 = p.plan.spre[s], n = p.plan.spre[s + 1] - a0;
@@ -200,7 +207,7 @@ __global__ void __launch_bounds__(256) shared_merge_kernel(const SharedParams p,
   const Shares sh((int64_t)p.plan.spre[p.num_seqs] * H, p.suf_workers);
   const int w1 = sh.owner(a + n - 1);
   for (int w = sh.owner(a); w <= w1; ++w)
-    add(p.suf_o, p.suf_ml, p.suf_rp, (int64_t)s * H + h + w, i * p.group + gq);
+    add_private((int64_t)s * H + h + w, i * p.group + gq);
   float inv = l > 0.f ? 1.f / l : 0.f;
   if (scaled) inv *= __ldg(p.v_scale + (p.scale_per_head ? h : 0));
   __half2 h01 = __floats2half2_rn(acc.x * inv, acc.y * inv);
@@ -237,7 +244,7 @@ struct SharedLayout {
       return here;
     };
     pre_o = take((size_t)pre_slots * pre_rp * kHeadDim * 4);
-    pre_ml = take((size_t)pre_slots * 2 * pre_rp * 4);
+    pre_ml = take((size_t)pre_slots * 3 * pre_rp * 4);
     suf_o = take((size_t)suf_slots * suf_rp * kHeadDim * 4);
     suf_ml = take((size_t)suf_slots * 2 * suf_rp * 4);
     total = at;

@@ -46,9 +46,9 @@ struct SharedParams {
   int32_t* status;
   SharedPlan plan;
   float* pre_o;             // prefix fragments: [slots][RP][128] unnormalised O
-  float* pre_ml;            // [slots][2][RP] m (log2 units) and l
+  float* pre_ml;            // [slots][3][RP] m (log2 units), and l of either half's keys
   float* suf_o;             // private fragments, the same
-  float* suf_ml;
+  float* suf_ml;            // [slots][2][RP] m and l
   int64_t num_pages;
   int32_t bt_stride;
   int32_t num_seqs;

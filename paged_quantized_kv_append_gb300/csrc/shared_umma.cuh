@@ -11,9 +11,10 @@
 // a tile has at most 128 rows, the even and the odd key tiles of the same rows
 // (two partial results, joined by the merge like any others).
 //
-// Warps: 0-3 and 4-7 the softmax of stream 0 and 1 (a thread per row), 8-11
-// widen the 8-bit codes to fp16 (exact; TMA writes the fp16 pool's rows into
-// place itself), 12 issues the copies, 13 and 14 the products of a stream each.
+// Warps: 0-7 and 8-15 the softmax of stream 0 and 1 (two threads per row, each
+// with 64 of a tile's 128 keys), 16-19 widen the 8-bit codes to fp16 (exact; TMA
+// writes the fp16 pool's rows into place itself), 20 issues the copies, 21 and
+// 22 the products of a stream each, 23 announces the share's fragments.
 //
 // The running maximum of a row is only raised when a score passes it by more
 // than 8 (probabilities stay <= 2^8 in fp16), so O is rescaled rarely, by the
@@ -117,6 +118,19 @@ __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* r) {
 __device__ __forceinline__ void tmem_wait_ld() {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
+// one column
+__device__ __forceinline__ uint32_t tmem_ld1_wait(uint32_t addr) {
+  uint32_t v;
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];\n\t"
+               "tcgen05.wait::ld.sync.aligned;"
+               : "=r"(v)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ void tmem_st1(uint32_t addr, uint32_t v) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(addr), "r"(v) : "memory");
+}
 // 16 columns, for the rare rescale of O beside a row of scores in registers
 __device__ __forceinline__ void tmem_ld16_wait(uint32_t addr, uint32_t* r) {
   asm volatile(
@@ -159,10 +173,9 @@ __device__ __forceinline__ uint64_t tc_desc(uint32_t addr, uint32_t half_stride)
          ((uint64_t)(1024 >> 4) << 32) | (uint64_t(1) << 46) | (uint64_t(2) << 61);
 }
 
-// kind::f16, fp16 A and B, fp32 D, M 128, N 64 (keys) and 128 (dims); B with
-// its rows along K for V
-constexpr uint32_t kIdescQK = (1u << 4) | ((64u >> 3) << 17) | ((128u >> 4) << 24);
-constexpr uint32_t kIdescPV = (1u << 4) | (1u << 16) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
+// kind::f16, fp16 A and B, fp32 D, M 128, N 128; B with its rows along K for V
+constexpr uint32_t kIdescQK = (1u << 4) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
+constexpr uint32_t kIdescPV = kIdescQK | (1u << 16);
 
 __device__ __forceinline__ uint64_t f2(float a, float b) {
   uint64_t r;
@@ -186,6 +199,21 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
   uint64_t r;
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
+}
+
+// barrier of 64 threads (two warps); pair_any also ORs their predicates
+__device__ __forceinline__ void pair_sync(int id) {
+  asm volatile("barrier.sync.aligned %0, 64;" ::"r"(id) : "memory");
+}
+__device__ __forceinline__ bool pair_any(int id, bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %2, 0;\n\t"
+      "barrier.red.or.pred.aligned q, %1, 64, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(id), "r"((uint32_t)v)
+      : "memory");
+  return r != 0;
 }
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -228,56 +256,59 @@ __device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* map
 // ---------------------------------------------------------------------------
 // Work
 // ---------------------------------------------------------------------------
+// A fragment of the CTA's share: key tiles [u0, u0 + nt) of one row tile.
 struct UmmaFrag {
-  int g, h, rt;       // group, kv-head, row tile
-  int u0, u1;         // key tiles [u0, u1)
+  int nt;             // key tiles; 0: the share is done
+  int dual;           // more than 128 rows: the streams split the rows
+  int h;              // kv-head
+  int seq0;           // the group's first sequence
   int row0, nrows;    // first row of the tile, rows of the group's kv-head
-  int pages;          // shared pages of the group
-  int seg;            // segment: row tiles in order over groups and kv-heads
-  bool dual;          // more than 128 rows: the streams split the rows
+  int page0, pages;   // first page of the fragment, shared pages of the group
+  int slot;           // of the partial result
+  int pad[3];
 };
+static_assert(sizeof(UmmaFrag) == 48, "three 16-byte words");
 
 // The CTA's fragments in order.  Segment (g, h, rt) covers the costs
 // [a, a + w T) of its T key tiles (w = 2 or 1); key tile i belongs to the share
 // that holds cost a + w i.
 struct UmmaIter {
-  const int* tab;     // the plan's rows of groups
-  int stride;         // entries per row
+  const SharedParams& p;
   int64_t x, e;
 
-  __device__ int goff(int g) const { return tab[g]; }
-  __device__ int gpages(int g) const { return tab[stride + g]; }
-  __device__ int gtiles(int g) const { return tab[2 * stride + g]; }
-  __device__ int gcost(int g) const { return tab[3 * stride + g]; }
-
-  // M groups, H kv-heads, `rows` rows of a (sequence, kv-head)
-  __device__ bool next(UmmaFrag& f, int M, int H, int rows) {
+  __device__ UmmaFrag next(int cta) {
+    const int M = p.num_groups, H = p.num_kv_heads;
+    const int32_t *goff = p.plan.goff(), *gpages = p.plan.gpages(M), *gtiles = p.plan.gtiles(M),
+                  *gcost = p.plan.gcost(M);
+    UmmaFrag f = {};
     while (x < e) {
-      int lo = 0, hi = M - 1;
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if ((int64_t)gcost(mid) * H <= x) lo = mid; else hi = mid - 1;
+      int g = 0, hi = M - 1;
+      while (g < hi) {
+        const int mid = (g + hi + 1) >> 1;
+        if ((int64_t)gcost[mid] * H <= x) g = mid; else hi = mid - 1;
       }
-      const int g = lo, C = gcost(g + 1) - gcost(g);
-      const int T = (gpages(g) + kUmmaPages - 1) / kUmmaPages;
-      const int64_t off = x - (int64_t)gcost(g) * H;
-      f.g = g;
+      const int C = gcost[g + 1] - gcost[g];
+      const int T = (gpages[g] + kUmmaPages - 1) / kUmmaPages;
+      const int64_t off = x - (int64_t)gcost[g] * H;
       f.h = (int)Shares::div(off, C);
       const int in = (int)(off - (int64_t)f.h * C);
-      f.rt = in / (2 * T);
-      f.nrows = (goff(g + 1) - goff(g)) * rows;
-      f.row0 = f.rt * kUmmaRows;
+      const int rt = in / (2 * T);
+      f.seq0 = goff[g];
+      f.nrows = (goff[g + 1] - f.seq0) * p.rows;
+      f.row0 = rt * kUmmaRows;
       f.dual = f.nrows - f.row0 > 128;
       const int w = f.dual ? 2 : 1;
-      const int64_t a = x - (in - f.rt * 2 * T);
-      f.u0 = (int)((x - a + w - 1) / w);
-      f.u1 = (int)min((int64_t)T, (e - a + w - 1) / w);
-      f.pages = gpages(g);
-      f.seg = gtiles(g) * H + f.h * (gtiles(g + 1) - gtiles(g)) + f.rt;
+      const int64_t a = x - (in - rt * 2 * T);
+      const int u0 = (int)((x - a + w - 1) / w);
+      f.nt = (int)min((int64_t)T, (e - a + w - 1) / w) - u0;
+      f.page0 = u0 * kUmmaPages;
+      f.pages = gpages[g];
+      f.slot = gtiles[g] * H + f.h * (gtiles[g + 1] - gtiles[g]) + rt + cta;
       x = min(e, a + (int64_t)w * T);
-      if (f.u0 < f.u1) return true;
+      if (f.nt > 0) return f;
     }
-    return false;
+    f.nt = 0;
+    return f;
   }
 };
 
@@ -294,7 +325,8 @@ template <int KVT>
 struct UmmaCfg {
   static constexpr bool kWide = KVT == PQKV_KV_FP16;      // rows need no widening
   static constexpr bool kRowScaled = KVT == PQKV_KV_INT8_ROW;
-  static constexpr int kThreads = 512;
+  static constexpr int kThreads = 768;
+  static constexpr int kRegLaunch = 80;
   static constexpr long long kWaitCycles = 1ll << 31;     // 1.04 s at 2.07 GHz
   // A row's reference maximum is raised when a score passes it by more than
   // this (log2): probabilities stay <= 2^14, within fp16's 2^16, and the fewer
@@ -313,24 +345,24 @@ struct UmmaCfg {
   static constexpr int kScOff = kCodeOff + kSlabs * kSlab;  // fp16 row scales: 3 stages of K and V
   static constexpr int kScBytes = kRowScaled ? 3 * 2 * 128 * 2 : 0;
   static constexpr int kBarOff = kScOff + kScBytes;
-  static constexpr int kBars = 4 + 8 + 14 + 2;
-  // the plan of up to kTabGroups groups is copied to shared memory (more are
-  // read from L2: a search per fragment)
-  static constexpr int kTabGroups = kRowScaled ? 15 : 48;
-  static constexpr int kTabOff = kBarOff + kBars * 8 + 8;
-  static constexpr int kSmemBytes = kTabOff + 4 * (kTabGroups + 1) * 4 + 1024;
+  static constexpr int kBars = 4 + 8 + 10 + 8;
+  // fragments announced by the scheduling warp: a ring of kFrags
+  static constexpr int kFrags = 4;
+  static constexpr int kReaders = kWide ? 18 : 22;         // warps that read them
+  static constexpr int kFragOff = kBarOff + kBars * 8 + 8;
+  static constexpr int kSmemBytes = kFragOff + kFrags * (int)sizeof(UmmaFrag) + 1024;
   static_assert(kSmemBytes <= 232448, "shared memory of a block");
   // registers per thread of the softmax, widening and issuing warps, of the
-  // 128 * 512 that the block is launched with
-  static constexpr int kRegSoftmax = 152, kRegWiden = 120, kRegIssue = 88;
-  static_assert(2 * kRegSoftmax + kRegWiden + kRegIssue <= 4 * 128, "registers of the launch");
+  // 80 * 768 that the block is launched with
+  static constexpr int kRegSoftmax = 88, kRegWiden = 72, kRegIssue = 56;
+  static_assert(4 * kRegSoftmax + kRegWiden + kRegIssue <= 6 * kRegLaunch, "registers of the launch");
 };
 
 // ---------------------------------------------------------------------------
 // The kernel
 // ---------------------------------------------------------------------------
 template <int KVT>
-__global__ void __launch_bounds__(512, 1)
+__global__ void __launch_bounds__(768, 1)
     shared_umma_kernel(const __grid_constant__ CUtensorMap map, const SharedParams p) {
   using Cfg = UmmaCfg<KVT>;
   extern __shared__ uint8_t smem_raw[];
@@ -345,14 +377,15 @@ __global__ void __launch_bounds__(512, 1)
   uint64_t* v_full = bars + 8;
   uint64_t* v_empty = bars + 10;
   uint64_t* q_ready = bars + 12;       // [stream] the fragment's query rows are in place
-  uint64_t* s_full = bars + 14;        // [stream][half] 64 keys' scores in TMEM
-  uint64_t* p_ready = bars + 18;       // [stream][half] their probabilities, and O rescaled
-  uint64_t* o_done = bars + 22;        // [stream] their product with V is done
-  uint64_t* o_last = bars + 24;        // [stream] the fragment's last product with V is done
-  uint64_t* drain = bars + 26;         // [stream] after a wait that ran out
+  uint64_t* s_full = bars + 14;        // [stream] scores in TMEM
+  uint64_t* p_ready = bars + 16;       // [stream] their probabilities, and O rescaled
+  uint64_t* o_last = bars + 18;        // [stream] the fragment's last product with V is done
+  uint64_t* drain = bars + 20;         // after a wait that ran out
+  uint64_t* frag_full = bars + 22;     // [kFrags]
+  uint64_t* frag_empty = bars + 26;    // [kFrags]
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Cfg::kBarOff + Cfg::kBars * 8);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Cfg::kBarOff + Cfg::kBars * 8 + 4);
-  const int M = p.num_groups, H = p.num_kv_heads;
+  const int H = p.num_kv_heads;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
@@ -360,45 +393,30 @@ __global__ void __launch_bounds__(512, 1)
       mbar_init(&code_full[i], 1);
       mbar_init(&code_empty[i], 4);
       mbar_init(&k_full[i], Cfg::kWide ? 1 : 4);
-      mbar_init(&k_empty[i], 2);
+      mbar_init(&k_empty[i], 1);
       mbar_init(&v_full[i], Cfg::kWide ? 1 : 4);
-      mbar_init(&v_empty[i], 2);
-      mbar_init(&q_ready[i], 4);
+      mbar_init(&v_empty[i], 1);
+      mbar_init(&q_ready[i], 8);
       mbar_init(&s_full[i], 1);
-      mbar_init(&s_full[2 + i], 1);
-      mbar_init(&p_ready[i], 4);
-      mbar_init(&p_ready[2 + i], 4);
-      mbar_init(&o_done[i], 1);
+      mbar_init(&p_ready[i], 8);
       mbar_init(&o_last[i], 1);
-      mbar_init(&drain[i], 1);
+    }
+    mbar_init(drain, 1);
+    for (int i = 0; i < Cfg::kFrags; ++i) {
+      mbar_init(&frag_full[i], 1);
+      mbar_init(&frag_empty[i], Cfg::kReaders);
     }
     *abort_flag = 0;
     fence_barrier_init();
   }
-  if (warp == 13) tmem_alloc_512(tmem_slot);
-  if (warp == 12 && lane == 0) prefetch_tensormap(&map);
+  if (warp == 21) tmem_alloc_512(tmem_slot);
+  if (warp == 20 && lane == 0) prefetch_tensormap(&map);
   grid_dependency_wait();
   grid_dependents_launch();
-  UmmaIter it;
-  it.tab = p.plan.groups;
-  it.stride = M + 1;
-  if (M <= Cfg::kTabGroups) {
-    int* tab = reinterpret_cast<int*>(smem + Cfg::kTabOff);
-    for (int i = tid; i < 4 * (M + 1); i += Cfg::kThreads) tab[i] = p.plan.groups[i];
-    it.tab = tab;
-  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-
-  const Shares sh((int64_t)it.gcost(M) * H, p.pre_workers);
-  it.x = it.e = 0;
-  if ((int)blockIdx.x < sh.n) {
-    it.x = sh.start(blockIdx.x);
-    it.e = sh.start(blockIdx.x + 1);
-  }
-  UmmaFrag f;
 
   // Bounded wait (about 1 s).  When one runs out the whole CTA stops at its next waits.
   // Called by whole warps; every lane gets the same answer.
@@ -420,227 +438,264 @@ __global__ void __launch_bounds__(512, 1)
     }
   };
 
-  if (warp < 8) {
-    // ================= softmax: thread = row =================
+  // Fragment n of the CTA's share (waits until it is announced; false after a
+  // wait that ran out), and the warp's word that it is done with it.
+  const UmmaFrag* frags = reinterpret_cast<const UmmaFrag*>(smem + Cfg::kFragOff);
+  auto frag_at = [&](uint32_t n, const UmmaFrag*& f) -> bool {
+    f = frags + n % Cfg::kFrags;
+    return wait(&frag_full[n % Cfg::kFrags], (n / Cfg::kFrags) & 1);
+  };
+  auto frag_done = [&](uint32_t n) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&frag_empty[n % Cfg::kFrags]);
+  };
+
+  if (warp < 16) {
+    // ================= softmax: two threads per row =================
     regs_up<Cfg::kRegSoftmax>();
-    const int st = warp >> 2, wq = warp & 3, r = wq * 32 + lane;
+    const int st = warp >> 3, half = (warp >> 2) & 1, wq = warp & 3, r = wq * 32 + lane;
     const uint32_t lane_sel = (uint32_t)(wq * 32) << 16;
-    const uint32_t tS = tmem + lane_sel + st * 128, tO = tmem + lane_sel + 256 + st * 128;
-    uint32_t n_step = 0;             // steps of this stream so far (a key tile: two halves)
-    uint32_t n_frag = 0;             // its fragments with a step
+    // this thread's 64 scores, over them its 64 probabilities, and 64 values of O
+    const uint32_t tS = tmem + lane_sel + st * 128 + half * 64;
+    const uint32_t tO = tmem + lane_sel + 256 + st * 128 + half * 64;
+    const int pair = 1 + st * 4 + wq;                       // barrier of the row's two warps
+    const uint32_t tPeer = tS + 63 - half * 128 + 64;       // the other half's last column
+    uint32_t n_step = 0;             // steps of this stream so far
+    uint32_t n_last = 0;             // its fragments with a step
     uint32_t n_tile = 0;             // key tiles of the CTA so far (row scales' stages)
-    // the fragment's row of this thread, or -1; its query row into shared memory
-    auto load_row = [&]() -> int {
-      const int row = f.row0 + (f.dual ? st * 128 : 0) + r;
-      const int steps = f.dual ? f.u1 - f.u0 : (f.u1 - f.u0 + 1 - st) / 2;
-      const bool live = row < f.nrows;
-      if (steps > 0) {
-        const int64_t tok = (int64_t)it.goff(f.g) * p.q_len + row / p.group;
+    uint32_t n = 0;                  // fragments
+    const UmmaFrag* f;
+    // whether fragment f has a row for this thread; half of it into shared memory
+    auto load_row = [&]() -> bool {
+      const int nt = f->nt, dual = f->dual, row = f->row0 + (dual ? st * 128 : 0) + r;
+      const bool live = row < f->nrows;
+      if (dual || nt > st) {
+        const int64_t tok = (int64_t)f->seq0 * p.q_len + row / p.group;
         const uint4* src = reinterpret_cast<const uint4*>(
-            p.q + (tok * p.num_q_heads + f.h * p.group + row % p.group) * kHeadDim);
-        const uint32_t dst = sbase + Cfg::kQOff + st * Cfg::kTile + r * 128;
-        uint4 v[16];
+            p.q + (tok * p.num_q_heads + f->h * p.group + row % p.group) * kHeadDim + half * 64);
+        const uint32_t dst = sbase + Cfg::kQOff + st * Cfg::kTile + half * Cfg::kHalf + r * 128;
+        uint4 v[8];
 #pragma unroll
-        for (int c = 0; c < 16; ++c) v[c] = live ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
+        for (int c = 0; c < 8; ++c) v[c] = live ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
 #pragma unroll
-        for (int c = 0; c < 16; ++c)
-          sts128(dst + (c >> 3) * Cfg::kHalf + (((c & 7) ^ (r & 7)) << 4), v[c].x, v[c].y, v[c].z,
-                 v[c].w);
+        for (int c = 0; c < 8; ++c)
+          sts128(dst + ((c ^ (r & 7)) << 4), v[c].x, v[c].y, v[c].z, v[c].w);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&q_ready[st]);
       }
-      return live ? row : -1;
+      return live;
     };
-    bool ok = it.next(f, M, H, p.rows);
-    int my_row = ok ? load_row() : -1;
+    // 32 scores from column c on: scaled by their rows' scales, -inf behind the prefix
+    auto scores = [&](uint32_t* s, int c, int valid, uint32_t sc) {
+      tmem_ld32(tS + c, s);
+      tmem_wait_ld();
+      tmem_landed32(s);
+      if constexpr (Cfg::kRowScaled) {
+#pragma unroll
+        for (int k = 0; k < 32; k += 8) {
+          const uint4 k8 = lds128u(sc + (c + k) * 2);
+          const uint32_t kk[4] = {k8.x, k8.y, k8.z, k8.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float2 ks = __half22float2(*reinterpret_cast<const __half2*>(&kk[j]));
+            s[k + 2 * j] = __float_as_uint(__uint_as_float(s[k + 2 * j]) * ks.x);
+            s[k + 2 * j + 1] = __float_as_uint(__uint_as_float(s[k + 2 * j + 1]) * ks.y);
+          }
+        }
+      }
+      if (valid < 64) {
+#pragma unroll
+        for (int k = 0; k < 32; ++k)
+          if (c + k >= valid) s[k] = 0xff800000u;
+      }
+    };
+    auto max32 = [&](const uint32_t* s) -> float {
+      float m[4] = {kNoScore, kNoScore, kNoScore, kNoScore};
+#pragma unroll
+      for (int k = 0; k < 32; k += 2)
+        m[(k >> 1) & 3] = max3(m[(k >> 1) & 3], __uint_as_float(s[k]), __uint_as_float(s[k + 1]));
+      return max3(fmaxf(m[0], m[1]), m[2], m[3]);
+    };
+    bool ok = frag_at(n, f) && f->nt > 0;
+    bool live = ok && load_row();
     while (ok) {
       float scale = p.sm_scale_log2;
       if constexpr (KVT == PQKV_KV_FP8_E4M3 || KVT == PQKV_KV_INT8) {
-        const int hs = p.scale_per_head ? f.h : 0;
+        const int hs = p.scale_per_head ? f->h : 0;
         const float ks = __ldg(p.k_scale + hs), vs = __ldg(p.v_scale + hs);
         if (!(ks > 0.f && ks <= 3.4e38f && vs > 0.f && vs <= 3.4e38f))
           report(p.status, PQKV_DEV_BAD_SCALE);
         scale *= ks;
       }
-      const int nt = f.u1 - f.u0, steps = f.dual ? nt : (nt + 1 - st) / 2;
-      const int keys = f.pages * kPageSize - f.u0 * kUmmaKeys;     // of the fragment, and behind
-      const bool dual = f.dual;
-      const bool warp_live = __any_sync(0xffffffffu, my_row >= 0);
-      const int64_t slot = (int64_t)f.seg + blockIdx.x;
-      const int at = st * (p.pre_rp / 2) + r;
+      const int nt = f->nt, dual = f->dual, slot = f->slot;
+      const int steps = dual ? nt : (nt + 1 - st) / 2;
+      // keys of the prefix from this thread's first on
+      int valid = (f->pages - f->page0) * kPageSize - half * 64 - (dual ? 0 : st * kUmmaKeys);
+      const bool warp_live = __any_sync(0xffffffffu, live);
       float ref = kNoScore, l = 0.f;
 #pragma unroll 1
-      for (int i = 0; ok && i < steps; ++i) {
-        const int u = dual ? i : 2 * i + st;
-        const uint32_t sc = sbase + Cfg::kScOff + (n_tile + u) % 3 * 512;
+      for (int i = 0; i < steps; ++i) {
+        if (!wait(&s_full[st], n_step & 1)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        if (warp_live) {
+          // 64 fp16 scales of K, of V 256 bytes on
+          const uint32_t sc = sbase + Cfg::kScOff + half * 128 +
+                              (n_tile + (dual ? i : 2 * i + st)) % 3 * 512;
+          uint32_t s[32], s2[32];
+          scores(s2, 32, valid, sc);
+          const float hi = max32(s2);
+          scores(s, 0, valid, sc);
+          const float m2 = fmaxf(hi, max32(s)) * scale;
+          if (pair_any(pair, m2 > ref + Cfg::kRaise)) {
+            // raise: the two warps tell each other their rows' maxima (in the last
+            // score column of their half, put back afterwards) and rescale half of
+            // O each.  O is still: the last product with V came before these scores
+            const uint32_t keep = tmem_ld1_wait(tS + 63);
+            tmem_st1(tS + 63, __float_as_uint(m2));
+            tmem_wait_st();
+            tc_fence_before();
+            pair_sync(pair);
+            tc_fence_after();
+            const float both = fmaxf(m2, __uint_as_float(tmem_ld1_wait(tPeer)));
+            tc_fence_before();
+            pair_sync(pair);
+            tc_fence_after();
+            tmem_st1(tS + 63, keep);
+            tmem_wait_st();
+            const float nref = both > ref + Cfg::kRaise ? both : ref;
+            const float fct = ex2(ref - nref);
+            ref = nref;
+            l *= fct;
+            if (i > 0) {
 #pragma unroll 1
-        for (int half = 0; half < 2; ++half) {
-          if (!wait(&s_full[2 * st + half], n_step & 1)) {
-            ok = false;
-            break;
+              for (int c = 0; c < 64; c += 16) {
+                uint32_t o[16];
+                tmem_ld16_wait(tO + c, o);
+#pragma unroll
+                for (int k = 0; k < 16; ++k)
+                  o[k] = __float_as_uint(__uint_as_float(o[k]) * fct);
+                tmem_st16(tO + c, o);
+              }
+            }
           }
-          tc_fence_after();
-          if (warp_live) {
-            const uint32_t tH = tS + 64 * half;
-            uint32_t s[64];
-            tmem_ld32(tH, s);
-            tmem_ld32(tH + 32, s + 32);
-            tmem_wait_ld();
-            tmem_landed32(s);
-            tmem_landed32(s + 32);
-            const uint32_t sch = sc + 128 * half;          // 64 fp16 scales of K, of V 256 bytes on
-            if constexpr (Cfg::kRowScaled) {
+          const uint64_t scale2 = f2(scale, scale), ref2 = f2(-ref, -ref);
+          uint64_t sum[4] = {0, 0, 0, 0};
 #pragma unroll
-              for (int c = 0; c < 64; c += 8) {
-                const uint4 k8 = lds128u(sch + c * 2);
-                const uint32_t kk[4] = {k8.x, k8.y, k8.z, k8.w};
+          for (int c = 0; c < 64; c += 32) {
+            if (c) scores(s, 32, valid, sc);           // read again: registers are short
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                  const float2 ks = __half22float2(*reinterpret_cast<const __half2*>(&kk[j]));
-                  s[c + 2 * j] = __float_as_uint(__uint_as_float(s[c + 2 * j]) * ks.x);
-                  s[c + 2 * j + 1] = __float_as_uint(__uint_as_float(s[c + 2 * j + 1]) * ks.y);
-                }
-              }
-            }
-            const int valid = keys - u * kUmmaKeys - 64 * half;
-            if (valid < 64) {
-#pragma unroll
-              for (int c = 0; c < 64; ++c)
-                if (c >= valid) s[c] = 0xff800000u;            // -inf
-            }
-            float mx4[4] = {kNoScore, kNoScore, kNoScore, kNoScore};
-#pragma unroll
-            for (int c = 0; c < 64; c += 2)
-              mx4[(c >> 1) & 3] = max3(mx4[(c >> 1) & 3], __uint_as_float(s[c]),
-                                       __uint_as_float(s[c + 1]));
-            const float m2 = max3(fmaxf(mx4[0], mx4[1]), mx4[2], mx4[3]) * scale;
-            const bool raise = m2 > ref + Cfg::kRaise;
-            if (__any_sync(0xffffffffu, raise)) {
-              const float nref = raise ? m2 : ref;
-              const float fct = ex2(ref - nref);
-              ref = nref;
-              l *= fct;
-              if (i + half > 0) {                              // O holds something
-                // the half before this one (the one before that is done: this
-                // half's scores were issued behind its product)
-                if (!wait(&o_done[st], (half + 1) & 1)) {
-                  ok = false;
-                  break;
-                }
-                tc_fence_after();
-#pragma unroll 1
-                for (int c = 0; c < 128; c += 16) {
-                  uint32_t o[16];
-                  tmem_ld16_wait(tO + c, o);
-#pragma unroll
-                  for (int k = 0; k < 16; ++k)
-                    o[k] = __float_as_uint(__uint_as_float(o[k]) * fct);
-                  tmem_st16(tO + c, o);
-                }
-              }
-            }
-            const uint64_t scale2 = f2(scale, scale), ref2 = f2(-ref, -ref);
-            uint64_t sum[4] = {0, 0, 0, 0};
-            uint32_t ph[32];
-#pragma unroll
-            for (int c = 0; c < 32; ++c) {
+            for (int k = 0; k < 16; ++k) {
               float a, b;
-              unf2(fma2(f2(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1])), scale2, ref2),
+              unf2(fma2(f2(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1])), scale2, ref2),
                    a, b);
               a = ex2(a);
               b = ex2(b);
-              sum[c & 3] = add2(sum[c & 3], f2(a, b));
+              sum[k & 3] = add2(sum[k & 3], f2(a, b));
               if constexpr (Cfg::kRowScaled) {
                 // p * (V row scale), rounded once: the fp32 product
                 uint32_t w;
-                asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w) : "r"(sch + 256 + c * 4));
+                asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w) : "r"(sc + 256 + (c + 2 * k) * 2));
                 const float2 vs = __half22float2(*reinterpret_cast<const __half2*>(&w));
                 a *= vs.x;
                 b *= vs.y;
               }
-              ph[c] = pack_half2(a, b);
+              s[k] = pack_half2(a, b);
             }
-            tmem_st32(tH, ph);
-            float a, b;
-            unf2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), a, b);
-            l += a + b;
-            tmem_wait_st();
+            tmem_st16(tS + c / 2, s);
           }
-          // (a warp without a row: its probabilities feed rows that nobody reads)
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&p_ready[2 * st + half]);
+          float a, b;
+          unf2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), a, b);
+          l += a + b;
+          tmem_wait_st();
         }
+        // (a warp without a row: its probabilities feed rows that nobody reads)
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_ready[st]);
         n_step += 1;
+        valid -= dual ? kUmmaKeys : 2 * kUmmaKeys;
       }
       n_tile += nt;
       if (!ok) break;
       // ---- the next fragment's query row (this one's scores are done), so that
       // its first product runs under what follows
-      const bool live = my_row >= 0;
-      ok = it.next(f, M, H, p.rows);
-      if (ok) my_row = load_row();
+      frag_done(n);
+      n += 1;
+      const bool store = live;
+      if (!frag_at(n, f)) break;
+      ok = f->nt > 0;
+      live = ok && load_row();
       // ---- O, m and l of the fragment
       if (steps > 0) {
-        if (!wait(&o_last[st], n_frag & 1)) break;
-        n_frag += 1;
+        if (!wait(&o_last[st], n_last & 1)) break;
+        n_last += 1;
         tc_fence_after();
       }
       if (warp_live) {
-        float* dst = p.pre_o + (slot * p.pre_rp + at) * kHeadDim;
+        const int at = st * (p.pre_rp / 2) + r;
+        float* dst = p.pre_o + ((int64_t)slot * p.pre_rp + at) * kHeadDim + half * 64;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
+        for (int c = 0; c < 64; c += 32) {
           uint32_t o[32];
           if (steps > 0) {
-            tmem_ld32(tO + 32 * c, o);
+            tmem_ld32(tO + c, o);
             tmem_wait_ld();
             tmem_landed32(o);
           } else {
 #pragma unroll
             for (int k = 0; k < 32; ++k) o[k] = 0;
           }
-          if (live) {
+          if (store) {
 #pragma unroll
-            for (int k = 0; k < 32; k += 8) stg256(dst + 32 * c + k, o + k);
+            for (int k = 0; k < 32; k += 8) stg256(dst + c + k, o + k);
           }
         }
-        if (live) {
-          p.pre_ml[slot * 2 * p.pre_rp + at] = ref;
-          p.pre_ml[slot * 2 * p.pre_rp + p.pre_rp + at] = l;
+        if (store) {                                           // m, and l of either half
+          float* ml = p.pre_ml + (int64_t)slot * 3 * p.pre_rp + at;
+          if (half == 0) ml[0] = ref;
+          ml[(1 + half) * p.pre_rp] = l;
         }
       }
       tc_fence_before();
     }
-  } else if (warp < 12) {
+  } else if (warp < 20) {
     // ================= widen the codes =================
     regs_down<Cfg::kRegWiden>();
     if constexpr (!Cfg::kWide) {
-      const int wt = tid - 256;
+      const int wt = tid - 512;
       uint32_t n_slab = 0, n_tile = 0;
       bool ok = true;
       // INT8_ROW: K and V row scale (fp16 bits) of this thread's token of key
       // tile u; 0 behind the prefix and for pages outside the pool
+      const UmmaFrag* f;
       auto row_scale = [&](int u) -> ushort2 {
-        const int tok = u * kUmmaKeys + wt, pg = tok / kPageSize, rr = tok % kPageSize;
-        if (pg >= f.pages) return make_ushort2(0, 0);
-        const int id = __ldg(p.block_table + (int64_t)it.goff(f.g) * p.bt_stride + pg);
+        const int pg = f->page0 + u * kUmmaPages + wt / kPageSize, rr = wt % kPageSize;
+        if (pg >= f->pages) return make_ushort2(0, 0);
+        const int id = __ldg(p.block_table + (int64_t)f->seq0 * p.bt_stride + pg);
         if (id < 0 || (int64_t)id >= p.num_pages) return make_ushort2(0, 0);
         const uint16_t* src = reinterpret_cast<const uint16_t*>(p.k_scale) +
-                              (((int64_t)id * H + f.h) * 8 + (rr & 7)) * 4 + (rr >> 3);
+                              (((int64_t)id * H + f->h) * 8 + (rr & 7)) * 4 + (rr >> 3);
         return make_ushort2(__ldg(src), __ldg(src + 2));
       };
       ushort2 ahead = make_ushort2(0, 0);
-      while (ok && it.next(f, M, H, p.rows)) {
-        for (int u = f.u0; ok && u < f.u1; ++u, ++n_tile) {
+      for (uint32_t n = 0; ok; ++n) {
+        if (!frag_at(n, f)) break;
+        const int nt = f->nt;
+        if (nt == 0) break;
+        for (int u = 0; ok && u < nt; ++u, ++n_tile) {
           if constexpr (Cfg::kRowScaled) {
             // The tile's fp16 row scales, a token per thread, read a tile ahead.
             // Stage n % 3 was last read by the softmax of tile n - 3, whose
             // product with V the V stage's release for tile n - 1 came after.
             uint16_t* dst = reinterpret_cast<uint16_t*>(smem + Cfg::kScOff + n_tile % 3 * 512);
-            dst[wt] = u == f.u0 ? row_scale(u).x : ahead.x;
-            dst[128 + wt] = u == f.u0 ? row_scale(u).y : ahead.y;
-            if (u + 1 < f.u1) ahead = row_scale(u + 1);
+            if (u == 0) ahead = row_scale(0);
+            dst[wt] = ahead.x;
+            dst[128 + wt] = ahead.y;
+            if (u + 1 < nt) ahead = row_scale(u + 1);
           }
 #pragma unroll 1
           for (int kv = 0; kv < 2; ++kv, ++n_slab) {
@@ -681,25 +736,35 @@ __global__ void __launch_bounds__(512, 1)
             }
           }
         }
+        frag_done(n);
       }
     }
   } else {
   regs_down<Cfg::kRegIssue>();
-  if (warp == 12) {
+  if (warp == 20) {
     // ================= copies =================
     uint32_t n = 0, n_tile = 0;      // copies (K or V of a key tile) and key tiles so far
     bool ok = true;
-    while (ok && it.next(f, M, H, p.rows)) {
-      const int32_t* row = p.block_table + (int64_t)it.goff(f.g) * p.bt_stride;
-      for (int u = f.u0; ok && u < f.u1; ++u, ++n_tile) {
-        // lane = page of the tile; pages behind the prefix read as zeros
-        // (a page id one past the pool: the copy's bounds fill them)
-        int id = (int)p.num_pages;
+    const UmmaFrag* f;
+    for (uint32_t nf = 0; ok; ++nf) {
+      if (!(ok = frag_at(nf, f))) break;
+      const int nt = f->nt, h = f->h;
+      if (nt == 0) break;
+      const int32_t* row = p.block_table + (int64_t)f->seq0 * p.bt_stride + f->page0;
+      const int left = f->pages - f->page0;
+      // lane = page of the tile, looked up a tile ahead; pages behind the prefix
+      // read as zeros (a page id one past the pool: the copy's bounds fill them)
+      auto page_id = [&](int u) -> int {
         const int pg = u * kUmmaPages + lane;
-        if (lane < kUmmaPages && pg < f.pages) {
-          id = __ldg(row + pg);
-          if (id < 0 || (int64_t)id >= p.num_pages) report(p.status, PQKV_DEV_PAGE_RANGE);
-        }
+        return lane < kUmmaPages && u < nt && pg < left ? __ldg(row + pg) : (int)p.num_pages;
+      };
+      int next_id = page_id(0);
+      for (int u = 0; ok && u < nt; ++u, ++n_tile) {
+        const int id = next_id;
+        next_id = page_id(u + 1);
+        if (lane < kUmmaPages && u * kUmmaPages + lane < left &&
+            (id < 0 || (int64_t)id >= p.num_pages))
+          report(p.status, PQKV_DEV_PAGE_RANGE);
         for (int kv = 0; kv < 2; ++kv) {
           if constexpr (Cfg::kWide) {
             const int stage = n_tile & 1;
@@ -711,8 +776,8 @@ __global__ void __launch_bounds__(512, 1)
             if (lane < kUmmaPages) {
               const uint32_t dst =
                   sbase + (kv ? Cfg::kVOff : Cfg::kKOff) + stage * Cfg::kTile + lane * 2048;
-              tma_load_5d(dst, &map, full, 0, 0, kv * kPageSize, f.h, id);
-              tma_load_5d(dst + Cfg::kHalf, &map, full, 0, 1, kv * kPageSize, f.h, id);
+              tma_load_5d(dst, &map, full, 0, 0, kv * kPageSize, h, id);
+              tma_load_5d(dst + Cfg::kHalf, &map, full, 0, 1, kv * kPageSize, h, id);
             }
             ++n;
           } else {
@@ -723,11 +788,12 @@ __global__ void __launch_bounds__(512, 1)
             __syncwarp();
             if (lane < kUmmaPages)
               tma_load_5d(sbase + Cfg::kCodeOff + slot * Cfg::kSlab + lane * 2048, &map,
-                          &code_full[slot], 0, 0, kv * kPageSize, f.h, id);
+                          &code_full[slot], 0, 0, kv * kPageSize, h, id);
             ++n;
           }
         }
       }
+      if (ok) frag_done(nf);
     }
     // after a wait that ran out: no copy may be in flight when the CTA ends
     __syncwarp();
@@ -740,87 +806,96 @@ __global__ void __launch_bounds__(512, 1)
           (void)mbar_wait(&code_full[i % Cfg::kSlabs], (i / Cfg::kSlabs) & 1);
       }
     }
-  } else if (warp < 15) {
-    // ================= products: a warp per stream =================
-    // The tensor pipe takes few products ahead of the one it works on, so a
-    // wait between two products of a warp leaves it idle; with a warp for each
-    // stream the other stream's products fill the gap.
-    const int st = warp - 13;
-    uint32_t n_tile = 0, n_q = 0, n_step = 0;
+  } else if (warp == 21) {
+    // ================= products =================
+    // The streams take turns: a stream's product with V and its next scores, then
+    // the other's.  Issued by a warp each, the streams' products mixed, both had
+    // their scores at the same time and then the tensor cores idle.
+    uint32_t n_tile = 0, n_q[2] = {0, 0}, n_step[2] = {0, 0};
     bool ok = true;
-    const uint64_t q_desc = tc_desc(sbase + Cfg::kQOff + st * Cfg::kTile, 16),
-                   k_desc = tc_desc(sbase + Cfg::kKOff, 16),
+    const uint64_t q_desc = tc_desc(sbase + Cfg::kQOff, 16), k_desc = tc_desc(sbase + Cfg::kKOff, 16),
                    v_desc = tc_desc(sbase + Cfg::kVOff, Cfg::kHalf);
-    const uint32_t tS = tmem + st * 128, tO = tmem + 256 + st * 128;
-    while (ok && it.next(f, M, H, p.rows)) {
-      const int nt = f.u1 - f.u0;
-      const bool dual = f.dual;
-      const int steps = dual ? nt : (nt + 1 - st) / 2;
-      // S = Q K^T on half a key tile.  A stage is free again when both streams
-      // are done with it, or after its one stream's second arrival.
-      auto qk = [&](uint32_t tl, int half) -> bool {
-        const uint32_t stage = tl & 1;
-        if (!half && !wait(&k_full[stage], (tl >> 1) & 1)) return false;
+    const UmmaFrag* f;
+    for (uint32_t nf = 0; ok; ++nf) {
+      if (!(ok = frag_at(nf, f))) break;
+      const int nt = __shfl_sync(0xffffffffu, f->nt, 0);
+      const bool dual = __shfl_sync(0xffffffffu, f->dual, 0);
+      if (nt == 0) break;
+      const int steps = dual ? 2 * nt : nt;              // step i: stream i & 1
+      // S = Q K^T of step i on its key tile
+      auto qk = [&](int i, int st) -> bool {
+        const uint32_t tl = n_tile + (dual ? i >> 1 : i), stage = tl & 1;
+        if (!wait(&k_full[stage], (tl >> 1) & 1)) return false;
         tc_fence_after();
         if (elect_one()) {
-          const uint64_t b = k_desc + (uint64_t)((stage * Cfg::kTile + half * 8192) >> 4);
+          const uint64_t a = q_desc + (uint64_t)(st * (Cfg::kTile >> 4)),
+                         b = k_desc + (uint64_t)(stage * (Cfg::kTile >> 4));
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
             const uint64_t off = (uint64_t)(((k >> 2) * Cfg::kHalf + (k & 3) * 32) >> 4);
-            tc_mma_ss(tS + 64 * half, q_desc + off, b + off, kIdescQK, k > 0);
+            tc_mma_ss(tmem + st * 128, a + off, b + off, kIdescQK, k > 0);
           }
-          tc_commit(&s_full[2 * st + half]);
-          if (half) {
-            tc_commit(&k_empty[stage]);
-            if (!dual) tc_commit(&k_empty[stage]);
-          }
+          tc_commit(&s_full[st]);
+          if (!dual || st == 1) tc_commit(&k_empty[stage]);
         }
         __syncwarp();
         return true;
       };
-      // O += P V on half a key tile
-      auto pv = [&](uint32_t tl, int half, bool acc, bool last) -> bool {
-        const uint32_t stage = tl & 1;
-        if (!half && !wait(&v_full[stage], (tl >> 1) & 1)) return false;
-        if (!wait(&p_ready[2 * st + half], n_step & 1)) return false;
+      // O += P V of step i; P lies over the scores, 32 columns for either half's
+      // 64 keys.  Then the stream's next scores, over the probabilities: products
+      // of one thread run in order
+      auto pv = [&](int i, int st) -> bool {
+        const uint32_t tl = n_tile + (dual ? i >> 1 : i), stage = tl & 1;
+        if (!wait(&v_full[stage], (tl >> 1) & 1) || !wait(&p_ready[st], n_step[st] & 1)) return false;
+        n_step[st] += 1;
         tc_fence_after();
         if (elect_one()) {
-          const uint64_t b = v_desc + (uint64_t)((stage * Cfg::kTile + half * 8192) >> 4);
+          const uint64_t b = v_desc + (uint64_t)(stage * (Cfg::kTile >> 4));
+          const uint32_t tS = tmem + st * 128, tO = tmem + 256 + st * 128;
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            tc_mma_ts(tO, tS + 64 * half + k * 8, b + (uint64_t)(k * 2048 >> 4), kIdescPV,
-                      acc || k > 0);
-          tc_commit(&o_done[st]);
-          if (half) {
-            tc_commit(&v_empty[stage]);
-            if (!dual) tc_commit(&v_empty[stage]);
-            if (last) tc_commit(&o_last[st]);
-          }
+          for (int k = 0; k < 8; ++k)
+            tc_mma_ts(tO, tS + (k >> 2) * 64 + (k & 3) * 8, b + (uint64_t)(k * 2048 >> 4), kIdescPV,
+                      i > 1 || k > 0);
+          if (!dual || st == 1) tc_commit(&v_empty[stage]);
+          if (i + 2 >= steps) tc_commit(&o_last[st]);
         }
         __syncwarp();
-        return true;
+        return i + 2 >= steps || qk(i + 2, st);
       };
-      // Half h's next scores go over its probabilities, right behind the product
-      // that reads them (products of one thread run in order), so that they are
-      // there when the softmax is done with the other half.
-      if (steps > 0) {
-        const uint32_t tl = n_tile + (dual ? 0 : st);
-        ok = wait(&q_ready[st], n_q & 1) && qk(tl, 0) && qk(tl, 1);
-        n_q += 1;
+      ok = wait(&q_ready[0], n_q[0] & 1) && qk(0, 0);
+      n_q[0] += 1;
+      if (ok && steps > 1) {
+        ok = wait(&q_ready[1], n_q[1] & 1) && qk(1, 1);
+        n_q[1] += 1;
       }
 #pragma unroll 1
-      for (int i = 0; ok && i < steps; ++i) {
-        const uint32_t tl = n_tile + (dual ? i : 2 * i + st), next = tl + (dual ? 1 : 2);
-        const bool more = i + 1 < steps;
-        ok = pv(tl, 0, i > 0, false) && (!more || qk(next, 0)) && pv(tl, 1, true, !more) &&
-             (!more || qk(next, 1));
-        n_step += 1;
-      }
+      for (int i = 0; ok && i < steps; i += 2) ok = pv(i, 0) && (i + 1 >= steps || pv(i + 1, 1));
       n_tile += nt;
+      if (ok) frag_done(nf);
     }
     if (!ok) {                       // products in flight end before the TMEM is freed
-      if (elect_one()) tc_commit(&drain[st]);
-      (void)mbar_wait(&drain[st], 0);
+      if (elect_one()) tc_commit(drain);
+      (void)mbar_wait(drain, 0);
+    }
+  } else if (warp == 22) {
+    // ================= (no role) =================
+  } else {
+    // ================= the share's fragments =================
+    const Shares sh((int64_t)p.plan.gcost(p.num_groups)[p.num_groups] * H, p.pre_workers);
+    UmmaIter it{p, 0, 0};
+    if ((int)blockIdx.x < sh.n) {
+      it.x = sh.start(blockIdx.x);
+      it.e = sh.start(blockIdx.x + 1);
+    }
+    UmmaFrag* out = reinterpret_cast<UmmaFrag*>(smem + Cfg::kFragOff);
+    for (uint32_t n = 0;; ++n) {
+      const UmmaFrag f = it.next(blockIdx.x);
+      if (n >= Cfg::kFrags && !wait(&frag_empty[n % Cfg::kFrags], (n / Cfg::kFrags + 1) & 1)) break;
+      if (lane == 0) {
+        out[n % Cfg::kFrags] = f;
+        mbar_arrive(&frag_full[n % Cfg::kFrags]);
+      }
+      if (f.nt == 0) break;
     }
   }
   }
@@ -828,7 +903,7 @@ __global__ void __launch_bounds__(512, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 13) tmem_free_512(tmem);
+  if (warp == 21) tmem_free_512(tmem);
 }
 
 template <int KVT>
@@ -838,13 +913,13 @@ cudaError_t launch_shared_umma_t(const SharedParams& p, const CUtensorMap& map,
   static std::atomic<uint64_t> done{0};
   const cudaError_t e = opt_in_smem(shared_umma_kernel<KVT>, Cfg::kSmemBytes, done);
   if (e != cudaSuccess) return e;
-  // the register split needs the 128 registers per thread that the launch
+  // the register split needs the 80 registers per thread that the launch
   // bounds allow; a build that used fewer would wait for them forever
   static const int regs = [] {
     cudaFuncAttributes at;
     return cudaFuncGetAttributes(&at, shared_umma_kernel<KVT>) == cudaSuccess ? at.numRegs : 0;
   }();
-  if (regs < 128) return cudaErrorLaunchOutOfResources;
+  if (regs < Cfg::kRegLaunch) return cudaErrorLaunchOutOfResources;
   return launch_pdl(shared_umma_kernel<KVT>, p.pre_workers, Cfg::kThreads, Cfg::kSmemBytes, stream,
                     map, p);
 }
