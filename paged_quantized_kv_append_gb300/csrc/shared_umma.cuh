@@ -701,8 +701,10 @@ __global__ void __launch_bounds__(768, 1)
           for (int kv = 0; kv < 2; ++kv, ++n_slab) {
             const int slot = n_slab % Cfg::kSlabs, stage = n_tile & 1;
             uint64_t* empty = (kv ? v_empty : k_empty) + stage;
-            if (!wait(&code_full[slot], (n_slab / Cfg::kSlabs) & 1) ||
-                (n_tile >= 2 && !wait(empty, ((n_tile >> 1) + 1) & 1))) {
+            // both at once, a barrier per lane
+            const bool odd = (lane & 1) && n_tile >= 2;
+            if (!wait(odd ? empty : &code_full[slot],
+                      (odd ? (n_tile >> 1) + 1 : n_slab / Cfg::kSlabs) & 1)) {
               ok = false;
               break;
             }
@@ -822,31 +824,47 @@ __global__ void __launch_bounds__(768, 1)
       const bool dual = __shfl_sync(0xffffffffu, f->dual, 0);
       if (nt == 0) break;
       const int steps = dual ? 2 * nt : nt;              // step i: stream i & 1
-      // S = Q K^T of step i on its key tile
-      auto qk = [&](int i, int st) -> bool {
-        const uint32_t tl = n_tile + (dual ? i >> 1 : i), stage = tl & 1;
-        if (!wait(&k_full[stage], (tl >> 1) & 1)) return false;
-        tc_fence_after();
-        if (elect_one()) {
-          const uint64_t a = q_desc + (uint64_t)(st * (Cfg::kTile >> 4)),
-                         b = k_desc + (uint64_t)(stage * (Cfg::kTile >> 4));
+      auto tile_of = [&](int i) -> uint32_t { return n_tile + (dual ? i >> 1 : i); };
+      // S = Q K^T of step i on its key tile (one thread)
+      auto qk = [&](int i, int st) {
+        const uint32_t stage = tile_of(i) & 1;
+        const uint64_t a = q_desc + (uint64_t)(st * (Cfg::kTile >> 4)),
+                       b = k_desc + (uint64_t)(stage * (Cfg::kTile >> 4));
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const uint64_t off = (uint64_t)(((k >> 2) * Cfg::kHalf + (k & 3) * 32) >> 4);
-            tc_mma_ss(tmem + st * 128, a + off, b + off, kIdescQK, k > 0);
-          }
-          tc_commit(&s_full[st]);
-          if (!dual || st == 1) tc_commit(&k_empty[stage]);
+        for (int k = 0; k < 8; ++k) {
+          const uint64_t off = (uint64_t)(((k >> 2) * Cfg::kHalf + (k & 3) * 32) >> 4);
+          tc_mma_ss(tmem + st * 128, a + off, b + off, kIdescQK, k > 0);
         }
-        __syncwarp();
-        return true;
+        tc_commit(&s_full[st]);
+        if (!dual || st == 1) tc_commit(&k_empty[stage]);
       };
-      // O += P V of step i; P lies over the scores, 32 columns for either half's
-      // 64 keys.  Then the stream's next scores, over the probabilities: products
-      // of one thread run in order
-      auto pv = [&](int i, int st) -> bool {
-        const uint32_t tl = n_tile + (dual ? i >> 1 : i), stage = tl & 1;
-        if (!wait(&v_full[stage], (tl >> 1) & 1) || !wait(&p_ready[st], n_step[st] & 1)) return false;
+      // the fragment's first scores of a stream
+      auto begin = [&](int st) -> bool {
+        const uint32_t tl = tile_of(st);
+        const bool ready = wait(lane & 1 ? &k_full[tl & 1] : &q_ready[st],
+                                (lane & 1 ? tl >> 1 : n_q[st]) & 1);
+        n_q[st] += 1;
+        tc_fence_after();
+        if (ready && elect_one()) qk(st, st);
+        __syncwarp();
+        return ready;
+      };
+      // O += P V of step i, P over the scores (32 columns for either half's 64
+      // keys); then the stream's next scores, over P: products of one thread run
+      // in order.  The lanes look at the three barriers of the step at once.
+      auto step = [&](int i, int st) -> bool {
+        const uint32_t tl = tile_of(i), stage = tl & 1, next = tile_of(i + 2);
+        const bool more = i + 2 < steps;
+        uint64_t* bar = &p_ready[st];
+        uint32_t parity = n_step[st];
+        if (lane & 1) {
+          bar = &v_full[stage];
+          parity = tl >> 1;
+        } else if ((lane & 2) && more) {
+          bar = &k_full[next & 1];
+          parity = next >> 1;
+        }
+        if (!wait(bar, parity & 1)) return false;
         n_step[st] += 1;
         tc_fence_after();
         if (elect_one()) {
@@ -857,19 +875,15 @@ __global__ void __launch_bounds__(768, 1)
             tc_mma_ts(tO, tS + (k >> 2) * 64 + (k & 3) * 8, b + (uint64_t)(k * 2048 >> 4), kIdescPV,
                       i > 1 || k > 0);
           if (!dual || st == 1) tc_commit(&v_empty[stage]);
-          if (i + 2 >= steps) tc_commit(&o_last[st]);
+          if (more) qk(i + 2, st);
+          else tc_commit(&o_last[st]);
         }
         __syncwarp();
-        return i + 2 >= steps || qk(i + 2, st);
+        return true;
       };
-      ok = wait(&q_ready[0], n_q[0] & 1) && qk(0, 0);
-      n_q[0] += 1;
-      if (ok && steps > 1) {
-        ok = wait(&q_ready[1], n_q[1] & 1) && qk(1, 1);
-        n_q[1] += 1;
-      }
+      ok = begin(0) && (steps < 2 || begin(1));
 #pragma unroll 1
-      for (int i = 0; ok && i < steps; i += 2) ok = pv(i, 0) && (i + 1 >= steps || pv(i + 1, 1));
+      for (int i = 0; ok && i < steps; i += 2) ok = step(i, 0) && (i + 1 >= steps || step(i + 1, 1));
       n_tile += nt;
       if (ok) frag_done(nf);
     }
