@@ -12,9 +12,9 @@
 // (two partial results, joined by the merge like any others).
 //
 // Warps: 0-7 and 8-15 the softmax of stream 0 and 1 (two threads per row, each
-// with 64 of a tile's 128 keys), 16-19 widen the 8-bit codes to fp16 (exact; TMA
-// writes the fp16 pool's rows into place itself), 20 issues the copies, 21 and
-// 22 the products of a stream each, 23 announces the share's fragments.
+// with 64 of a tile's 128 keys), 16-19 and 20-23 widen the 8-bit codes of K and of
+// V to fp16 (exact; TMA writes the fp16 pool's rows into place itself), 24 issues
+// the copies, 25 the products, 27 announces the share's fragments.
 //
 // The running maximum of a row is only raised when a score passes it by more
 // than 8 (probabilities stay <= 2^8 in fp16), so O is rescaled rarely, by the
@@ -325,8 +325,8 @@ template <int KVT>
 struct UmmaCfg {
   static constexpr bool kWide = KVT == PQKV_KV_FP16;      // rows need no widening
   static constexpr bool kRowScaled = KVT == PQKV_KV_INT8_ROW;
-  static constexpr int kThreads = 768;
-  static constexpr int kRegLaunch = 80;
+  static constexpr int kThreads = 896;
+  static constexpr int kRegLaunch = 72;
   static constexpr long long kWaitCycles = 1ll << 31;     // 1.04 s at 2.07 GHz
   // A row's reference maximum is raised when a score passes it by more than
   // this (log2): probabilities stay <= 2^14, within fp16's 2^16, and the fewer
@@ -342,32 +342,31 @@ struct UmmaCfg {
   static constexpr int kCodeOff = kVOff + 2 * kTile;      // staged codes: slabs of 128 rows
   static constexpr int kSlab = 128 * 128;
   static constexpr int kSlabs = kWide ? 0 : 2;
-  static constexpr int kScOff = kCodeOff + kSlabs * kSlab;  // fp16 row scales: 3 stages of K and V
-  static constexpr int kScBytes = kRowScaled ? 3 * 2 * 128 * 2 : 0;
+  static constexpr int kScOff = kCodeOff + kSlabs * kSlab;  // fp16 row scales: 4 stages of K and V
+  static constexpr int kScBytes = kRowScaled ? 4 * 2 * 128 * 2 : 0;
   static constexpr int kBarOff = kScOff + kScBytes;
   static constexpr int kBars = 4 + 8 + 10 + 8;
   // fragments announced by the scheduling warp: a ring of kFrags
   static constexpr int kFrags = 4;
-  static constexpr int kReaders = kWide ? 18 : 22;         // warps that read them
+  static constexpr int kReaders = kWide ? 18 : 26;         // warps that read them
   static constexpr int kFragOff = kBarOff + kBars * 8 + 8;
-  static constexpr int kSmemBytes = kFragOff + kFrags * (int)sizeof(UmmaFrag) + 1024;
+  static constexpr int kSmemBytes = kFragOff + kFrags * (int)sizeof(UmmaFrag);
   static_assert(kSmemBytes <= 232448, "shared memory of a block");
   // registers per thread of the softmax, widening and issuing warps, of the
-  // 80 * 768 that the block is launched with
-  static constexpr int kRegSoftmax = 88, kRegWiden = 72, kRegIssue = 56;
-  static_assert(4 * kRegSoftmax + kRegWiden + kRegIssue <= 6 * kRegLaunch, "registers of the launch");
+  // 72 * 896 that the block is launched with
+  static constexpr int kRegSoftmax = 88, kRegWiden = 48, kRegIssue = 56;
+  static_assert(4 * kRegSoftmax + 2 * kRegWiden + kRegIssue <= 7 * kRegLaunch,
+                "registers of the launch");
 };
 
 // ---------------------------------------------------------------------------
 // The kernel
 // ---------------------------------------------------------------------------
 template <int KVT>
-__global__ void __launch_bounds__(768, 1)
+__global__ void __launch_bounds__(896, 1)
     shared_umma_kernel(const __grid_constant__ CUtensorMap map, const SharedParams p) {
   using Cfg = UmmaCfg<KVT>;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                             ~uintptr_t(1023));
+  extern __shared__ __align__(1024) uint8_t smem[];       // the swizzle's atoms are 1 KB
   const uint32_t sbase = smem_u32(smem);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Cfg::kBarOff);
   uint64_t* code_full = bars;          // [2] a slab of codes has landed
@@ -409,8 +408,8 @@ __global__ void __launch_bounds__(768, 1)
     *abort_flag = 0;
     fence_barrier_init();
   }
-  if (warp == 21) tmem_alloc_512(tmem_slot);
-  if (warp == 20 && lane == 0) prefetch_tensormap(&map);
+  if (warp == 25) tmem_alloc_512(tmem_slot);
+  if (warp == 24 && lane == 0) prefetch_tensormap(&map);
   grid_dependency_wait();
   grid_dependents_launch();
   tc_fence_before();
@@ -544,7 +543,7 @@ __global__ void __launch_bounds__(768, 1)
         if (warp_live) {
           // 64 fp16 scales of K, of V 256 bytes on
           const uint32_t sc = sbase + Cfg::kScOff + half * 128 +
-                              (n_tile + (dual ? i : 2 * i + st)) % 3 * 512;
+                              (n_tile + (dual ? i : 2 * i + st)) % 4 * 512;
           uint32_t s[32], s2[32];
           scores(s2, 32, valid, sc);
           const float hi = max32(s2);
@@ -662,88 +661,89 @@ __global__ void __launch_bounds__(768, 1)
       }
       tc_fence_before();
     }
-  } else if (warp < 20) {
+  } else if (warp < 24) {
     // ================= widen the codes =================
     regs_down<Cfg::kRegWiden>();
     if constexpr (!Cfg::kWide) {
-      const int wt = tid - 512;
-      uint32_t n_slab = 0, n_tile = 0;
+      const int kv = (warp - 16) >> 2, wt = (tid - 512) & 127;       // K or V
+      uint64_t *full = kv ? v_full : k_full, *empty = kv ? v_empty : k_empty;
+      const uint32_t src = sbase + Cfg::kCodeOff + kv * Cfg::kSlab;
+      uint32_t n_tile = 0;
       bool ok = true;
+      const UmmaFrag* f;
       // INT8_ROW: K and V row scale (fp16 bits) of this thread's token of key
       // tile u; 0 behind the prefix and for pages outside the pool
-      const UmmaFrag* f;
       auto row_scale = [&](int u) -> ushort2 {
         const int pg = f->page0 + u * kUmmaPages + wt / kPageSize, rr = wt % kPageSize;
         if (pg >= f->pages) return make_ushort2(0, 0);
         const int id = __ldg(p.block_table + (int64_t)f->seq0 * p.bt_stride + pg);
         if (id < 0 || (int64_t)id >= p.num_pages) return make_ushort2(0, 0);
-        const uint16_t* src = reinterpret_cast<const uint16_t*>(p.k_scale) +
-                              (((int64_t)id * H + f->h) * 8 + (rr & 7)) * 4 + (rr >> 3);
-        return make_ushort2(__ldg(src), __ldg(src + 2));
+        const uint16_t* from = reinterpret_cast<const uint16_t*>(p.k_scale) +
+                               (((int64_t)id * H + f->h) * 8 + (rr & 7)) * 4 + (rr >> 3);
+        return make_ushort2(__ldg(from), __ldg(from + 2));
       };
       ushort2 ahead = make_ushort2(0, 0);
       for (uint32_t n = 0; ok; ++n) {
         if (!frag_at(n, f)) break;
         const int nt = f->nt;
         if (nt == 0) break;
-        for (int u = 0; ok && u < nt; ++u, ++n_tile) {
+#pragma unroll 1
+        for (int u = 0; u < nt; ++u, ++n_tile) {
+          const uint32_t stage = n_tile & 1;
+          if constexpr (Cfg::kRowScaled)
+            if (kv == 0 && u == 0) ahead = row_scale(0);
+          // the codes have landed and the stage is free: a barrier per lane
+          const bool odd = (lane & 1) && n_tile >= 2;
+          if (!wait(odd ? empty + stage : &code_full[kv], (odd ? (n_tile >> 1) + 1 : n_tile) & 1)) {
+            ok = false;
+            break;
+          }
           if constexpr (Cfg::kRowScaled) {
             // The tile's fp16 row scales, a token per thread, read a tile ahead.
-            // Stage n % 3 was last read by the softmax of tile n - 3, whose
-            // product with V the V stage's release for tile n - 1 came after.
-            uint16_t* dst = reinterpret_cast<uint16_t*>(smem + Cfg::kScOff + n_tile % 3 * 512);
-            if (u == 0) ahead = row_scale(0);
-            dst[wt] = ahead.x;
-            dst[128 + wt] = ahead.y;
-            if (u + 1 < nt) ahead = row_scale(u + 1);
+            // Stage n % 4 was last read by the softmax of tile n - 4, whose
+            // probabilities went into their product before the scores of tile
+            // n - 2, waited for above, were formed.
+            if (kv == 0) {
+              uint16_t* to = reinterpret_cast<uint16_t*>(smem + Cfg::kScOff + n_tile % 4 * 512);
+              to[wt] = ahead.x;
+              to[128 + wt] = ahead.y;
+              if (u + 1 < nt) ahead = row_scale(u + 1);
+            }
           }
-#pragma unroll 1
-          for (int kv = 0; kv < 2; ++kv, ++n_slab) {
-            const int slot = n_slab % Cfg::kSlabs, stage = n_tile & 1;
-            uint64_t* empty = (kv ? v_empty : k_empty) + stage;
-            // both at once, a barrier per lane
-            const bool odd = (lane & 1) && n_tile >= 2;
-            if (!wait(odd ? empty : &code_full[slot],
-                      (odd ? (n_tile >> 1) + 1 : n_slab / Cfg::kSlabs) & 1)) {
-              ok = false;
-              break;
-            }
-            const uint32_t src = sbase + Cfg::kCodeOff + slot * Cfg::kSlab;
-            const uint32_t dst = sbase + (kv ? Cfg::kVOff : Cfg::kKOff) + stage * Cfg::kTile;
+          const uint32_t dst = sbase + (kv ? Cfg::kVOff : Cfg::kKOff) + stage * Cfg::kTile;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const int idx = i * 128 + wt, row = idx >> 3, j = idx & 7;
-              const uint4 c = lds128u(src + row * 128 + ((j ^ (row & 7)) << 4));
-              uint32_t w[8];
-              dequant_word<KVT>(c.x, w[0], w[1]);
-              dequant_word<KVT>(c.y, w[2], w[3]);
-              dequant_word<KVT>(c.z, w[4], w[5]);
-              dequant_word<KVT>(c.w, w[6], w[7]);
-              // the row's 16 values are chunks 2 (j & 3) and the next of half
-              // j >> 2; the halves' lanes take the two in opposite order, so
-              // that a row's eight lanes store to eight different chunks
-              const uint32_t at = dst + (j >> 2) * Cfg::kHalf + row * 128;
-              const int c0 = 2 * (j & 3) + (j >> 2), c1 = c0 ^ 1;
-              const bool up = j >> 2;
-              sts128(at + ((c0 ^ (row & 7)) << 4), up ? w[4] : w[0], up ? w[5] : w[1],
-                     up ? w[6] : w[2], up ? w[7] : w[3]);
-              sts128(at + ((c1 ^ (row & 7)) << 4), up ? w[0] : w[4], up ? w[1] : w[5],
-                     up ? w[2] : w[6], up ? w[3] : w[7]);
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-              mbar_arrive((kv ? v_full : k_full) + stage);
-              mbar_arrive(&code_empty[slot]);
-            }
+          for (int i = 0; i < 8; ++i) {
+            const int idx = i * 128 + wt, row = idx >> 3, j = idx & 7;
+            const uint4 c = lds128u(src + row * 128 + ((j ^ (row & 7)) << 4));
+            uint32_t w[8];
+            dequant_word<KVT>(c.x, w[0], w[1]);
+            dequant_word<KVT>(c.y, w[2], w[3]);
+            dequant_word<KVT>(c.z, w[4], w[5]);
+            dequant_word<KVT>(c.w, w[6], w[7]);
+            // the row's 16 values are chunks 2 (j & 3) and the next of half j >> 2;
+            // the halves' lanes take the two in opposite order, so that a row's
+            // eight lanes store to eight different chunks
+            const uint32_t at = dst + (j >> 2) * Cfg::kHalf + row * 128;
+            const int c0 = 2 * (j & 3) + (j >> 2), c1 = c0 ^ 1;
+            const bool up = j >> 2;
+            sts128(at + ((c0 ^ (row & 7)) << 4), up ? w[4] : w[0], up ? w[5] : w[1],
+                   up ? w[6] : w[2], up ? w[7] : w[3]);
+            sts128(at + ((c1 ^ (row & 7)) << 4), up ? w[0] : w[4], up ? w[1] : w[5],
+                   up ? w[2] : w[6], up ? w[3] : w[7]);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&full[stage]);
+            mbar_arrive(&code_empty[kv]);
           }
         }
-        frag_done(n);
+        if (ok) frag_done(n);
       }
     }
   } else {
   regs_down<Cfg::kRegIssue>();
-  if (warp == 20) {
+  if (warp == 24) {
     // ================= copies =================
     uint32_t n = 0, n_tile = 0;      // copies (K or V of a key tile) and key tiles so far
     bool ok = true;
@@ -783,14 +783,13 @@ __global__ void __launch_bounds__(768, 1)
             }
             ++n;
           } else {
-            const int slot = n % Cfg::kSlabs;
-            ok = n < Cfg::kSlabs || wait(&code_empty[slot], ((n / Cfg::kSlabs) + 1) & 1);
+            ok = n_tile < 1 || wait(&code_empty[kv], (n_tile + 1) & 1);
             if (!ok) break;
-            if (lane == 0) mbar_arrive_expect_tx(&code_full[slot], Cfg::kSlab);
+            if (lane == 0) mbar_arrive_expect_tx(&code_full[kv], Cfg::kSlab);
             __syncwarp();
             if (lane < kUmmaPages)
-              tma_load_5d(sbase + Cfg::kCodeOff + slot * Cfg::kSlab + lane * 2048, &map,
-                          &code_full[slot], 0, 0, kv * kPageSize, h, id);
+              tma_load_5d(sbase + Cfg::kCodeOff + kv * Cfg::kSlab + lane * 2048, &map,
+                          &code_full[kv], 0, 0, kv * kPageSize, h, id);
             ++n;
           }
         }
@@ -804,86 +803,103 @@ __global__ void __launch_bounds__(768, 1)
         for (uint32_t i = n > 4 ? n - 4 : 0; i < n; ++i)     // copy i: K or V of tile i / 2
           (void)mbar_wait((i & 1 ? v_full : k_full) + ((i >> 1) & 1), (i >> 2) & 1);
       } else {
-        for (uint32_t i = n > Cfg::kSlabs ? n - Cfg::kSlabs : 0; i < n; ++i)
-          (void)mbar_wait(&code_full[i % Cfg::kSlabs], (i / Cfg::kSlabs) & 1);
+        for (uint32_t i = n > 2 ? n - 2 : 0; i < n; ++i)     // K or V of tile i / 2
+          (void)mbar_wait(&code_full[i & 1], (i >> 1) & 1);
       }
     }
-  } else if (warp == 21) {
+  } else if (warp == 25) {
     // ================= products =================
     // The streams take turns: a stream's product with V and its next scores, then
     // the other's.  Issued by a warp each, the streams' products mixed, both had
     // their scores at the same time and then the tensor cores idle.
-    uint32_t n_tile = 0, n_q[2] = {0, 0}, n_step[2] = {0, 0};
+    // counters of stream 0 and 1: fragments begun, steps
+    uint32_t n_tile = 0, q0 = 0, q1 = 0, s0 = 0, s1 = 0;
     bool ok = true;
     const uint64_t q_desc = tc_desc(sbase + Cfg::kQOff, 16), k_desc = tc_desc(sbase + Cfg::kKOff, 16),
                    v_desc = tc_desc(sbase + Cfg::kVOff, Cfg::kHalf);
+    // S = Q K^T of stream st on K stage `stage` (one thread)
+    auto qk = [&](auto stream, uint32_t stage, bool release) {
+      constexpr int st = decltype(stream)::value;
+      const uint64_t a = q_desc + (uint64_t)(st * (Cfg::kTile >> 4)),
+                     b = k_desc + (uint64_t)(stage * (Cfg::kTile >> 4));
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const uint64_t off = (uint64_t)(((k >> 2) * Cfg::kHalf + (k & 3) * 32) >> 4);
+        tc_mma_ss(tmem + st * 128, a + off, b + off, kIdescQK, k > 0);
+      }
+      tc_commit(&s_full[st]);
+      if (release) tc_commit(&k_empty[stage]);
+    };
+    // a stream's first scores of a fragment, on key tile tl
+    auto begin = [&](auto stream, uint32_t tl, uint32_t& nq, bool release) -> bool {
+      constexpr int st = decltype(stream)::value;
+      if (!wait(lane & 1 ? &k_full[tl & 1] : &q_ready[st], (lane & 1 ? tl >> 1 : nq) & 1))
+        return false;
+      nq += 1;
+      tc_fence_after();
+      if (elect_one()) qk(stream, tl & 1, release);
+      __syncwarp();
+      return true;
+    };
+    // O += P V on key tile tl, P over the scores (32 columns for either half's 64
+    // keys); then the stream's next scores (key tile `next`), over P: products of
+    // one thread run in order.  The lanes look at the three barriers at once.
+    auto step = [&](auto stream, uint32_t tl, uint32_t next, bool more, bool acc, bool release,
+                    uint32_t& ns) -> bool {
+      constexpr int st = decltype(stream)::value;
+      const uint32_t stage = tl & 1;
+      uint64_t* bar = &p_ready[st];
+      uint32_t parity = ns;
+      if (lane & 1) {
+        bar = &v_full[stage];
+        parity = tl >> 1;
+      } else if ((lane & 2) && more) {
+        bar = &k_full[next & 1];
+        parity = next >> 1;
+      }
+      if (!wait(bar, parity & 1)) return false;
+      ns += 1;
+      tc_fence_after();
+      if (elect_one()) {
+        const uint64_t b = v_desc + (uint64_t)(stage * (Cfg::kTile >> 4));
+        const uint32_t tS = tmem + st * 128, tO = tmem + 256 + st * 128;
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          tc_mma_ts(tO, tS + (k >> 2) * 64 + (k & 3) * 8, b + (uint64_t)(k * 2048 >> 4), kIdescPV,
+                    acc || k > 0);
+        if (release) tc_commit(&v_empty[stage]);
+        if (more) qk(stream, next & 1, release);
+        else tc_commit(&o_last[st]);
+      }
+      __syncwarp();
+      return true;
+    };
+    const std::integral_constant<int, 0> A;
+    const std::integral_constant<int, 1> B;
     const UmmaFrag* f;
     for (uint32_t nf = 0; ok; ++nf) {
       if (!(ok = frag_at(nf, f))) break;
       const int nt = __shfl_sync(0xffffffffu, f->nt, 0);
-      const bool dual = __shfl_sync(0xffffffffu, f->dual, 0);
       if (nt == 0) break;
-      const int steps = dual ? 2 * nt : nt;              // step i: stream i & 1
-      auto tile_of = [&](int i) -> uint32_t { return n_tile + (dual ? i >> 1 : i); };
-      // S = Q K^T of step i on its key tile (one thread)
-      auto qk = [&](int i, int st) {
-        const uint32_t stage = tile_of(i) & 1;
-        const uint64_t a = q_desc + (uint64_t)(st * (Cfg::kTile >> 4)),
-                       b = k_desc + (uint64_t)(stage * (Cfg::kTile >> 4));
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const uint64_t off = (uint64_t)(((k >> 2) * Cfg::kHalf + (k & 3) * 32) >> 4);
-          tc_mma_ss(tmem + st * 128, a + off, b + off, kIdescQK, k > 0);
-        }
-        tc_commit(&s_full[st]);
-        if (!dual || st == 1) tc_commit(&k_empty[stage]);
-      };
-      // the fragment's first scores of a stream
-      auto begin = [&](int st) -> bool {
-        const uint32_t tl = tile_of(st);
-        const bool ready = wait(lane & 1 ? &k_full[tl & 1] : &q_ready[st],
-                                (lane & 1 ? tl >> 1 : n_q[st]) & 1);
-        n_q[st] += 1;
-        tc_fence_after();
-        if (ready && elect_one()) qk(st, st);
-        __syncwarp();
-        return ready;
-      };
-      // O += P V of step i, P over the scores (32 columns for either half's 64
-      // keys); then the stream's next scores, over P: products of one thread run
-      // in order.  The lanes look at the three barriers of the step at once.
-      auto step = [&](int i, int st) -> bool {
-        const uint32_t tl = tile_of(i), stage = tl & 1, next = tile_of(i + 2);
-        const bool more = i + 2 < steps;
-        uint64_t* bar = &p_ready[st];
-        uint32_t parity = n_step[st];
-        if (lane & 1) {
-          bar = &v_full[stage];
-          parity = tl >> 1;
-        } else if ((lane & 2) && more) {
-          bar = &k_full[next & 1];
-          parity = next >> 1;
-        }
-        if (!wait(bar, parity & 1)) return false;
-        n_step[st] += 1;
-        tc_fence_after();
-        if (elect_one()) {
-          const uint64_t b = v_desc + (uint64_t)(stage * (Cfg::kTile >> 4));
-          const uint32_t tS = tmem + st * 128, tO = tmem + 256 + st * 128;
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            tc_mma_ts(tO, tS + (k >> 2) * 64 + (k & 3) * 8, b + (uint64_t)(k * 2048 >> 4), kIdescPV,
-                      i > 1 || k > 0);
-          if (!dual || st == 1) tc_commit(&v_empty[stage]);
-          if (more) qk(i + 2, st);
-          else tc_commit(&o_last[st]);
-        }
-        __syncwarp();
-        return true;
-      };
-      ok = begin(0) && (steps < 2 || begin(1));
+      if (__shfl_sync(0xffffffffu, f->dual, 0)) {
+        // both streams on every key tile
+        ok = begin(A, n_tile, q0, false) && begin(B, n_tile, q1, true);
 #pragma unroll 1
-      for (int i = 0; ok && i < steps; i += 2) ok = step(i, 0) && (i + 1 >= steps || step(i + 1, 1));
+        for (int u = 0; ok && u < nt; ++u) {
+          const uint32_t tl = n_tile + u;
+          ok = step(A, tl, tl + 1, u + 1 < nt, u > 0, false, s0) &&
+               step(B, tl, tl + 1, u + 1 < nt, u > 0, true, s1);
+        }
+      } else {
+        // the even key tiles are stream 0's, the odd ones stream 1's
+        ok = begin(A, n_tile, q0, true) && (nt < 2 || begin(B, n_tile + 1, q1, true));
+#pragma unroll 1
+        for (int u = 0; ok && u < nt; u += 2) {
+          const uint32_t tl = n_tile + u;
+          ok = step(A, tl, tl + 2, u + 2 < nt, u > 0, true, s0) &&
+               (u + 1 >= nt || step(B, tl + 1, tl + 3, u + 3 < nt, u > 0, true, s1));
+        }
+      }
       n_tile += nt;
       if (ok) frag_done(nf);
     }
@@ -891,7 +907,7 @@ __global__ void __launch_bounds__(768, 1)
       if (elect_one()) tc_commit(drain);
       (void)mbar_wait(drain, 0);
     }
-  } else if (warp == 22) {
+  } else if (warp == 26) {
     // ================= (no role) =================
   } else {
     // ================= the share's fragments =================
@@ -917,7 +933,7 @@ __global__ void __launch_bounds__(768, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 21) tmem_free_512(tmem);
+  if (warp == 25) tmem_free_512(tmem);
 }
 
 template <int KVT>
@@ -927,7 +943,7 @@ cudaError_t launch_shared_umma_t(const SharedParams& p, const CUtensorMap& map,
   static std::atomic<uint64_t> done{0};
   const cudaError_t e = opt_in_smem(shared_umma_kernel<KVT>, Cfg::kSmemBytes, done);
   if (e != cudaSuccess) return e;
-  // the register split needs the 80 registers per thread that the launch
+  // the register split needs the 72 registers per thread that the launch
   // bounds allow; a build that used fewer would wait for them forever
   static const int regs = [] {
     cudaFuncAttributes at;
