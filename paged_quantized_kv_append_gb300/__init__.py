@@ -16,6 +16,7 @@ page and kv-head a 16-token K tile followed by a V tile -- of uint8 codes
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -49,6 +50,8 @@ _lib_lock = threading.Lock()
 def load_library(path: str | None = None):
     """Load libpqkv.so (built in-tree by ``python -m paged_quantized_kv_append_gb300.build``)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lib_lock:
         if _lib is not None:
             return _lib
@@ -420,10 +423,46 @@ def lse_merge(parts_o, parts_lse, out, out_lse=None, stream=None):
     return out
 
 
+@functools.lru_cache(maxsize=256)
 def shared_prefix_workspace_size(num_seqs, num_groups, q_len, num_q_heads, num_kv_heads) -> int:
     """Bytes of workspace of paged_attention_shared_prefix (0: sizes it refuses)."""
     return int(load_library().pqkv_paged_attention_shared_prefix_workspace_size(
         num_seqs, num_groups, q_len, num_q_heads, num_kv_heads, HEAD_DIM))
+
+
+def _refuse(name, x, dtype, shape, idx):
+    raise ValueError("%s must be a contiguous %s tensor of shape %s on cuda:%d, got %s %s on %s%s" % (
+        name, dtype, list(shape), idx, x.dtype, list(x.shape), x.device,
+        "" if x.is_contiguous() else ", not contiguous"))
+
+
+def _check_ints(idx, dtype, named):
+    """Every (name, tensor, shape) a contiguous tensor of this dtype on cuda:idx."""
+    for name, x, shape in named:
+        if (x.dtype is not dtype or x.shape != shape or not x.is_contiguous()
+                or x.get_device() != idx):
+            _refuse(name, x, dtype, shape, idx)
+
+
+def _cuda_index(name, x):
+    """The device index of a CUDA tensor (the host's cost per call counts: a
+    step's bookkeeping is a few microseconds of GPU time)."""
+    idx = x.get_device()
+    if idx < 0:
+        raise ValueError("%s must be a CUDA tensor, got %s" % (name, x.device))
+    return idx
+
+
+def _call_on(idx, stream, fn, *args):
+    """fn(*args, stream) with device idx current."""
+    if stream is None:
+        raw = torch._C._cuda_getCurrentRawStream(idx)
+    else:
+        raw = stream.cuda_stream
+    if torch.cuda.current_device() == idx:
+        return fn(*args, raw)
+    with torch.cuda.device(idx):
+        return fn(*args, raw)
 
 
 def paged_attention_shared_prefix(q, pages, block_table, seq_lens, group_offsets, prefix_lens,
@@ -442,71 +481,44 @@ def paged_attention_shared_prefix(q, pages, block_table, seq_lens, group_offsets
     of shared_prefix_workspace_size() bytes may be given instead."""
     kd = _dtype_id(kv_dtype)
     _check_pages(pages, kd)
-    H = pages.shape[1]
-    dev = pages.device
-    if q.dtype != torch.float16 or q.dim() != 3 or q.shape[2] != HEAD_DIM or not q.is_contiguous():
-        raise ValueError("q must be contiguous fp16 [num_seqs*q_len, Hq, 128]")
-    if out.shape != q.shape or out.dtype != torch.float16 or not out.is_contiguous():
-        raise ValueError("out must be contiguous fp16 shaped like q")
-    i32 = torch.int32
-    _int_tensor("seq_lens", seq_lens, i32, (None,), dev)
-    B = seq_lens.shape[0]
-    _int_tensor("block_table", block_table, i32, (B, None), dev)
-    _int_tensor("prefix_lens", prefix_lens, i32, (None,), dev)
-    M = prefix_lens.shape[0]
-    _int_tensor("group_offsets", group_offsets, i32, (M + 1,), dev)
-    if q.shape[0] != B * q_len:
-        raise ValueError("q has %d rows, expected num_seqs*q_len = %d" % (q.shape[0], B * q_len))
+    idx = pages.get_device()
+    N, H = pages.shape[0], pages.shape[1]
+    B, M = seq_lens.shape[0], prefix_lens.shape[0]
     Hq = q.shape[1]
-    sph = 0
+    rows = (B * q_len, Hq, HEAD_DIM)
+    _check_ints(idx, torch.float16, (("q", q, rows), ("out", out, rows)))
+    W = block_table.shape[-1]
+    _check_ints(idx, torch.int32, (("seq_lens", seq_lens, (B,)), ("block_table", block_table, (B, W)),
+                                   ("prefix_lens", prefix_lens, (M,)),
+                                   ("group_offsets", group_offsets, (M + 1,))))
+    sph, ks, vs = 0, None, None
     if kd in _SCALED:
         sph = _check_scale(k_scale, H, "k_scale")
         if _check_scale(v_scale, H, "v_scale") != sph:
             raise ValueError("k_scale and v_scale must have the same shape")
-        _on_device(dev, k_scale=k_scale, v_scale=v_scale)
-    else:
-        k_scale = v_scale = None
-    _on_device(dev, q=q, out=out, workspace=workspace)
-    _check_status(status, dev)
-    lib = load_library()
-    with torch.cuda.device(dev):
-        if workspace is None:
-            need = shared_prefix_workspace_size(B, M, q_len, Hq, H)
+        if k_scale.get_device() != idx or v_scale.get_device() != idx:
+            raise ValueError("k_scale and v_scale must be on cuda:%d" % idx)
+        ks, vs = k_scale.data_ptr(), v_scale.data_ptr()
+    if status is not None:
+        _check_status(status, pages.device)
+    if workspace is None:
+        need = shared_prefix_workspace_size(B, M, q_len, Hq, H)
+        if stream is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=pages.device)
+        else:                            # owned by the stream it is used on
             with torch.cuda.stream(stream):
-                workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-        rc = lib.pqkv_paged_attention_shared_prefix(
-            _ptr(q), _ptr(out), _ptr(pages), pages.shape[0], _ptr(block_table),
-            block_table.shape[1], _ptr(seq_lens), B, _ptr(group_offsets), _ptr(prefix_lens), M,
-            q_len, Hq, H, HEAD_DIM, PAGE_SIZE, kd, _ptr(k_scale), _ptr(v_scale), sph, max_seq_len,
-            max_prefix_len, _ptr(workspace), workspace.numel() * workspace.element_size(),
-            _ptr(status), _stream(q, stream))
-    _check(rc, "paged_attention_shared_prefix")
+                workspace = torch.empty(need, dtype=torch.uint8, device=pages.device)
+    elif workspace.get_device() != idx:
+        raise ValueError("workspace must be on cuda:%d, got %s" % (idx, workspace.device))
+    rc = _call_on(
+        idx, stream, load_library().pqkv_paged_attention_shared_prefix, q.data_ptr(),
+        out.data_ptr(), pages.data_ptr(), N, block_table.data_ptr(), W, seq_lens.data_ptr(), B,
+        group_offsets.data_ptr(), prefix_lens.data_ptr(), M, q_len, Hq, H, HEAD_DIM, PAGE_SIZE, kd,
+        ks, vs, sph, max_seq_len, max_prefix_len, workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), None if status is None else status.data_ptr())
+    if rc:
+        _check(rc, "paged_attention_shared_prefix")
     return out
-
-
-def _int_tensor(name, x, dtype, shape, dev):
-    """A contiguous integer CUDA tensor of this shape (None: any length) on dev."""
-    if x.dtype != dtype or x.dim() != len(shape) or not x.is_contiguous() or x.device != dev or \
-            any(n is not None and m != n for m, n in zip(x.shape, shape)):
-        raise ValueError("%s must be a contiguous %s tensor %s on %s, got %s %s on %s" % (
-            name, dtype, list(shape), dev, x.dtype, list(x.shape), x.device))
-
-
-def _table_args(seq_lens, block_table, free_pages, free_count, seq_lens_out, free_count_out,
-                status):
-    dev = block_table.device
-    if dev.type != "cuda":
-        raise ValueError("block_table must be a CUDA tensor")
-    i32 = torch.int32
-    _int_tensor("block_table", block_table, i32, (None, None), dev)
-    B = block_table.shape[0]
-    _int_tensor("seq_lens", seq_lens, i32, (B,), dev)
-    _int_tensor("seq_lens_out", seq_lens_out, i32, (B,), dev)
-    _int_tensor("free_pages", free_pages, i32, (None,), dev)
-    _int_tensor("free_count", free_count, i32, (1,), dev)
-    _int_tensor("free_count_out", free_count_out, i32, (1,), dev)
-    _check_status(status, dev)
-    return dev, B
 
 
 def extend_block_tables(seq_lens, new_tokens, block_table, free_pages, free_count, num_pages,
@@ -523,23 +535,33 @@ def extend_block_tables(seq_lens, new_tokens, block_table, free_pages, free_coun
     ``slot_mapping``, keeps its length, and its tokens get slot -1 (reported in
     ``status``).  ``seq_lens_out`` / ``free_count_out`` may be the inputs
     themselves.  Returns slot_mapping."""
-    dev, B = _table_args(seq_lens, block_table, free_pages, free_count, seq_lens_out,
-                         free_count_out, status)
-    _int_tensor("new_tokens", new_tokens, torch.int32, (B,), dev)
-    _int_tensor("slot_mapping", slot_mapping, torch.int64, (None,), dev)
-    T = slot_mapping.shape[0]
+    idx = _cuda_index("block_table", block_table)
+    B, W = seq_lens.shape[0], block_table.shape[-1]
+    T, cap = slot_mapping.shape[0], free_pages.shape[0]
+    row, one = (B,), (1,)
+    _check_ints(idx, torch.int32, (
+        ("block_table", block_table, (B, W)), ("seq_lens", seq_lens, row),
+        ("new_tokens", new_tokens, row), ("free_pages", free_pages, (cap,)),
+        ("free_count", free_count, one), ("seq_lens_out", seq_lens_out, row),
+        ("free_count_out", free_count_out, one)))
+    _check_ints(idx, torch.int64, (("slot_mapping", slot_mapping, (T,)),))
+    pos = off = None
     if positions is not None:
-        _int_tensor("positions", positions, torch.int32, (T,), dev)
+        _check_ints(idx, torch.int32, (("positions", positions, (T,)),))
+        pos = positions.data_ptr()
     if token_offsets is not None:
-        _int_tensor("token_offsets", token_offsets, torch.int32, (B + 1,), dev)
-    lib = load_library()
-    with torch.cuda.device(dev):
-        rc = lib.pqkv_extend_block_tables(
-            _ptr(seq_lens), _ptr(new_tokens), B, _ptr(block_table), block_table.shape[1],
-            _ptr(free_pages), _ptr(free_count), free_pages.shape[0], num_pages, PAGE_SIZE,
-            _ptr(seq_lens_out), _ptr(free_count_out), _ptr(slot_mapping), _ptr(positions), T,
-            _ptr(token_offsets), _ptr(status), _stream(block_table, stream))
-    _check(rc, "extend_block_tables")
+        _check_ints(idx, torch.int32, (("token_offsets", token_offsets, (B + 1,)),))
+        off = token_offsets.data_ptr()
+    if status is not None:
+        _check_status(status, block_table.device)
+    rc = _call_on(
+        idx, stream, load_library().pqkv_extend_block_tables, seq_lens.data_ptr(),
+        new_tokens.data_ptr(), B, block_table.data_ptr(), W, free_pages.data_ptr(),
+        free_count.data_ptr(), cap, num_pages, PAGE_SIZE, seq_lens_out.data_ptr(),
+        free_count_out.data_ptr(), slot_mapping.data_ptr(), pos, T, off,
+        None if status is None else status.data_ptr())
+    if rc:
+        _check(rc, "extend_block_tables")
     return slot_mapping
 
 
@@ -552,19 +574,27 @@ def truncate_block_tables(seq_lens, keep_lens, block_table, free_pages, free_cou
     another request -- a shared prefix -- and stay.  The block table is not
     changed.  ``seq_lens_out`` / ``free_count_out`` may be the inputs
     themselves.  Returns seq_lens_out."""
-    dev, B = _table_args(seq_lens, block_table, free_pages, free_count, seq_lens_out,
-                         free_count_out, status)
-    _int_tensor("keep_lens", keep_lens, torch.int32, (B,), dev)
+    idx = _cuda_index("block_table", block_table)
+    B, W, cap = seq_lens.shape[0], block_table.shape[-1], free_pages.shape[0]
+    row, one = (B,), (1,)
+    _check_ints(idx, torch.int32, (
+        ("block_table", block_table, (B, W)), ("seq_lens", seq_lens, row),
+        ("keep_lens", keep_lens, row), ("free_pages", free_pages, (cap,)),
+        ("free_count", free_count, one), ("seq_lens_out", seq_lens_out, row),
+        ("free_count_out", free_count_out, one)))
+    owned = None
     if owned_pages is not None:
-        _int_tensor("owned_pages", owned_pages, torch.int32, (B,), dev)
-    lib = load_library()
-    with torch.cuda.device(dev):
-        rc = lib.pqkv_truncate_block_tables(
-            _ptr(seq_lens), _ptr(keep_lens), _ptr(owned_pages), B, _ptr(block_table),
-            block_table.shape[1], _ptr(free_pages), _ptr(free_count), free_pages.shape[0],
-            PAGE_SIZE, _ptr(seq_lens_out), _ptr(free_count_out), _ptr(status),
-            _stream(block_table, stream))
-    _check(rc, "truncate_block_tables")
+        _check_ints(idx, torch.int32, (("owned_pages", owned_pages, row),))
+        owned = owned_pages.data_ptr()
+    if status is not None:
+        _check_status(status, block_table.device)
+    rc = _call_on(
+        idx, stream, load_library().pqkv_truncate_block_tables, seq_lens.data_ptr(),
+        keep_lens.data_ptr(), owned, B, block_table.data_ptr(), W, free_pages.data_ptr(),
+        free_count.data_ptr(), cap, PAGE_SIZE, seq_lens_out.data_ptr(), free_count_out.data_ptr(),
+        None if status is None else status.data_ptr())
+    if rc:
+        _check(rc, "truncate_block_tables")
     return seq_lens_out
 
 
