@@ -151,63 +151,122 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedP
   if (tid == 0) p.plan.spre[B] = total_s;
 }
 
-// One warp per output row: the row's fragments, prefix first, folded in with a
-// running maximum (a fixed order, so the result is deterministic).
+// kWarps warps per output row.  The row's fragments, the prefix's first, are dealt
+// to the row's warps; a warp loads four at once and folds them in with a running
+// maximum, and the warps' results are joined in order (a fixed order throughout,
+// so the result is deterministic).  A lane owns four dims.
+template <int kWarps>
 __global__ void __launch_bounds__(256) shared_merge_kernel(const SharedParams p, int scaled) {
+  __shared__ float4 s_acc[kWarps > 1 ? 8 : 1][32];
+  __shared__ float2 s_ml[8];
   grid_dependency_wait();
   grid_dependents_launch();
-  const int lane = threadIdx.x & 31;
-  const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = warp % kWarps;
+  const int64_t row = (int64_t)blockIdx.x * (8 / kWarps) + warp / kWarps;
   const int H = p.num_kv_heads, M = p.num_groups;
-  if (row >= (int64_t)p.num_seqs * p.q_len * p.num_q_heads) return;
-  const int hq = (int)(row % p.num_q_heads);
-  const int tok = (int)(row / p.num_q_heads);
-  const int s = tok / p.q_len, i = tok % p.q_len, h = hq / p.group, gq = hq % p.group;
-  const int g = p.plan.group[s];
+  const bool in = row < (int64_t)p.num_seqs * p.q_len * p.num_q_heads;
   float top = kNoScore, l = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  auto add = [&](const float* o, float m, float lw, int RP, int64_t slot, int r) {
-    const float4 v = __ldg(reinterpret_cast<const float4*>(o + (slot * RP + r) * kHeadDim) + lane);
-    const float Mn = fmaxf(top, m);
-    const float f0 = ex2(top - Mn), f1 = ex2(m - Mn);
-    l = l * f0 + lw * f1;
-    acc.x = acc.x * f0 + v.x * f1;
-    acc.y = acc.y * f0 + v.y * f1;
-    acc.z = acc.z * f0 + v.z * f1;
-    acc.w = acc.w * f0 + v.w * f1;
-    top = Mn;
-  };
-  auto add_prefix = [&](int64_t slot, int r) {
-    const float* ml = p.pre_ml + slot * 3 * p.pre_rp + r;
-    add(p.pre_o, __ldg(ml), __ldg(ml + p.pre_rp) + __ldg(ml + 2 * p.pre_rp), p.pre_rp, slot, r);
-  };
-  auto add_private = [&](int64_t slot, int r) {
-    const float* ml = p.suf_ml + slot * 2 * p.suf_rp + r;
-    add(p.suf_o, __ldg(ml), __ldg(ml + p.suf_rp), p.suf_rp, slot, r);
-  };
-  const int np = p.plan.gpages(M)[g];
-  if (np > 0) {
-    const int nrows = (p.plan.goff()[g + 1] - p.plan.goff()[g]) * p.rows;
-    const int R = (s - p.plan.goff()[g]) * p.rows + i * p.group + gq;
-    const int rt = R / kUmmaRows, r = R % kUmmaRows, T = (np + kUmmaPages - 1) / kUmmaPages;
-    const bool dual = nrows - rt * kUmmaRows > 128;
-    const int w = dual ? 2 : 1, nt = p.plan.gtiles(M)[g + 1] - p.plan.gtiles(M)[g];
-    const int64_t a = (int64_t)p.plan.gcost(M)[g] * H +
-                      (int64_t)h * (p.plan.gcost(M)[g + 1] - p.plan.gcost(M)[g]) + (int64_t)rt * 2 * T;
-    const int64_t seg = (int64_t)p.plan.gtiles(M)[g] * H + h * nt + rt;
-    const Shares sh((int64_t)p.plan.gcost(M)[M] * H, p.pre_workers);
-    const int c1 = sh.owner(a + (int64_t)w * (T - 1));
-    for (int c = sh.owner(a); c <= c1; ++c) {
-      add_prefix(seg + c, r);
-      if (!dual) add_prefix(seg + c, r + p.pre_rp / 2);
+  int h = 0;
+  if (in) {
+    const int hq = (int)(row % p.num_q_heads);
+    const int tok = (int)(row / p.num_q_heads);
+    const int s = tok / p.q_len, i = tok % p.q_len, gq = hq % p.group;
+    h = hq / p.group;
+    const int g = p.plan.group[s];
+    // -- the prefix's fragments: CTAs c0 .. c0 + n_pre / per - 1, `per` results each
+    const int np = p.plan.gpages(M)[g];
+    int n_pre = 0, per = 1, pre_r = 0;
+    int64_t pre_slot = 0;
+    if (np > 0) {
+      const int first = p.plan.goff()[g], tiles = p.plan.gtiles(M)[g], cost = p.plan.gcost(M)[g];
+      const int nrows = (p.plan.goff()[g + 1] - first) * p.rows;
+      const int R = (s - first) * p.rows + i * p.group + gq;
+      const int rt = R / kUmmaRows, T = (np + kUmmaPages - 1) / kUmmaPages;
+      const bool dual = nrows - rt * kUmmaRows > 128;
+      const int w = dual ? 2 : 1, nt = p.plan.gtiles(M)[g + 1] - tiles;
+      const int64_t a = (int64_t)cost * H + (int64_t)h * (p.plan.gcost(M)[g + 1] - cost) +
+                        (int64_t)rt * 2 * T;
+      const Shares sh((int64_t)p.plan.gcost(M)[M] * H, p.pre_workers);
+      const int c0 = sh.owner(a);
+      per = dual ? 1 : 2;
+      n_pre = (sh.owner(a + (int64_t)w * (T - 1)) - c0 + 1) * per;
+      pre_slot = (int64_t)tiles * H + h * nt + rt + c0;
+      pre_r = R % kUmmaRows;
+    }
+    // -- the private ones
+    const int a0 = p.plan.spre[s], n = p.plan.spre[s + 1] - a0;
+    const int64_t a = (int64_t)a0 * H + (int64_t)h * n;
+    const Shares sh((int64_t)p.plan.spre[p.num_seqs] * H, p.suf_workers);
+    const int w0 = sh.owner(a), total = n_pre + sh.owner(a + n - 1) - w0 + 1;
+    const int64_t suf_slot = (int64_t)s * H + h + w0;
+    const int suf_r = i * p.group + gq;
+    for (int k0 = sub; k0 < total; k0 += 4 * kWarps) {
+      float m[4], lw[4];
+      float4 v[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int k = k0 + j * kWarps;
+        m[j] = kNoScore;
+        lw[j] = 0.f;
+        v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (k < n_pre) {
+          const int64_t slot = pre_slot + k / per;
+          const int r = pre_r + (per > 1 ? (k & 1) * (p.pre_rp / 2) : 0);
+          const float* ml = p.pre_ml + slot * 3 * p.pre_rp + r;
+          m[j] = __ldg(ml);
+          lw[j] = __ldg(ml + p.pre_rp) + __ldg(ml + 2 * p.pre_rp);
+          v[j] = __ldg(reinterpret_cast<const float4*>(p.pre_o + (slot * p.pre_rp + r) * kHeadDim) +
+                       lane);
+        } else if (k < total) {
+          const int64_t slot = suf_slot + (k - n_pre);
+          const float* ml = p.suf_ml + slot * 2 * p.suf_rp + suf_r;
+          m[j] = __ldg(ml);
+          lw[j] = __ldg(ml + p.suf_rp);
+          v[j] = __ldg(reinterpret_cast<const float4*>(p.suf_o +
+                                                       (slot * p.suf_rp + suf_r) * kHeadDim) +
+                       lane);
+        }
+      }
+      const float mn = fmaxf(fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])), top);
+      const float f = ex2(top - mn);
+      l *= f;
+      acc.x *= f;
+      acc.y *= f;
+      acc.z *= f;
+      acc.w *= f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float w = ex2(m[j] - mn);
+        l += w * lw[j];
+        acc.x += w * v[j].x;
+        acc.y += w * v[j].y;
+        acc.z += w * v[j].z;
+        acc.w += w * v[j].w;
+      }
+      top = mn;
     }
   }
-  const int a0 = p.plan.spre[s], n = p.plan.spre[s + 1] - a0;
-  const int64_t a = (int64_t)a0 * H + (int64_t)h * n;
-  const Shares sh((int64_t)p.plan.spre[p.num_seqs] * H, p.suf_workers);
-  const int w1 = sh.owner(a + n - 1);
-  for (int w = sh.owner(a); w <= w1; ++w)
-    add_private((int64_t)s * H + h + w, i * p.group + gq);
+  if constexpr (kWarps > 1) {
+    s_acc[warp][lane] = acc;
+    if (lane == 0) s_ml[warp] = make_float2(top, l);
+    __syncthreads();
+    if (sub) return;
+#pragma unroll
+    for (int j = 1; j < kWarps; ++j) {
+      const float2 ml = s_ml[warp + j];
+      const float4 v = s_acc[warp + j][lane];
+      const float mn = fmaxf(top, ml.x);
+      const float f0 = ex2(top - mn), f1 = ex2(ml.x - mn);
+      l = l * f0 + ml.y * f1;
+      acc.x = acc.x * f0 + v.x * f1;
+      acc.y = acc.y * f0 + v.y * f1;
+      acc.z = acc.z * f0 + v.z * f1;
+      acc.w = acc.w * f0 + v.w * f1;
+      top = mn;
+    }
+  }
+  if (!in) return;
   float inv = l > 0.f ? 1.f / l : 0.f;
   if (scaled) inv *= __ldg(p.v_scale + (p.scale_per_head ? h : 0));
   __half2 h01 = __floats2half2_rn(acc.x * inv, acc.y * inv);
@@ -218,9 +277,30 @@ __global__ void __launch_bounds__(256) shared_merge_kernel(const SharedParams p,
   *reinterpret_cast<uint2*>(p.out + row * kHeadDim + 4 * lane) = pk;
 }
 
-constexpr int kMaxSms = 160;   // the workspace holds the partial results of this many SMs
+template <int kWarps>
+cudaError_t launch_merge_t(const SharedParams& p, int scaled, cudaStream_t stream) {
+  const int64_t rows = (int64_t)p.num_seqs * p.q_len * p.num_q_heads;
+  const int per_block = 8 / kWarps;
+  return launch_pdl(shared_merge_kernel<kWarps>, (unsigned)((rows + per_block - 1) / per_block), 256,
+                    0, stream, p, scaled);
+}
+
+// Warps per row by the partial results a row may have: one warp folds four in the
+// time of one load, so more warps pay from about eight results on.
+cudaError_t launch_merge(const SharedParams& p, int scaled, cudaStream_t stream) {
+  const int64_t rows = (int64_t)p.num_seqs * p.rows;         // of a kv-head
+  const int64_t segs = (int64_t)umma_tiles((int)rows) * p.num_kv_heads;
+  const int64_t results = (p.pre_workers / segs + 1) * (rows <= 128 ? 2 : 1) +
+                          p.suf_workers / ((int64_t)p.num_seqs * p.num_kv_heads) + 1;
+  if (results > 32) return launch_merge_t<8>(p, scaled, stream);
+  if (results > 16) return launch_merge_t<4>(p, scaled, stream);
+  if (results > 8) return launch_merge_t<2>(p, scaled, stream);
+  return launch_merge_t<1>(p, scaled, stream);
+}
 
 size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
+
+constexpr int kMaxSms = 160;   // the workspace holds the partial results of this many SMs
 
 // Sizes of a call, and where its arrays lie in the workspace.
 struct SharedLayout {
@@ -315,9 +395,8 @@ cudaError_t launch_shared_prefix(const AttnArgs& a, const SharedArgs& sa, void* 
     default: e = launch_shared_int8(p, prefix_map, map, stream); break;
   }
   if (e != cudaSuccess) return e;
-  const int64_t rows = (int64_t)B * a.q_len * a.num_q_heads;
   const int scaled = a.kv_dtype == PQKV_KV_FP8_E4M3 || a.kv_dtype == PQKV_KV_INT8;
-  return launch_pdl(shared_merge_kernel, (unsigned)((rows + 7) / 8), 256, 0, stream, p, scaled);
+  return launch_merge(p, scaled, stream);
 }
 
 }  // namespace pqkv
