@@ -13,8 +13,9 @@
 //
 // Warps: 0-7 and 8-15 the softmax of stream 0 and 1 (two threads per row, each
 // with 64 of a tile's 128 keys), 16-19 and 20-23 widen the 8-bit codes of K and of
-// V to fp16 (exact; TMA writes the fp16 pool's rows into place itself), 24 issues
-// the copies, 25 the products, 27 announces the share's fragments.
+// V to fp16 (exact; TMA writes the fp16 pool's rows into place itself), 24 and
+// 26 issue the copies of K and V, 25 the products, 27 announces the share's
+// fragments.
 //
 // The running maximum of a row is only raised when a score passes it by more
 // than 8 (probabilities stay <= 2^8 in fp16), so O is rescaled rarely, by the
@@ -348,13 +349,13 @@ struct UmmaCfg {
   static constexpr int kBars = 4 + 8 + 10 + 8;
   // fragments announced by the scheduling warp: a ring of kFrags
   static constexpr int kFrags = 4;
-  static constexpr int kReaders = kWide ? 18 : 26;         // warps that read them
+  static constexpr int kReaders = kWide ? 19 : 27;         // warps that read them
   static constexpr int kFragOff = kBarOff + kBars * 8 + 8;
   static constexpr int kSmemBytes = kFragOff + kFrags * (int)sizeof(UmmaFrag);
   static_assert(kSmemBytes <= 232448, "shared memory of a block");
   // registers per thread of the softmax, widening and issuing warps, of the
   // 72 * 896 that the block is launched with
-  static constexpr int kRegSoftmax = 88, kRegWiden = 48, kRegIssue = 56;
+  static constexpr int kRegSoftmax = 80, kRegWiden = 56, kRegIssue = 72;
   static_assert(4 * kRegSoftmax + 2 * kRegWiden + kRegIssue <= 7 * kRegLaunch,
                 "registers of the launch");
 };
@@ -711,31 +712,37 @@ __global__ void __launch_bounds__(896, 1)
             }
           }
           const uint32_t dst = sbase + (kv ? Cfg::kVOff : Cfg::kKOff) + stage * Cfg::kTile;
+          // the slab into registers, and it may be filled again
+          uint4 c[8];
+          const int j = wt & 7;
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            const int idx = i * 128 + wt, row = idx >> 3, j = idx & 7;
-            const uint4 c = lds128u(src + row * 128 + ((j ^ (row & 7)) << 4));
-            uint32_t w[8];
-            dequant_word<KVT>(c.x, w[0], w[1]);
-            dequant_word<KVT>(c.y, w[2], w[3]);
-            dequant_word<KVT>(c.z, w[4], w[5]);
-            dequant_word<KVT>(c.w, w[6], w[7]);
-            // the row's 16 values are chunks 2 (j & 3) and the next of half j >> 2;
-            // the halves' lanes take the two in opposite order, so that a row's
-            // eight lanes store to eight different chunks
+            const int row = i * 16 + (wt >> 3);
+            c[i] = lds128u(src + row * 128 + ((j ^ (row & 7)) << 4));
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&code_empty[kv]);
+          // A row's 16 values are chunks 2 (j & 3) and the next of half j >> 2; the
+          // halves' lanes take the two in opposite order, so that a row's eight
+          // lanes store to eight different chunks.
+          const int c0 = 2 * (j & 3) + (j >> 2), c1 = c0 ^ 1;
+          const bool up = j >> 2;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int row = i * 16 + (wt >> 3);
             const uint32_t at = dst + (j >> 2) * Cfg::kHalf + row * 128;
-            const int c0 = 2 * (j & 3) + (j >> 2), c1 = c0 ^ 1;
-            const bool up = j >> 2;
-            sts128(at + ((c0 ^ (row & 7)) << 4), up ? w[4] : w[0], up ? w[5] : w[1],
-                   up ? w[6] : w[2], up ? w[7] : w[3]);
-            sts128(at + ((c1 ^ (row & 7)) << 4), up ? w[0] : w[4], up ? w[1] : w[5],
-                   up ? w[2] : w[6], up ? w[3] : w[7]);
+            uint32_t w[8];
+            dequant_word<KVT>(up ? c[i].z : c[i].x, w[0], w[1]);
+            dequant_word<KVT>(up ? c[i].w : c[i].y, w[2], w[3]);
+            dequant_word<KVT>(up ? c[i].x : c[i].z, w[4], w[5]);
+            dequant_word<KVT>(up ? c[i].y : c[i].w, w[6], w[7]);
+            sts128(at + ((c0 ^ (row & 7)) << 4), w[0], w[1], w[2], w[3]);
+            sts128(at + ((c1 ^ (row & 7)) << 4), w[4], w[5], w[6], w[7]);
           }
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
             mbar_arrive(&full[stage]);
-            mbar_arrive(&code_empty[kv]);
           }
         }
         if (ok) frag_done(n);
@@ -743,9 +750,19 @@ __global__ void __launch_bounds__(896, 1)
     }
   } else {
   regs_down<Cfg::kRegIssue>();
-  if (warp == 24) {
-    // ================= copies =================
-    uint32_t n = 0, n_tile = 0;      // copies (K or V of a key tile) and key tiles so far
+  if (warp == 24 || warp == 26) {
+    // ================= copies: of K and of V =================
+    // One elected thread issues a tile's copies from warp-uniform code: by eight
+    // lanes, a page each, a copy took 110 cycles, and the 16 (fp16: 32) of a tile
+    // took longer than its products.
+    const int kv = warp == 26;
+    uint64_t *full = Cfg::kWide ? (kv ? v_full : k_full) : code_full + kv,
+             *empty = Cfg::kWide ? (kv ? v_empty : k_empty) : code_empty + kv;
+    constexpr uint32_t kStages = Cfg::kWide ? 2 : 1;
+    constexpr uint32_t kBytes = Cfg::kWide ? Cfg::kTile : Cfg::kSlab;
+    const uint32_t base =
+        sbase + (Cfg::kWide ? (kv ? Cfg::kVOff : Cfg::kKOff) : Cfg::kCodeOff + kv * Cfg::kSlab);
+    uint32_t n_tile = 0;
     bool ok = true;
     const UmmaFrag* f;
     for (uint32_t nf = 0; ok; ++nf) {
@@ -761,52 +778,36 @@ __global__ void __launch_bounds__(896, 1)
         return lane < kUmmaPages && u < nt && pg < left ? __ldg(row + pg) : (int)p.num_pages;
       };
       int next_id = page_id(0);
-      for (int u = 0; ok && u < nt; ++u, ++n_tile) {
+#pragma unroll 1
+      for (int u = 0; u < nt; ++u, ++n_tile) {
         const int id = next_id;
         next_id = page_id(u + 1);
-        if (lane < kUmmaPages && u * kUmmaPages + lane < left &&
+        if (kv == 0 && lane < kUmmaPages && u * kUmmaPages + lane < left &&
             (id < 0 || (int64_t)id >= p.num_pages))
           report(p.status, PQKV_DEV_PAGE_RANGE);
-        for (int kv = 0; kv < 2; ++kv) {
-          if constexpr (Cfg::kWide) {
-            const int stage = n_tile & 1;
-            uint64_t* full = (kv ? v_full : k_full) + stage;
-            ok = n_tile < 2 || wait((kv ? v_empty : k_empty) + stage, ((n_tile >> 1) + 1) & 1);
-            if (!ok) break;
-            if (lane == 0) mbar_arrive_expect_tx(full, Cfg::kTile);
-            __syncwarp();
-            if (lane < kUmmaPages) {
-              const uint32_t dst =
-                  sbase + (kv ? Cfg::kVOff : Cfg::kKOff) + stage * Cfg::kTile + lane * 2048;
-              tma_load_5d(dst, &map, full, 0, 0, kv * kPageSize, h, id);
-              tma_load_5d(dst + Cfg::kHalf, &map, full, 0, 1, kv * kPageSize, h, id);
-            }
-            ++n;
-          } else {
-            ok = n_tile < 1 || wait(&code_empty[kv], (n_tile + 1) & 1);
-            if (!ok) break;
-            if (lane == 0) mbar_arrive_expect_tx(&code_full[kv], Cfg::kSlab);
-            __syncwarp();
-            if (lane < kUmmaPages)
-              tma_load_5d(sbase + Cfg::kCodeOff + kv * Cfg::kSlab + lane * 2048, &map,
-                          &code_full[kv], 0, 0, kv * kPageSize, h, id);
-            ++n;
-          }
+        int ids[kUmmaPages];
+#pragma unroll
+        for (int i = 0; i < kUmmaPages; ++i) ids[i] = __shfl_sync(0xffffffffu, id, i);
+        const uint32_t stage = n_tile % kStages;
+        ok = n_tile < kStages || wait(empty + stage, (n_tile / kStages + 1) & 1);
+        if (!ok) break;
+        if (elect_one()) {
+          mbar_arrive_expect_tx(full + stage, kBytes);
+#pragma unroll
+          for (int i = 0; i < kUmmaPages; ++i)
+#pragma unroll
+            for (int part = 0; part < (Cfg::kWide ? 2 : 1); ++part)
+              tma_load_5d(base + stage * kBytes + part * Cfg::kHalf + i * 2048, &map, full + stage, 0,
+                          part, kv * kPageSize, h, ids[i]);
         }
+        __syncwarp();
       }
       if (ok) frag_done(nf);
     }
     // after a wait that ran out: no copy may be in flight when the CTA ends
-    __syncwarp();
-    if (!ok && lane == 0) {
-      if constexpr (Cfg::kWide) {
-        for (uint32_t i = n > 4 ? n - 4 : 0; i < n; ++i)     // copy i: K or V of tile i / 2
-          (void)mbar_wait((i & 1 ? v_full : k_full) + ((i >> 1) & 1), (i >> 2) & 1);
-      } else {
-        for (uint32_t i = n > 2 ? n - 2 : 0; i < n; ++i)     // K or V of tile i / 2
-          (void)mbar_wait(&code_full[i & 1], (i >> 1) & 1);
-      }
-    }
+    if (!ok && lane == 0)
+      for (uint32_t i = n_tile > kStages ? n_tile - kStages : 0; i < n_tile; ++i)
+        (void)mbar_wait(full + i % kStages, (i / kStages) & 1);
   } else if (warp == 25) {
     // ================= products =================
     // The streams take turns: a stream's product with V and its next scores, then
@@ -907,8 +908,6 @@ __global__ void __launch_bounds__(896, 1)
       if (elect_one()) tc_commit(drain);
       (void)mbar_wait(drain, 0);
     }
-  } else if (warp == 26) {
-    // ================= (no role) =================
   } else {
     // ================= the share's fragments =================
     const Shares sh((int64_t)p.plan.gcost(p.num_groups)[p.num_groups] * H, p.pre_workers);
