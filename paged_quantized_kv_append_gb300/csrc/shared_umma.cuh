@@ -144,6 +144,22 @@ __device__ __forceinline__ void tmem_ld16_wait(uint32_t addr, uint32_t* r) {
       : "r"(addr)
       : "memory");
 }
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_landed16(uint32_t* r) {
+  asm volatile(""
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
+                 "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]),
+                 "+r"(r[13]), "+r"(r[14]), "+r"(r[15])::"memory");
+}
 __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* r) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
@@ -329,12 +345,14 @@ struct UmmaCfg {
   static constexpr int kThreads = 896;
   static constexpr int kRegLaunch = 72;
   static constexpr long long kWaitCycles = 1ll << 31;     // 1.04 s at 2.07 GHz
-  // A row's reference maximum is raised when a score passes it by more than
-  // this (log2): probabilities stay <= 2^14, within fp16's 2^16, and the fewer
-  // rescales of O the better (8 as in the decode kernel: 300 cycles a step on
-  // scores with outliers).  Row-scaled V: p times a scale of up to 2^8 has to
-  // fit too.
-  static constexpr float kRaise = kRowScaled ? 8.f : 14.f;
+  // A row's reference is raised when a score passes it by more than kRaise (log2),
+  // to kAbove above that score: probabilities stay <= 2^15, within fp16's 2^16, and
+  // between two raises lie 18.  A raise holds its stream up by about 500 cycles; on
+  // scores with outliers a step in three had one with 14 and nothing above, one in
+  // seven has now.  Probabilities under 2^-11 of the largest are subnormal in
+  // fp16 (steps of 2^-24): each is off by at most 2^-25 in units of l >= 2^-3.
+  // Row-scaled V: p times a scale of up to 2^8 has to fit fp16 too.
+  static constexpr float kRaise = kRowScaled ? 8.f : 15.f, kAbove = 3.f;
   static constexpr int kHalf = 128 * 128;                 // 16 KB: 128 rows of 64 values
   static constexpr int kTile = 2 * kHalf;
   static constexpr int kQOff = 0;                         // 2 streams
@@ -346,7 +364,7 @@ struct UmmaCfg {
   static constexpr int kScOff = kCodeOff + kSlabs * kSlab;  // fp16 row scales: 4 stages of K and V
   static constexpr int kScBytes = kRowScaled ? 4 * 2 * 128 * 2 : 0;
   static constexpr int kBarOff = kScOff + kScBytes;
-  static constexpr int kBars = 4 + 8 + 10 + 8;
+  static constexpr int kBars = 4 + 8 + 12 + 8;
   // fragments announced by the scheduling warp: a ring of kFrags
   static constexpr int kFrags = 4;
   static constexpr int kReaders = kWide ? 19 : 27;         // warps that read them
@@ -378,11 +396,11 @@ __global__ void __launch_bounds__(896, 1)
   uint64_t* v_empty = bars + 10;
   uint64_t* q_ready = bars + 12;       // [stream] the fragment's query rows are in place
   uint64_t* s_full = bars + 14;        // [stream] scores in TMEM
-  uint64_t* p_ready = bars + 16;       // [stream] their probabilities, and O rescaled
-  uint64_t* o_last = bars + 18;        // [stream] the fragment's last product with V is done
-  uint64_t* drain = bars + 20;         // after a wait that ran out
-  uint64_t* frag_full = bars + 22;     // [kFrags]
-  uint64_t* frag_empty = bars + 26;    // [kFrags]
+  uint64_t* p_ready = bars + 16;       // [stream][part] probabilities (32 of a thread's 64 keys)
+  uint64_t* o_last = bars + 20;        // [stream] the fragment's last product with V is done
+  uint64_t* drain = bars + 22;         // after a wait that ran out
+  uint64_t* frag_full = bars + 24;     // [kFrags]
+  uint64_t* frag_empty = bars + 28;    // [kFrags]
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Cfg::kBarOff + Cfg::kBars * 8);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Cfg::kBarOff + Cfg::kBars * 8 + 4);
   const int H = p.num_kv_heads;
@@ -399,6 +417,7 @@ __global__ void __launch_bounds__(896, 1)
       mbar_init(&q_ready[i], 8);
       mbar_init(&s_full[i], 1);
       mbar_init(&p_ready[i], 8);
+      mbar_init(&p_ready[2 + i], 8);
       mbar_init(&o_last[i], 1);
     }
     mbar_init(drain, 1);
@@ -459,7 +478,7 @@ __global__ void __launch_bounds__(896, 1)
     const uint32_t tS = tmem + lane_sel + st * 128 + half * 64;
     const uint32_t tO = tmem + lane_sel + 256 + st * 128 + half * 64;
     const int pair = 1 + st * 4 + wq;                       // barrier of the row's two warps
-    const uint32_t tPeer = tS + 63 - half * 128 + 64;       // the other half's last column
+    const uint32_t tPeer = tS + 31 + (half ? -64 : 64);     // the other half's maximum
     uint32_t n_step = 0;             // steps of this stream so far
     uint32_t n_last = 0;             // its fragments with a step
     uint32_t n_tile = 0;             // key tiles of the CTA so far (row scales' stages)
@@ -486,14 +505,12 @@ __global__ void __launch_bounds__(896, 1)
       }
       return live;
     };
-    // 32 scores from column c on: scaled by their rows' scales, -inf behind the prefix
-    auto scores = [&](uint32_t* s, int c, int valid, uint32_t sc) {
-      tmem_ld32(tS + c, s);
-      tmem_wait_ld();
-      tmem_landed32(s);
+    // 16 scores from column c on, once landed: scaled by their rows' scales, -inf
+    // behind the prefix
+    auto dress = [&](uint32_t* s, int c, int valid, uint32_t sc) {
       if constexpr (Cfg::kRowScaled) {
 #pragma unroll
-        for (int k = 0; k < 32; k += 8) {
+        for (int k = 0; k < 16; k += 8) {
           const uint4 k8 = lds128u(sc + (c + k) * 2);
           const uint32_t kk[4] = {k8.x, k8.y, k8.z, k8.w};
 #pragma unroll
@@ -506,16 +523,9 @@ __global__ void __launch_bounds__(896, 1)
       }
       if (valid < 64) {
 #pragma unroll
-        for (int k = 0; k < 32; ++k)
+        for (int k = 0; k < 16; ++k)
           if (c + k >= valid) s[k] = 0xff800000u;
       }
-    };
-    auto max32 = [&](const uint32_t* s) -> float {
-      float m[4] = {kNoScore, kNoScore, kNoScore, kNoScore};
-#pragma unroll
-      for (int k = 0; k < 32; k += 2)
-        m[(k >> 1) & 3] = max3(m[(k >> 1) & 3], __uint_as_float(s[k]), __uint_as_float(s[k + 1]));
-      return max3(fmaxf(m[0], m[1]), m[2], m[3]);
     };
     bool ok = frag_at(n, f) && f->nt > 0;
     bool live = ok && load_row();
@@ -545,77 +555,115 @@ __global__ void __launch_bounds__(896, 1)
           // 64 fp16 scales of K, of V 256 bytes on
           const uint32_t sc = sbase + Cfg::kScOff + half * 128 +
                               (n_tile + (dual ? i : 2 * i + st)) % 4 * 512;
-          uint32_t s[32], s2[32];
-          scores(s2, 32, valid, sc);
-          const float hi = max32(s2);
-          scores(s, 0, valid, sc);
-          const float m2 = fmaxf(hi, max32(s)) * scale;
+          // -- the maximum.  The first 32 scores stay in registers, the others are
+          // read again below (registers are short)
+          uint32_t s[32];
+          float m2;
+          {
+            uint32_t v[32];
+            tmem_ld32(tS, s);
+            tmem_ld32(tS + 32, v);
+            tmem_wait_ld();
+            tmem_landed32(s);
+            tmem_landed32(v);
+            float m[4] = {kNoScore, kNoScore, kNoScore, kNoScore};
+#pragma unroll
+            for (int c = 0; c < 32; c += 16) {
+              dress(v + c, 32 + c, valid, sc);
+              dress(s + c, c, valid, sc);
+            }
+#pragma unroll
+            for (int k = 0; k < 32; k += 2) {
+              m[k & 2] = max3(m[k & 2], __uint_as_float(v[k]), __uint_as_float(v[k + 1]));
+              m[1 + (k & 2)] = max3(m[1 + (k & 2)], __uint_as_float(s[k]), __uint_as_float(s[k + 1]));
+            }
+            m2 = max3(fmaxf(m[0], m[1]), m[2], m[3]) * scale;
+          }
           if (pair_any(pair, m2 > ref + Cfg::kRaise)) {
-            // raise: the two warps tell each other their rows' maxima (in the last
-            // score column of their half, put back afterwards) and rescale half of
-            // O each.  O is still: the last product with V came before these scores
-            const uint32_t keep = tmem_ld1_wait(tS + 63);
-            tmem_st1(tS + 63, __float_as_uint(m2));
+            // -- raise: the two warps tell each other their rows' maxima (over the
+            // last of the scores that are in registers) and rescale half of O each.
+            // O is still: the last product with V came before these scores
+            tmem_st1(tS + 31, __float_as_uint(m2));
             tmem_wait_st();
             tc_fence_before();
             pair_sync(pair);
             tc_fence_after();
             const float both = fmaxf(m2, __uint_as_float(tmem_ld1_wait(tPeer)));
-            tc_fence_before();
-            pair_sync(pair);
-            tc_fence_after();
-            tmem_st1(tS + 63, keep);
-            tmem_wait_st();
-            const float nref = both > ref + Cfg::kRaise ? both : ref;
+            const float nref = both > ref + Cfg::kRaise ? both + Cfg::kAbove : ref;
             const float fct = ex2(ref - nref);
             ref = nref;
             l *= fct;
             if (i > 0) {
 #pragma unroll 1
-              for (int c = 0; c < 64; c += 16) {
-                uint32_t o[16];
-                tmem_ld16_wait(tO + c, o);
+              for (int c = 0; c < 64; c += 32) {
+                uint32_t o[32];
+                tmem_ld32(tO + c, o);
+                tmem_wait_ld();
+                tmem_landed32(o);
 #pragma unroll
-                for (int k = 0; k < 16; ++k)
-                  o[k] = __float_as_uint(__uint_as_float(o[k]) * fct);
-                tmem_st16(tO + c, o);
+                for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * fct);
+                tmem_st32(tO + c, o);
               }
             }
+            tc_fence_before();
+            pair_sync(pair);                 // both maxima are read: P may go over them
+            tc_fence_after();
           }
+          // -- the probabilities, 16 keys at a time; the first 32 are handed over
+          // while the others are formed
           const uint64_t scale2 = f2(scale, scale), ref2 = f2(-ref, -ref);
-          uint64_t sum[4] = {0, 0, 0, 0};
+          uint64_t sum[2] = {0, 0};
+          uint32_t ph[16];
 #pragma unroll
-          for (int c = 0; c < 64; c += 32) {
-            if (c) scores(s, 32, valid, sc);           // read again: registers are short
+          for (int c = 0; c < 4; ++c) {
+            uint32_t* x = s + 16 * (c & 1);
+            if (c >= 2) {
+              tmem_wait_ld();
+              tmem_landed16(x);
+              if (c == 2) tmem_ld16(tS + 48, s + 16);
+              dress(x, 16 * c, valid, sc);
+            }
 #pragma unroll
-            for (int k = 0; k < 16; ++k) {
+            for (int k = 0; k < 8; ++k) {
               float a, b;
-              unf2(fma2(f2(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1])), scale2, ref2),
+              unf2(fma2(f2(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1])), scale2, ref2),
                    a, b);
               a = ex2(a);
               b = ex2(b);
-              sum[k & 3] = add2(sum[k & 3], f2(a, b));
+              sum[k & 1] = add2(sum[k & 1], f2(a, b));
               if constexpr (Cfg::kRowScaled) {
                 // p * (V row scale), rounded once: the fp32 product
                 uint32_t w;
-                asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w) : "r"(sc + 256 + (c + 2 * k) * 2));
+                asm volatile("ld.shared.b32 %0, [%1];"
+                             : "=r"(w)
+                             : "r"(sc + 256 + (16 * c + 2 * k) * 2));
                 const float2 vs = __half22float2(*reinterpret_cast<const __half2*>(&w));
                 a *= vs.x;
                 b *= vs.y;
               }
-              s[k] = pack_half2(a, b);
+              ph[8 * (c & 1) + k] = pack_half2(a, b);
             }
-            tmem_st16(tS + c / 2, s);
+            if (c == 0) tmem_ld16(tS + 32, s);         // lands under the second 16
+            if (c == 1) {
+              tmem_st16(tS, ph);
+              tmem_wait_st();
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&p_ready[2 * st]);
+            }
           }
+          tmem_st16(tS + 16, ph);
           float a, b;
-          unf2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), a, b);
+          unf2(add2(sum[0], sum[1]), a, b);
           l += a + b;
           tmem_wait_st();
+        } else if (lane == 0) {
+          mbar_arrive(&p_ready[2 * st]);
         }
         // (a warp without a row: its probabilities feed rows that nobody reads)
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&p_ready[st]);
+        if (lane == 0) mbar_arrive(&p_ready[2 * st + 1]);
         n_step += 1;
         valid -= dual ? kUmmaKeys : 2 * kUmmaKeys;
       }
@@ -844,30 +892,34 @@ __global__ void __launch_bounds__(896, 1)
     };
     // O += P V on key tile tl, P over the scores (32 columns for either half's 64
     // keys); then the stream's next scores (key tile `next`), over P: products of
-    // one thread run in order.  The lanes look at the three barriers at once.
+    // one thread run in order.  The lanes look at a wait's two barriers at once.
     auto step = [&](auto stream, uint32_t tl, uint32_t next, bool more, bool acc, bool release,
                     uint32_t& ns) -> bool {
       constexpr int st = decltype(stream)::value;
       const uint32_t stage = tl & 1;
-      uint64_t* bar = &p_ready[st];
-      uint32_t parity = ns;
-      if (lane & 1) {
-        bar = &v_full[stage];
-        parity = tl >> 1;
-      } else if ((lane & 2) && more) {
-        bar = &k_full[next & 1];
-        parity = next >> 1;
+      const uint64_t b = v_desc + (uint64_t)(stage * (Cfg::kTile >> 4));
+      const uint32_t tS = tmem + st * 128, tO = tmem + 256 + st * 128;
+      // (a part: 32 keys of either half)
+      if (!wait(lane & 1 ? &v_full[stage] : &p_ready[2 * st], (lane & 1 ? tl >> 1 : ns) & 1))
+        return false;
+      tc_fence_after();
+      if (elect_one()) {
+        tc_mma_ts(tO, tS, b, kIdescPV, acc);
+        tc_mma_ts(tO, tS + 8, b + 128, kIdescPV, true);
+        tc_mma_ts(tO, tS + 64, b + 512, kIdescPV, true);
+        tc_mma_ts(tO, tS + 72, b + 640, kIdescPV, true);
       }
-      if (!wait(bar, parity & 1)) return false;
+      __syncwarp();
+      const bool odd = (lane & 1) && more;
+      if (!wait(odd ? &k_full[next & 1] : &p_ready[2 * st + 1], (odd ? next >> 1 : ns) & 1))
+        return false;
       ns += 1;
       tc_fence_after();
       if (elect_one()) {
-        const uint64_t b = v_desc + (uint64_t)(stage * (Cfg::kTile >> 4));
-        const uint32_t tS = tmem + st * 128, tO = tmem + 256 + st * 128;
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          tc_mma_ts(tO, tS + (k >> 2) * 64 + (k & 3) * 8, b + (uint64_t)(k * 2048 >> 4), kIdescPV,
-                    acc || k > 0);
+        tc_mma_ts(tO, tS + 16, b + 256, kIdescPV, true);
+        tc_mma_ts(tO, tS + 24, b + 384, kIdescPV, true);
+        tc_mma_ts(tO, tS + 80, b + 768, kIdescPV, true);
+        tc_mma_ts(tO, tS + 88, b + 896, kIdescPV, true);
         if (release) tc_commit(&v_empty[stage]);
         if (more) qk(stream, next & 1, release);
         else tc_commit(&o_last[st]);
