@@ -6,9 +6,9 @@ namespace pqkv {
 
 cudaError_t launch_shared_int8(const SharedParams& p, const CUtensorMap& prefix_map,
                              const CUtensorMap& map, cudaStream_t st) {
-  const cudaError_t e = launch_shared_umma_t<PQKV_KV_INT8>(p, prefix_map, st);
+  const cudaError_t e = launch_private_dtype<PQKV_KV_INT8>(p, map, p.suf_rp / 8, st);
   if (e != cudaSuccess) return e;
-  return launch_private_dtype<PQKV_KV_INT8>(p, map, p.suf_rp / 8, st);
+  return launch_shared_umma_t<PQKV_KV_INT8>(p, prefix_map, st);
 }
 
 }  // namespace pqkv

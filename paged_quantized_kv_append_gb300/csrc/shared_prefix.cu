@@ -55,6 +55,15 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedP
   grid_dependency_wait();
   grid_dependents_launch();
   const int tid = threadIdx.x, B = p.num_seqs, M = p.num_groups;
+  // -- everything that is read, at once
+  const int per = (B + kPlanThreads - 1) / kPlanThreads, gper = (M + kPlanThreads - 1) / kPlanThreads;
+  int len[kPlanEach], want[kPlanEach];
+#pragma unroll
+  for (int i = 0; i < kPlanEach; ++i) {
+    const int s = tid * per + i, g = tid * gper + i;
+    len[i] = i < per && s < B ? p.seq_lens[s] : 0;
+    want[i] = i < gper && g < M ? p.prefix_lens[g] : 0;
+  }
   // -- the groups: contiguous, in order, every sequence in one.  Offsets that
   //    are not are reported, and nothing is shared then
   bool ok = true;
@@ -69,40 +78,36 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedP
   if (!ok) {
     if (tid == 0) report(p.status, PQKV_DEV_SEQ_RANGE);
     for (int g = tid; g <= M; g += kPlanThreads) s_off[g] = g == 0 ? 0 : B;
+    __syncthreads();
   }
-  __syncthreads();
   // -- the sequences' lengths, and the shortest of each group
-  const int per = (B + kPlanThreads - 1) / kPlanThreads;
-  int len[kPlanEach], grp[kPlanEach];
+  int grp[kPlanEach];
 #pragma unroll
   for (int i = 0; i < kPlanEach; ++i) {
     const int s = tid * per + i;
-    len[i] = grp[i] = 0;
+    grp[i] = 0;
     if (i >= per || s >= B) continue;
-    int L = p.seq_lens[s];
     const int Lmax = p.bt_stride * kPageSize;
-    if (L < p.q_len || L > Lmax) {
+    if (len[i] < p.q_len || len[i] > Lmax) {
       report(p.status, PQKV_DEV_SEQ_RANGE);
-      L = max(p.q_len, min(L, Lmax));
+      len[i] = max(p.q_len, min(len[i], Lmax));
     }
-    len[i] = L;
     grp[i] = last_at_most(s_off, M, s);
-    atomicMin(&s_min[grp[i]], L - p.q_len);
+    atomicMin(&s_min[grp[i]], len[i] - p.q_len);
   }
   __syncthreads();
   // -- the groups' shared pages, row tiles and costs
-  const int gper = (M + kPlanThreads - 1) / kPlanThreads;
   int tiles[kPlanEach], costs[kPlanEach], tsum = 0, psum = 0;
 #pragma unroll
   for (int i = 0; i < kPlanEach; ++i) {
     const int g = tid * gper + i;
     tiles[i] = costs[i] = 0;
     if (i >= gper || g >= M) continue;
-    const int n = s_off[g + 1] - s_off[g], want = p.prefix_lens[g];
+    const int n = s_off[g + 1] - s_off[g];
     int pages = 0;
     if (n > 0 && ok) {
-      if (want < 0 || want > s_min[g] + p.q_len) report(p.status, PQKV_DEV_SEQ_RANGE);
-      pages = max(0, min(want, s_min[g])) / kPageSize;
+      if (want[i] < 0 || want[i] > s_min[g] + p.q_len) report(p.status, PQKV_DEV_SEQ_RANGE);
+      pages = max(0, min(want[i], s_min[g])) / kPageSize;
     }
     p.plan.gpages(M)[g] = pages;
     p.plan.goff()[g] = s_off[g];

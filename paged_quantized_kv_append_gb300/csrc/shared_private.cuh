@@ -50,16 +50,16 @@ __global__ void __launch_bounds__(WarpCfg<KVT, NT>::kThreads, WarpCfg<KVT, NT>::
   const int g = lane >> 2, t = lane & 3;
   const int H = p.num_kv_heads;
 
+  if (tid < W * S) {
+    mbar_init(&bars[tid], 1);
+    fence_barrier_init();
+  }
+  if (tid == 0) prefetch_tensormap(&map);
   grid_dependency_wait();
   grid_dependents_launch();
   for (int i = tid; i <= N; i += Cfg::kThreads) {
     pre[i] = p.plan.spre[i];
     if (i < N) page0[i] = p.plan.page0[i];
-  }
-  if (tid == 0) {
-    prefetch_tensormap(&map);
-    for (int i = 0; i < W * S; ++i) mbar_init(&bars[i], 1);
-    fence_barrier_init();
   }
   __syncthreads();
 

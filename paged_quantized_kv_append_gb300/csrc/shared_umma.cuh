@@ -430,7 +430,10 @@ __global__ void __launch_bounds__(896, 1)
   }
   if (warp == 25) tmem_alloc_512(tmem_slot);
   if (warp == 24 && lane == 0) prefetch_tensormap(&map);
-  grid_dependency_wait();
+  // No wait for the launch before (the private keys' kernel) here: it reads and
+  // writes nothing that this kernel writes or reads, and its blocks let this
+  // kernel's be scheduled only after they have waited for the plan.  The SMs that
+  // it leaves first start on the prefix.
   grid_dependents_launch();
   tc_fence_before();
   __syncthreads();
@@ -985,6 +988,8 @@ __global__ void __launch_bounds__(896, 1)
   __syncthreads();
   tc_fence_after();
   if (warp == 25) tmem_free_512(tmem);
+  // what comes after this kernel comes after the private keys' too
+  grid_dependency_wait();
 }
 
 template <int KVT>
