@@ -99,6 +99,36 @@ __global__ void __launch_bounds__(WarpCfg<KVT, NT>::kThreads, WarpCfg<KVT, NT>::
     id = __ldg(p.block_table + (int64_t)s * p.bt_stride + page0[s] + pg);
     if (id < 0 || (int64_t)id >= p.num_pages) report(p.status, PQKV_DEV_PAGE_RANGE);
   };
+  // -- query rows: lane (g, t) holds, of row 8 nt + g, the values that its own
+  // fragment-table entries take
+  int q_off[NT];                        // of the row, from the sequence's and head's first
+  uint32_t q_pos = 0;                   // 4 bits each: query position of rows 8 nt + 2 t + c
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const int r = 8 * nt + g;
+    q_off[nt] = r < p.rows ? (r / p.group * p.num_q_heads + r % p.group) * kHeadDim : -1;
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const int rr = 8 * nt + 2 * t + c;     // (rows behind the last see what the last sees)
+      q_pos |= (uint32_t)(min(rr, p.rows - 1) / p.group) << (4 * (2 * nt + c));
+    }
+  }
+  uint4 qv[NT][4];
+  auto fetch_q = [&](int s, int h) {
+    const uint16_t* src =
+        p.q + ((int64_t)s * p.q_len * p.num_q_heads + (int64_t)h * p.group) * kHeadDim;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int k2 = 0; k2 < 4; ++k2)
+        qv[nt][k2] = q_off[nt] >= 0 ? __ldg(reinterpret_cast<const uint4*>(
+                                          src + q_off[nt] + k_dim_base<KVT>(t, 2 * k2)))
+                                    : make_uint4(0, 0, 0, 0);
+  };
+  {                                     // the first segment's, under the look-ups below
+    const int s = sequence_of(x0);
+    fetch_q(s, (int)Shares::div(x0 - (int64_t)pre[s] * H, pre[s + 1] - pre[s]));
+  }
   int cur_id, cur_h, nxt_id, nxt_h, ubase = 0;
   lookup(lane, cur_id, cur_h);
   lookup(32 + lane, nxt_id, nxt_h);
@@ -152,19 +182,12 @@ __global__ void __launch_bounds__(WarpCfg<KVT, NT>::kThreads, WarpCfg<KVT, NT>::
     const int npg = (int)min((int64_t)(np - pg0), x1 - x);
     const int L = p.plan.len[s], lim_min = L - p.q_len;
     const int key0 = (page0[s] + pg0) * kPageSize;
-    const int64_t tok0 = (int64_t)s * p.q_len;
     // ---- the segment's query rows, in fragment order (a lane's own entries)
+    if (x > x0) fetch_q(s, h);
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const int r = 8 * nt + g;
-      const uint16_t* src =
-          p.q + ((tok0 + r / p.group) * p.num_q_heads + h * p.group + r % p.group) * kHeadDim;
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int k2 = 0; k2 < 4; ++k2)
-        sQ[(k2 * NT + nt) * 32 + lane] =
-            r < p.rows ? __ldg(reinterpret_cast<const uint4*>(src + k_dim_base<KVT>(t, 2 * k2)))
-                      : make_uint4(0, 0, 0, 0);
-    }
+      for (int k2 = 0; k2 < 4; ++k2) sQ[(k2 * NT + nt) * 32 + lane] = qv[nt][k2];
     float qk_scale = p.sm_scale_log2;
     if constexpr (KVT != PQKV_KV_FP16 && KVT != PQKV_KV_INT8_ROW) {
       const int hs = p.scale_per_head ? h : 0;
@@ -223,9 +246,9 @@ __global__ void __launch_bounds__(WarpCfg<KVT, NT>::kThreads, WarpCfg<KVT, NT>::
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const int r = 8 * nt + 2 * t + (k & 1);
             const int tok = pos0 + g + ((k & 2) ? 8 : 0);
-            if (r < p.rows && tok > lim_min + r / p.group) sc[nt][k] = -INFINITY;
+            const int at = (q_pos >> (4 * (2 * nt + (k & 1)))) & 15;
+            if (tok > lim_min + at) sc[nt][k] = -INFINITY;
           }
       }
       // the reference maximum moves only past 2^8 (see attention_impl.cuh)
