@@ -112,7 +112,7 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedP
     p.plan.gpages(M)[g] = pages;
     p.plan.goff()[g] = s_off[g];
     tiles[i] = pages > 0 ? umma_tiles(n * p.rows) : 0;
-    costs[i] = umma_weight(n * p.rows) * ((pages + kUmmaPages - 1) / kUmmaPages);
+    costs[i] = umma_weight(n * p.rows, p.split_cost) * ((pages + kUmmaPages - 1) / kUmmaPages);
     tsum += tiles[i];
     psum += costs[i];
     s_min[g] = pages;
@@ -189,10 +189,10 @@ __global__ void __launch_bounds__(256) shared_merge_kernel(const SharedParams p,
       const int R = (s - first) * p.rows + i * p.group + gq;
       const int rt = R / kUmmaRows, T = (np + kUmmaPages - 1) / kUmmaPages;
       const bool dual = nrows - rt * kUmmaRows > 128;
-      const int w = dual ? 2 : 1, nt = p.plan.gtiles(M)[g + 1] - tiles;
+      const int w = dual ? kFullCost : p.split_cost, nt = p.plan.gtiles(M)[g + 1] - tiles;
       const int64_t a = (int64_t)cost * H + (int64_t)h * (p.plan.gcost(M)[g + 1] - cost) +
-                        (int64_t)rt * 2 * T;
-      const Shares sh((int64_t)p.plan.gcost(M)[M] * H, p.pre_workers);
+                        (int64_t)rt * kFullCost * T;
+      const Shares sh((int64_t)p.plan.gcost(M)[M] * H, p.pre_workers, kPrefixShare);
       const int c0 = sh.owner(a);
       per = dual ? 1 : 2;
       n_pre = (sh.owner(a + (int64_t)w * (T - 1)) - c0 + 1) * per;
@@ -202,7 +202,7 @@ __global__ void __launch_bounds__(256) shared_merge_kernel(const SharedParams p,
     // -- the private ones
     const int a0 = p.plan.spre[s], n = p.plan.spre[s + 1] - a0;
     const int64_t a = (int64_t)a0 * H + (int64_t)h * n;
-    const Shares sh((int64_t)p.plan.spre[p.num_seqs] * H, p.suf_workers);
+    const Shares sh((int64_t)p.plan.spre[p.num_seqs] * H, p.suf_workers, kPrivateShare);
     const int w0 = sh.owner(a), total = n_pre + sh.owner(a + n - 1) - w0 + 1;
     const int64_t suf_slot = (int64_t)s * H + h + w0;
     const int suf_r = i * p.group + gq;
@@ -389,6 +389,7 @@ cudaError_t launch_shared_prefix(const AttnArgs& a, const SharedArgs& sa, void* 
   p.suf_rp = lay.suf_rp;
   p.pre_workers = lay.pre_workers;
   p.suf_workers = lay.suf_workers;
+  p.split_cost = a.kv_dtype == PQKV_KV_FP8_E4M3 || a.kv_dtype == PQKV_KV_INT8 ? 3 : 2;
   p.sm_scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)a.head_dim));
 
   cudaError_t e = launch_pdl(shared_plan_kernel, 1, kPlanThreads, 0, stream, p);

@@ -62,21 +62,20 @@ struct SharedParams {
   int32_t pre_rp;           // rows of a prefix fragment's slot
   int32_t suf_rp;           // padded rows of a private fragment
   int32_t pre_workers;      // CTAs of the prefix launch
+  int32_t split_cost;       // of a key tile for a row tile of at most 128 rows; see kFullCost
   int32_t suf_workers;      // warps of the private-key launch
   float sm_scale_log2;      // log2(e) / sqrt(head_dim)
 };
 
 // Equal contiguous shares of U units over at most `most` workers, at least
-// kMinShare units each (fewer, larger shares where there is little to do: each
+// `min_share` units each (fewer, larger shares where there is little to do: each
 // share ends in a partial result that the merge has to read).  Every share is
 // non-empty, so the workers holding units of [a, b) are owner(a)..owner(b-1).
-constexpr int kMinShare = 2;
-
 struct Shares {
   int64_t U;
   int n;
-  __device__ __forceinline__ Shares(int64_t units, int most) : U(units) {
-    const int64_t want = units / kMinShare;
+  __device__ __forceinline__ Shares(int64_t units, int most, int min_share) : U(units) {
+    const int64_t want = div(units, min_share);
     n = (int)(want < most ? (units > 0 && want < 1 ? 1 : want) : most);
   }
   static __device__ __forceinline__ int64_t div(int64_t a, int64_t b) {
@@ -91,16 +90,23 @@ constexpr int kUmmaRows = 256;      // rows of a full row tile
 constexpr int kUmmaKeys = 128;      // keys of a key tile
 constexpr int kUmmaPages = kUmmaKeys / kPageSize;
 
-// Work of the prefix: (row tile, key tile) pairs of a kv-head.  A row tile's
-// cost per key tile: 2 for more than 128 rows, else 1 (half the
-// products).  The row tiles of a kv-head: full ones, then the rest.
+// Work of the prefix: (row tile, key tile) pairs of a kv-head.  The row tiles of a
+// kv-head are full ones, then the rest.  A key tile costs a row tile of more than
+// 128 rows kFullCost, a smaller one (half the products, the same codes to widen)
+// split_cost.  For E4M3 and INT8, where widening decides a small row tile, 3
+// (cycles per key tile: 2940 against 2350; decode of 256: 109 us, with 2: 112).  For
+// FP16, with nothing to widen (2620 against 1500), and INT8_ROW, whose scores cost the
+// softmax more, 2 (verification of 4 groups: 105 us, with 3: 111).
+constexpr int kFullCost = 4;
 __host__ __device__ __forceinline__ int umma_tiles(int rows) {
   return (rows + kUmmaRows - 1) / kUmmaRows;
 }
-__host__ __device__ __forceinline__ int umma_weight(int rows) {
+__host__ __device__ __forceinline__ int umma_weight(int rows, int split_cost) {
   const int rem = rows % kUmmaRows;
-  return 2 * (rows / kUmmaRows) + (rem > 128 ? 2 : (rem > 0 ? 1 : 0));
+  return kFullCost * (rows / kUmmaRows) + (rem > 128 ? kFullCost : (rem > 0 ? split_cost : 0));
 }
+constexpr int kPrivateShare = 2;             // pages, the least of a warp
+constexpr int kPrefixShare = kFullCost;      // a key tile, the least of a CTA
 
 // A call's two halves, per KV format (shared_<format>.cu).  prefix_map: see
 // encode_prefix_map; map: the attention's own.

@@ -64,7 +64,7 @@ __global__ void __launch_bounds__(WarpCfg<KVT, NT>::kThreads, WarpCfg<KVT, NT>::
   __syncthreads();
 
   const int64_t U = (int64_t)pre[N] * H;
-  const Shares sh(U, p.suf_workers);
+  const Shares sh(U, p.suf_workers, kPrivateShare);
   const int worker = warp * gridDim.x + blockIdx.x;     // neighbouring shares on different SMs
   if (worker >= sh.n) return;
   const int64_t x0 = sh.start(worker), x1 = sh.start(worker + 1);
