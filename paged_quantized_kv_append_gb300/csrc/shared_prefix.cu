@@ -140,7 +140,7 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedP
   for (int i = 0; i < kPlanEach; ++i) {
     const int s = tid * per + i;
     if (i >= per || s >= B) continue;
-    own += (len[i] + kPageSize - 1) / kPageSize - s_min[grp[i]];
+    own += (len[i] + kPageSize - 1) / kPageSize - s_min[grp[i]] + kSegmentCost;
   }
   int at = block_scan(own, total_s);
 #pragma unroll
@@ -151,7 +151,7 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedP
     p.plan.group[s] = grp[i];
     p.plan.page0[s] = s_min[grp[i]];
     p.plan.spre[s] = at;
-    at += (len[i] + kPageSize - 1) / kPageSize - s_min[grp[i]];
+    at += (len[i] + kPageSize - 1) / kPageSize - s_min[grp[i]] + kSegmentCost;
   }
   if (tid == 0) p.plan.spre[B] = total_s;
 }
@@ -203,7 +203,7 @@ __global__ void __launch_bounds__(256) shared_merge_kernel(const SharedParams p,
     const int a0 = p.plan.spre[s], n = p.plan.spre[s + 1] - a0;
     const int64_t a = (int64_t)a0 * H + (int64_t)h * n;
     const Shares sh((int64_t)p.plan.spre[p.num_seqs] * H, p.suf_workers, kPrivateShare);
-    const int w0 = sh.owner(a), total = n_pre + sh.owner(a + n - 1) - w0 + 1;
+    const int w0 = sh.owner(a), total = n_pre + sh.owner(a + n - kSegmentCost - 1) - w0 + 1;
     const int64_t suf_slot = (int64_t)s * H + h + w0;
     const int suf_r = i * p.group + gq;
     for (int k0 = sub; k0 < total; k0 += 4 * kWarps) {

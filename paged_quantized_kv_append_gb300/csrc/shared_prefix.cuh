@@ -24,7 +24,7 @@ struct SharedPlan {
   int32_t* len;       // [N]     tokens of the sequence, clamped into its row
   int32_t* group;     // [N]     its group
   int32_t* page0;     // [N]     its first private page = its group's shared pages
-  int32_t* spre;      // [N + 1] private pages of the sequences before it
+  int32_t* spre;      // [N + 1] units of the sequences before it, see kSegmentCost
   // four rows of M + 1: the group's first sequence, its shared pages, the row
   // tiles of a kv-head in the groups before it, and those tiles' cost
   int32_t* groups;
@@ -105,7 +105,13 @@ __host__ __device__ __forceinline__ int umma_weight(int rows, int split_cost) {
   const int rem = rows % kUmmaRows;
   return kFullCost * (rows / kUmmaRows) + (rem > 128 ? kFullCost : (rem > 0 ? split_cost : 0));
 }
-constexpr int kPrivateShare = 2;             // pages, the least of a warp
+// Work of the private keys: the units of a (sequence, kv-head) segment are its pages,
+// then kSegmentCost that stand for its query rows and its partial result: a share in
+// sequences of one or two private pages holds many segments, and by pages alone one SM
+// worked 99K cycles where the others took 61K (fp16 verification of 32 x 8: 125 us, with
+// 1, 2 or 4 here 112, with 6 113).
+constexpr int kSegmentCost = 2;
+constexpr int kPrivateShare = 2;             // units, the least of a warp
 constexpr int kPrefixShare = kFullCost;      // a key tile, the least of a CTA
 
 // A call's two halves, per KV format (shared_<format>.cu).  prefix_map: see

@@ -1,6 +1,6 @@
 // The private keys of a shared-prefix batch: short caches of many sequences.
-// One warp per share: the fragments of a contiguous range of (page, kv-head)
-// units, each streamed by the warp alone (no barrier between warps, so a
+// One warp per share: the fragments of a contiguous range of units (the pages of
+// (sequence, kv-head) segments, and what a segment costs besides), each streamed by the warp alone (no barrier between warps, so a
 // sequence with a few pages costs a few pages).  Per page the products are the
 // attention kernel's: S^T = K Q^T with the page's tokens as M and the G*q_len
 // query rows as N, O^T = V^T P^T.
@@ -44,7 +44,7 @@ __global__ void __launch_bounds__(WarpCfg<KVT, NT>::kThreads, WarpCfg<KVT, NT>::
                                              ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Cfg::kBarOff);
   const int N = p.num_seqs;
-  int* pre = reinterpret_cast<int*>(smem + Cfg::kTabOff);   // [N + 1] private pages before
+  int* pre = reinterpret_cast<int*>(smem + Cfg::kTabOff);   // [N + 1] units before
   int* page0 = pre + N + 1;                                 // [N] first private page
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, t = lane & 3;
@@ -67,8 +67,8 @@ __global__ void __launch_bounds__(WarpCfg<KVT, NT>::kThreads, WarpCfg<KVT, NT>::
   const Shares sh(U, p.suf_workers, kPrivateShare);
   const int worker = warp * gridDim.x + blockIdx.x;     // neighbouring shares on different SMs
   if (worker >= sh.n) return;
-  const int64_t x0 = sh.start(worker), x1 = sh.start(worker + 1);
-  const int ntot = (int)(x1 - x0);
+  int64_t x0 = sh.start(worker);
+  const int64_t x1 = sh.start(worker + 1);
 
   auto sequence_of = [&](int64_t x) {
     int lo = 0, hi = N - 1;
@@ -78,6 +78,26 @@ __global__ void __launch_bounds__(WarpCfg<KVT, NT>::kThreads, WarpCfg<KVT, NT>::
     }
     return lo;
   };
+  // unit x: sequence s, kv-head h, page `pg` of its np private ones (or behind them)
+  auto unit = [&](int64_t x, int& s, int& h, int& pg, int& np) {
+    s = sequence_of(x);
+    const int n = pre[s + 1] - pre[s];
+    const int64_t off = x - (int64_t)pre[s] * H, seg = Shares::div(off, n);
+    h = (int)seg;
+    pg = (int)(off - seg * n);
+    np = n - kSegmentCost;
+  };
+  int s0, h0;
+  {                                     // the first page
+    int pg, np;
+    unit(x0, s0, h0, pg, np);
+    if (pg >= np) {
+      x0 += np + kSegmentCost - pg;
+      if (x0 >= x1) return;
+      unit(x0, s0, h0, pg, np);
+    }
+  }
+  const int ntot = (int)(x1 - x0);
   uint8_t* ring = smem + warp * S * Cfg::kTileBytes;
   uint64_t* full = bars + warp * S;
   uint16_t* scales = reinterpret_cast<uint16_t*>(smem + Cfg::kScOff) + warp * S * 32;
@@ -86,16 +106,15 @@ __global__ void __launch_bounds__(WarpCfg<KVT, NT>::kThreads, WarpCfg<KVT, NT>::
   uint64_t scale_policy = policy;
   if constexpr (Cfg::kRowScaled) scale_policy = l2_evict_last_policy();
 
+  // the page of unit u of the share, and its kv-head: -1 where there is no page
   auto lookup = [&](int u, int& id, int& h) {
     id = 0;
-    h = 0;
+    h = -1;
     if (u >= ntot) return;
-    const int64_t x = x0 + u;
-    const int s = sequence_of(x), np = pre[s + 1] - pre[s];
-    const int64_t off = x - (int64_t)pre[s] * H;
-    const int64_t seg = Shares::div(off, np);
-    const int pg = (int)(off - seg * np);
-    h = (int)seg;
+    int s, pg, np, hs;
+    unit(x0 + u, s, hs, pg, np);
+    if (pg >= np) return;
+    h = hs;
     id = __ldg(p.block_table + (int64_t)s * p.bt_stride + page0[s] + pg);
     if (id < 0 || (int64_t)id >= p.num_pages) report(p.status, PQKV_DEV_PAGE_RANGE);
   };
@@ -125,27 +144,28 @@ __global__ void __launch_bounds__(WarpCfg<KVT, NT>::kThreads, WarpCfg<KVT, NT>::
                                           src + q_off[nt] + k_dim_base<KVT>(t, 2 * k2)))
                                     : make_uint4(0, 0, 0, 0);
   };
-  {                                     // the first segment's, under the look-ups below
-    const int s = sequence_of(x0);
-    fetch_q(s, (int)Shares::div(x0 - (int64_t)pre[s] * H, pre[s + 1] - pre[s]));
-  }
+  fetch_q(s0, h0);                      // the first segment's, under the look-ups below
   int cur_id, cur_h, nxt_id, nxt_h, ubase = 0;
   lookup(lane, cur_id, cur_h);
   lookup(32 + lane, nxt_id, nxt_h);
-  int issued = 0, consumed = 0;
+  int issued = 0, consumed = 0, u = 0;
   auto issue_next = [&]() {
-    const int u = issued;
-    if (u >= ntot) return;
-    if (u - ubase >= 32) {
-      cur_id = nxt_id;
-      cur_h = nxt_h;
-      ubase += 32;
-      lookup(ubase + 32 + lane, nxt_id, nxt_h);
+    int h = -1, at = 0;
+    while (h < 0) {
+      if (u >= ntot) return;
+      if (u - ubase >= 32) {
+        cur_id = nxt_id;
+        cur_h = nxt_h;
+        ubase += 32;
+        lookup(ubase + 32 + lane, nxt_id, nxt_h);
+      }
+      at = u - ubase;
+      h = __shfl_sync(0xffffffffu, cur_h, at);
+      u += 1;
     }
-    const int id = __shfl_sync(0xffffffffu, cur_id, u - ubase);
-    const int h = __shfl_sync(0xffffffffu, cur_h, u - ubase);
+    const int id = __shfl_sync(0xffffffffu, cur_id, at);
     if (lane == 0) {
-      const int stage = u % S;
+      const int stage = issued % S;
       const bool id_ok = id >= 0 && (int64_t)id < p.num_pages;
       if constexpr (Cfg::kRowScaled) {
         // as in the attention kernel: the page's row scales on the tile's barrier
@@ -166,7 +186,7 @@ __global__ void __launch_bounds__(WarpCfg<KVT, NT>::kThreads, WarpCfg<KVT, NT>::
         tma_load_4d(ring + stage * Cfg::kTileBytes, &map, &full[stage], 0, 0, h, id, policy);
       }
     }
-    issued = u + 1;
+    issued += 1;
   };
 #pragma unroll 1
   for (int k = 0; k < S; ++k) issue_next();
@@ -175,10 +195,8 @@ __global__ void __launch_bounds__(WarpCfg<KVT, NT>::kThreads, WarpCfg<KVT, NT>::
   qf.tab = sQ;
   bool dead = false;
   for (int64_t x = x0; x < x1;) {
-    const int s = sequence_of(x), np = pre[s + 1] - pre[s];
-    const int64_t off = x - (int64_t)pre[s] * H;
-    const int h = (int)Shares::div(off, np);
-    const int pg0 = (int)(off - (int64_t)h * np);
+    int s, h, pg0, np;
+    unit(x, s, h, pg0, np);
     const int npg = (int)min((int64_t)(np - pg0), x1 - x);
     const int L = p.plan.len[s], lim_min = L - p.q_len;
     const int key0 = (page0[s] + pg0) * kPageSize;
@@ -336,7 +354,7 @@ __global__ void __launch_bounds__(WarpCfg<KVT, NT>::kThreads, WarpCfg<KVT, NT>::
                                o[2 * k4 + 1][nt][c + 2]);
       }
     __syncwarp();
-    x += npg;
+    x += npg + kSegmentCost;            // (behind x1 where the share ends inside)
   }
   // after a wait that ran out: never leave with a copy in flight
   if (dead && lane == 0)
