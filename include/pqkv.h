@@ -332,7 +332,9 @@ int pqkv_paged_attention_noalloc(const void* q, void* out, const void* pages, in
  * the same arguments (up to the order of the sums).  Shared are the whole pages
  * of min(prefix_lens[g], min over the group of seq_lens[s] - q_len): a prefix
  * that ends inside a page, and the q_len new tokens, stay private.
- * prefix_lens[g] < 16 shares nothing; groups may be empty.
+ * prefix_lens[g] < 16 shares nothing; groups may be empty.  A sequence of a
+ * group without a prefix is what pqkv_paged_attention would make of it, at the
+ * speed of short caches.
  *
  *   q, out, pages, block_table, seq_lens, k_scale, v_scale, status and the
  *   size arguments as in pqkv_paged_attention.
@@ -341,8 +343,11 @@ int pqkv_paged_attention_noalloc(const void* q, void* out, const void* pages, in
  *                   (the result is still right).
  *   prefix_lens     int32 [num_groups] (device); negative, or longer than a
  *                   sequence of the group: PQKV_DEV_SEQ_RANGE, and clamped.
- *   max_seq_len, max_prefix_len  upper bounds of seq_lens and prefix_lens that
- *                   size the launches (0: unknown).  They change speed only.
+ *   max_seq_len, max_prefix_len  upper bounds of seq_lens and prefix_lens
+ *                   (0: unknown).  They size the grids, and no more than
+ *                   max_prefix_len tokens of a prefix are shared (under 16:
+ *                   none, and nothing is launched for them); the result is
+ *                   right whatever they are.
  *   workspace       device scratch of at least
  *                   pqkv_paged_attention_shared_prefix_workspace_size() bytes,
  *                   256-byte aligned.  It needs no initial value and keeps

@@ -476,7 +476,7 @@ def paged_attention_shared_prefix(q, pages, block_table, seq_lens, group_offsets
     [num_groups]) in the same pool pages: their ``block_table`` rows agree over
     the whole pages of that length.  Everything else, and the result, as in
     paged_attention.  ``max_seq_len`` / ``max_prefix_len`` are upper bounds of
-    the lengths (0: unknown) that only size the launches.  The default
+    the lengths (0: unknown) that size the launches.  The default
     workspace is taken from the caching allocator for the call; a uint8 tensor
     of shared_prefix_workspace_size() bytes may be given instead."""
     kd = _dtype_id(kv_dtype)

@@ -107,7 +107,7 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedP
     int pages = 0;
     if (n > 0 && ok) {
       if (want[i] < 0 || want[i] > s_min[g] + p.q_len) report(p.status, PQKV_DEV_SEQ_RANGE);
-      pages = max(0, min(want[i], s_min[g])) / kPageSize;
+      pages = max(0, min(min(want[i], s_min[g]), p.max_prefix)) / kPageSize;
     }
     p.plan.gpages(M)[g] = pages;
     p.plan.goff()[g] = s_off[g];
@@ -387,8 +387,17 @@ cudaError_t launch_shared_prefix(const AttnArgs& a, const SharedArgs& sa, void* 
   p.scale_per_head = a.scale_per_head ? 1 : 0;
   p.pre_rp = lay.pre_rp;
   p.suf_rp = lay.suf_rp;
-  p.pre_workers = lay.pre_workers;
-  p.suf_workers = lay.suf_workers;
+  // no more CTAs than the caller's bounds leave work for
+  const int cap = a.max_pages_per_seq * kPageSize;
+  const int longest = a.max_seq_len > 0 ? std::min(a.max_seq_len, cap) : cap;
+  p.max_prefix = sa.max_prefix_len > 0 ? std::min(sa.max_prefix_len, longest) : longest;
+  const int64_t tiles = (int64_t)(p.max_prefix / kPageSize + kUmmaPages - 1) / kUmmaPages *
+                        (umma_tiles(B * p.rows) + M) * a.num_kv_heads;
+  p.pre_workers = (int)std::min<int64_t>(lay.pre_workers, tiles);
+  const int64_t units = (int64_t)B * a.num_kv_heads *
+                        ((longest + kPageSize - 1) / kPageSize + kSegmentCost);
+  p.suf_workers =
+      (int)std::min<int64_t>(lay.suf_workers, (units / kPrivateShare + 7) / 8 * 8);
   p.split_cost = a.kv_dtype == PQKV_KV_FP8_E4M3 || a.kv_dtype == PQKV_KV_INT8 ? 3 : 2;
   p.sm_scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)a.head_dim));
 

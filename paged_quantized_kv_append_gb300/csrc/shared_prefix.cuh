@@ -61,7 +61,8 @@ struct SharedParams {
   int32_t scale_per_head;
   int32_t pre_rp;           // rows of a prefix fragment's slot
   int32_t suf_rp;           // padded rows of a private fragment
-  int32_t pre_workers;      // CTAs of the prefix launch
+  int32_t max_prefix;       // bound of the prefixes that are shared
+  int32_t pre_workers;      // CTAs of the prefix launch (0: nothing to share, no launch)
   int32_t split_cost;       // of a key tile for a row tile of at most 128 rows; see kFullCost
   int32_t suf_workers;      // warps of the private-key launch
   float sm_scale_log2;      // log2(e) / sqrt(head_dim)

@@ -17,9 +17,9 @@
 // 26 issue the copies of K and V, 25 the products, 27 announces the share's
 // fragments.
 //
-// The running maximum of a row is only raised when a score passes it by more
-// than 8 (probabilities stay <= 2^8 in fp16), so O is rescaled rarely, by the
-// softmax warps themselves, between two products of their stream.
+// A row's reference m follows its largest score loosely (see kRaise), so O is
+// rescaled rarely, by the softmax warps themselves, between two products of their
+// stream.
 #pragma once
 
 #include "shared_private.cuh"
@@ -132,18 +132,7 @@ __device__ __forceinline__ uint32_t tmem_ld1_wait(uint32_t addr) {
 __device__ __forceinline__ void tmem_st1(uint32_t addr, uint32_t v) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(addr), "r"(v) : "memory");
 }
-// 16 columns, for the rare rescale of O beside a row of scores in registers
-__device__ __forceinline__ void tmem_ld16_wait(uint32_t addr, uint32_t* r) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15])
-      : "r"(addr)
-      : "memory");
-}
+// 16 columns
 __device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t* r) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
@@ -154,6 +143,8 @@ __device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t* r) {
       : "r"(addr)
       : "memory");
 }
+// The loads are asynchronous: after the wait, mark the registers as written
+// here, so that nothing that reads them is scheduled before it.
 __device__ __forceinline__ void tmem_landed16(uint32_t* r) {
   asm volatile(""
                : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
@@ -168,8 +159,6 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* r) {
       "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(addr)
       : "memory");
 }
-// The loads are asynchronous: after the wait, mark the registers as written
-// here, so that nothing that reads them is scheduled before it.
 __device__ __forceinline__ void tmem_landed32(uint32_t* r) {
 #define PQKV_IO(i) "+r"(r[i])
   asm volatile("" : PQKV_R32(PQKV_IO)::"memory");
@@ -338,6 +327,35 @@ __device__ __forceinline__ void regs_down() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
+// The two warps of a row meet at a barrier in every step, and a warp whose wait ran out
+// would leave the other there.  So a warp says when it leaves (place -1), and after a
+// wait that ran out (anywhere in the CTA) it only does once the other has left too.
+// Until then it joins the other (in a raise, whose three barriers both pass) when the
+// other says that it joins (place: the step), or has not left for 50 ms: then the other
+// is at the barrier, or will say so at its own next wait.
+static __device__ __noinline__ void leave_pair(volatile int* place, int warp, int pair, int joined,
+                                        volatile int* abort_flag, long long limit) {
+  const int lane = threadIdx.x & 31;
+  const long long t0 = clock64();
+  long long t = t0;
+  for (;;) {
+    const long long now = clock64();
+    int other = *abort_flag && now - t0 < limit ? place[warp ^ 4] : -1;
+    if (other == 0 && now - t > 100000000) other = joined + 1;
+    other = __shfl_sync(0xffffffffu, other, 0);
+    if (other < 0) break;
+    if (other > joined) {
+      joined += 1;
+      if (lane == 0) place[warp] = joined;
+      (void)pair_any(pair, true);
+      pair_sync(pair);
+      pair_sync(pair);
+      if (lane == 0) place[warp] = -1;
+      t = clock64();
+    }
+  }
+}
+
 template <int KVT>
 struct UmmaCfg {
   static constexpr bool kWide = KVT == PQKV_KV_FP16;      // rows need no widening
@@ -367,7 +385,8 @@ struct UmmaCfg {
   // fragments announced by the scheduling warp: a ring of kFrags
   static constexpr int kFrags = 4;
   static constexpr int kReaders = kWide ? 19 : 27;         // warps that read them
-  static constexpr int kFragOff = kBarOff + kBars * 8 + 8;
+  static constexpr int kAtOff = kBarOff + kBars * 8 + 8;   // softmax warps' places, see leave_pair
+  static constexpr int kFragOff = kAtOff + 16 * 4;
   static constexpr int kSmemBytes = kFragOff + kFrags * (int)sizeof(UmmaFrag);
   static_assert(kSmemBytes <= 232448, "shared memory of a block");
   // registers per thread of the softmax, widening and issuing warps, of the
@@ -397,7 +416,7 @@ __global__ void __launch_bounds__(896, 1)
   uint64_t* s_full = bars + 14;        // [stream] scores in TMEM
   uint64_t* p_ready = bars + 16;       // [stream][part] probabilities (32 of a thread's 64 keys)
   uint64_t* o_last = bars + 20;        // [stream] the fragment's last product with V is done
-  uint64_t* drain = bars + 22;         // after a wait that ran out
+  uint64_t* drain = bars + 22;         // all products are done
   uint64_t* frag_full = bars + 24;     // [kFrags]
   uint64_t* frag_empty = bars + 28;    // [kFrags]
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Cfg::kBarOff + Cfg::kBars * 8);
@@ -427,6 +446,7 @@ __global__ void __launch_bounds__(896, 1)
     *abort_flag = 0;
     fence_barrier_init();
   }
+  if (tid < 16) reinterpret_cast<int*>(smem + Cfg::kAtOff)[tid] = 0;
   if (warp == 25) tmem_alloc_512(tmem_slot);
   if (warp == 24 && lane == 0) prefetch_tensormap(&map);
   // No wait for the launch before (the private keys' kernel) here: it reads and
@@ -706,6 +726,10 @@ __global__ void __launch_bounds__(896, 1)
       }
       tc_fence_before();
     }
+    __syncwarp();
+    volatile int* place = reinterpret_cast<volatile int*>(smem + Cfg::kAtOff);
+    if (lane == 0) place[warp] = -1;
+    if (*abort_flag) leave_pair(place, warp, pair, (int)n_step, abort_flag, 2 * Cfg::kWaitCycles);
   } else if (warp < 24) {
     // ================= widen the codes =================
     regs_down<Cfg::kRegWiden>();
@@ -863,8 +887,8 @@ __global__ void __launch_bounds__(896, 1)
       }
       if (ok) frag_done(nf);
     }
-    // after a wait that ran out: no copy may be in flight when the CTA ends
-    if (!ok && lane == 0)
+    // no copy may be in flight when the CTA ends, after a wait that ran out either
+    if (lane == 0)
       for (uint32_t i = n_tile > kStages ? n_tile - kStages : 0; i < n_tile; ++i)
         (void)mbar_wait(full + i % kStages, (i / kStages) & 1);
   } else if (warp == 25) {
@@ -967,10 +991,9 @@ __global__ void __launch_bounds__(896, 1)
       n_tile += nt;
       if (ok) frag_done(nf);
     }
-    if (!ok) {                       // products in flight end before the TMEM is freed
-      if (elect_one()) tc_commit(drain);
-      (void)mbar_wait(drain, 0);
-    }
+    // products in flight end before the TMEM is freed, after a wait that ran out too
+    if (elect_one()) tc_commit(drain);
+    (void)mbar_wait(drain, 0);
   } else {
     // ================= the share's fragments =================
     const Shares sh((int64_t)p.plan.gcost(p.num_groups)[p.num_groups] * H, p.pre_workers, kPrefixShare);
@@ -1004,6 +1027,7 @@ template <int KVT>
 cudaError_t launch_shared_umma_t(const SharedParams& p, const CUtensorMap& map,
                                  cudaStream_t stream) {
   using Cfg = UmmaCfg<KVT>;
+  if (p.pre_workers == 0) return cudaSuccess;
   static std::atomic<uint64_t> done{0};
   const cudaError_t e = opt_in_smem(shared_umma_kernel<KVT>, Cfg::kSmemBytes, done);
   if (e != cudaSuccess) return e;

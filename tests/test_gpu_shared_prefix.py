@@ -51,6 +51,32 @@ def test_groups_of_all_kinds(fmt):
     c.check(c.run(max_seq_len=int(c.lens.max()), max_prefix_len=333), "with bounds")
 
 
+@pytest.mark.parametrize("bounds", [dict(max_prefix_len=15), dict(max_prefix_len=160),
+                                    dict(max_prefix_len=16, max_seq_len=1),
+                                    dict(max_seq_len=100), dict(max_seq_len=1 << 30)])
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_bounds_that_do_not_hold_change_no_result(fmt, bounds):
+    c = SharedCase([(333, [5, 6, 90]), (0, [33]), (700, [20] * 9)], 16, 4, 5, fmt, seed=30)
+    c.check(c.run(**bounds))
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_many_groups_of_every_size(fmt):
+    """More groups than CTAs: a CTA's share spans several of them."""
+    rng = np.random.default_rng(31)
+    groups = [(int(rng.integers(0, 200)), (2 + rng.integers(0, 30, rng.integers(0, 4))).tolist())
+              for _ in range(400)]
+    c = SharedCase(groups, 4, 2, 2, fmt, seed=31)
+    c.check(c.run())
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_sequences_of_one_page_beside_a_long_one(fmt):
+    """Shares of the private keys that hold many segments, one segment, and none."""
+    c = SharedCase([(64, [1] * 150 + [3000] + [1] * 49)], 8, 8, 1, fmt, seed=32)
+    c.check(c.run())
+
+
 @pytest.mark.parametrize("fmt", FORMATS)
 def test_long_private_parts(fmt):
     c = SharedCase([(96, [2000, 1, 700]), (640, [3, 1500])], 8, 2, 1, fmt, seed=4)
