@@ -263,6 +263,60 @@ def test_a_given_workspace_may_hold_anything():
         c.run(workspace=ws.cpu())
 
 
+def test_two_graphs_that_share_a_workspace():
+    """Replayed in turn on one stream, neither finds what the other left."""
+    pq = require_gpu()
+    cases = [SharedCase([(400, [30, 50]), (0, [9])], 8, 2, 5, W.INT8, seed=33),
+             SharedCase([(96, [3] * 40)], 16, 2, 1, W.INT8_ROW, seed=34)]
+    need = max(pq.shared_prefix_workspace_size(len(c.lens), len(c.prefix), c.q_len, c.hq, c.hkv)
+               for c in cases)
+    ws = torch.full((need,), 0xFF, dtype=torch.uint8, device="cuda")
+    outs, graphs = [], []
+    for c in cases:
+        out = torch.empty_like(c.upload()["q"])
+        c.run(out=out, workspace=ws)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            c.run(out=out, workspace=ws)
+        outs.append(out)
+        graphs.append(graph)
+    for _ in range(3):
+        for out, graph in zip(outs, graphs):
+            out.fill_(float("nan"))
+            graph.replay()
+    for c, out in zip(cases, outs):
+        c.check(out)
+
+
+@pytest.mark.parametrize("fmt", [W.FP16, W.INT8_ROW])
+def test_pages_past_four_gigabytes(fmt):
+    pq = require_gpu()
+    c = SharedCase([(150, [20, 33, 5]), (40, [7])], 16, 8, 2, fmt, seed=35)
+    g = c.upload()
+    n, page = g["pages"].shape[0], g["pages"][0].numel() * g["pages"].element_size()
+    top = (1 << 32) // page + 5                       # pages in front of the case's own
+    big = pq.new_pages(top + n, 8, fmt, "cuda")
+    big[top:].copy_(g["pages"])
+    if fmt == W.INT8_ROW:
+        pq.row_scales(big)[top:].copy_(pq.row_scales(g["pages"]))
+    c.check(c.run(pages=big, block_table=torch.where(g["block_table"] >= 0, g["block_table"] + top,
+                                                     g["block_table"])))
+
+
+def test_an_empty_batch_and_the_longest_row():
+    pq = require_gpu()
+    c = SharedCase([(100, [6, 7])], 8, 2, 1, W.FP8_E4M3, seed=36)
+    g = c.upload()
+    none = torch.empty(0, dtype=torch.int32, device="cuda")
+    out = c.run(q=g["q"][:0], out=g["q"][:0].clone(), seq_lens=none, prefix_lens=none,
+                block_table=g["block_table"][:0], group_offsets=torch.zeros_like(g["seq_lens"][:1]))
+    assert out.shape[0] == 0
+    wide = torch.full((2, 524288 // 16), -1, dtype=torch.int32, device="cuda")
+    wide[:, :g["block_table"].shape[1]] = g["block_table"]
+    c.check(c.run(block_table=wide))
+
+
 def test_rows_behind_the_batch_are_left():
     """q and out may be the leading rows of larger buffers."""
     c = SharedCase([(200, [9, 8, 30])], 8, 2, 5, W.FP8_E4M3, seed=31)
