@@ -164,35 +164,35 @@ template <int kWarps>
 __global__ void __launch_bounds__(256) shared_merge_kernel(const SharedParams p, int scaled) {
   __shared__ float4 s_acc[kWarps > 1 ? 8 : 1][32];
   __shared__ float2 s_ml[8];
-  grid_dependency_wait();
-  grid_dependents_launch();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = warp % kWarps;
   const int64_t row = (int64_t)blockIdx.x * (8 / kWarps) + warp / kWarps;
   const int H = p.num_kv_heads, M = p.num_groups;
   const bool in = row < (int64_t)p.num_seqs * p.q_len * p.num_q_heads;
   float top = kNoScore, l = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  int h = 0;
+  int h = 0, n_pre = 0, per = 1, pre_r = 0, total = 0, suf_r = 0;
+  int64_t pre_slot = 0, suf_slot = 0;
   if (in) {
     const int hq = (int)(row % p.num_q_heads);
     const int tok = (int)(row / p.num_q_heads);
     const int s = tok / p.q_len, i = tok % p.q_len, gq = hq % p.group;
     h = hq / p.group;
     const int g = p.plan.group[s];
+    const int a0 = p.plan.spre[s], n = p.plan.spre[s + 1] - a0;
+    const int units = p.plan.spre[p.num_seqs], costs = p.plan.gcost(M)[M];
     // -- the prefix's fragments: CTAs c0 .. c0 + n_pre / per - 1, `per` results each
-    const int np = p.plan.gpages(M)[g];
-    int n_pre = 0, per = 1, pre_r = 0;
-    int64_t pre_slot = 0;
+    const int np = p.plan.gpages(M)[g], first = p.plan.goff()[g];
+    const int behind = p.plan.goff()[g + 1];
+    const int tiles = p.plan.gtiles(M)[g], nt = p.plan.gtiles(M)[g + 1] - tiles;
+    const int cost = p.plan.gcost(M)[g], C = p.plan.gcost(M)[g + 1] - cost;
     if (np > 0) {
-      const int first = p.plan.goff()[g], tiles = p.plan.gtiles(M)[g], cost = p.plan.gcost(M)[g];
-      const int nrows = (p.plan.goff()[g + 1] - first) * p.rows;
+      const int nrows = (behind - first) * p.rows;
       const int R = (s - first) * p.rows + i * p.group + gq;
       const int rt = R / kUmmaRows, T = (np + kUmmaPages - 1) / kUmmaPages;
       const bool dual = nrows - rt * kUmmaRows > 128;
-      const int w = dual ? kFullCost : p.split_cost, nt = p.plan.gtiles(M)[g + 1] - tiles;
-      const int64_t a = (int64_t)cost * H + (int64_t)h * (p.plan.gcost(M)[g + 1] - cost) +
-                        (int64_t)rt * kFullCost * T;
-      const Shares sh((int64_t)p.plan.gcost(M)[M] * H, p.pre_workers, kPrefixShare);
+      const int w = dual ? kFullCost : p.split_cost;
+      const int64_t a = (int64_t)cost * H + (int64_t)h * C + (int64_t)rt * kFullCost * T;
+      const Shares sh((int64_t)costs * H, p.pre_workers, kPrefixShare);
       const int c0 = sh.owner(a);
       per = dual ? 1 : 2;
       n_pre = (sh.owner(a + (int64_t)w * (T - 1)) - c0 + 1) * per;
@@ -200,12 +200,18 @@ __global__ void __launch_bounds__(256) shared_merge_kernel(const SharedParams p,
       pre_r = R % kUmmaRows;
     }
     // -- the private ones
-    const int a0 = p.plan.spre[s], n = p.plan.spre[s + 1] - a0;
     const int64_t a = (int64_t)a0 * H + (int64_t)h * n;
-    const Shares sh((int64_t)p.plan.spre[p.num_seqs] * H, p.suf_workers, kPrivateShare);
-    const int w0 = sh.owner(a), total = n_pre + sh.owner(a + n - kSegmentCost - 1) - w0 + 1;
-    const int64_t suf_slot = (int64_t)s * H + h + w0;
-    const int suf_r = i * p.group + gq;
+    const Shares sh((int64_t)units * H, p.suf_workers, kPrivateShare);
+    const int w0 = sh.owner(a);
+    total = n_pre + sh.owner(a + n - kSegmentCost - 1) - w0 + 1;
+    suf_slot = (int64_t)s * H + h + w0;
+    suf_r = i * p.group + gq;
+  }
+  // What is above reads the plan only, which was there before the prefix's kernel began
+  // (with the wait first, a call took 1 to 2 us longer).
+  grid_dependency_wait();
+  grid_dependents_launch();
+  if (in) {
     for (int k0 = sub; k0 < total; k0 += 4 * kWarps) {
       float m[4], lw[4];
       float4 v[4];
