@@ -83,11 +83,14 @@ enum {
 
 /* Device-side status bits (OR-ed into *status). */
 enum {
-  PQKV_DEV_SLOT_RANGE = 1,    /* append: slot >= num_pages*page_size; token skipped */
-  PQKV_DEV_SEQ_RANGE = 2,     /* attention: seq_len < q_len or beyond its block-table row */
+  PQKV_DEV_SLOT_RANGE = 1,    /* append: slot >= num_pages*page_size; token skipped.
+                                 block tables: the free-page stack ran out or over      */
+  PQKV_DEV_SEQ_RANGE = 2,     /* attention: seq_len < q_len or beyond its block-table row;
+                                 shared prefix, block tables: see there                 */
   PQKV_DEV_BAD_SCALE = 4,     /* a scale is not finite and > 0; work skipped        */
   PQKV_DEV_TIMEOUT = 8,       /* a pipeline wait ran out (about 1 s); outputs invalid */
-  PQKV_DEV_PAGE_RANGE = 16    /* attention: block-table entry outside [0, num_pages); read as zeros */
+  PQKV_DEV_PAGE_RANGE = 16    /* attention: block-table entry outside [0, num_pages); read as
+                                 zeros.  block tables: its token gets no slot           */
 };
 
 /* Largest supported sizes. */

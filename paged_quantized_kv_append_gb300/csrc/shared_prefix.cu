@@ -45,7 +45,9 @@ __device__ __forceinline__ int block_scan(int v, int& total) {
   return before + x - v;
 }
 
-// One block.  The shared pages of group g are the whole pages of
+// One block, 3 us: three dependent rounds of loads and two scans.  Every later kernel
+// needs all of it, so it is worth a launch of its own: repeated by each of 152 CTAs
+// it would cost them the same 3 us.  The shared pages of group g are the whole pages of
 // min(prefix_lens[g], min_s(L_s - q_len)): keys before every query of the
 // group, so no row needs a mask in the prefix, and every sequence keeps at
 // least its q_len new tokens private.
@@ -159,7 +161,11 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedP
 // kWarps warps per output row.  The row's fragments, the prefix's first, are dealt
 // to the row's warps; a warp loads four at once and folds them in with a running
 // maximum, and the warps' results are joined in order (a fixed order throughout,
-// so the result is deterministic).  A lane owns four dims.
+// so the result is deterministic).  A lane owns four dims.  Bound by the latency of its
+// loads out of L2 in three or four waves of blocks: 10240 rows with 8 results each (42
+// MB) take about 10 us behind the prefix's kernel, 18 from cold caches.  A block per
+// sequence and head that walked its rows in one wave was slower (64 x 5: 184 against
+// 178 us): the rows' loads then wait for the join before them.
 template <int kWarps>
 __global__ void __launch_bounds__(256) shared_merge_kernel(const SharedParams p, int scaled) {
   __shared__ float4 s_acc[kWarps > 1 ? 8 : 1][32];

@@ -20,6 +20,17 @@
 // A row's reference m follows its largest score loosely (see kRaise), so O is
 // rescaled rarely, by the softmax warps themselves, between two products of their
 // stream.
+//
+// What bounds it: a stream's chain of scores, softmax and product with V.  The 32
+// products of a tile of 256 rows take 2048 cycles (64 each); a tile takes 2840 for
+// fp16, 3150 for E4M3 and INT8 (whose widening shares the softmax's issue slots) and
+// more for INT8_ROW, which scales its scores; TMEM holds no third stream (128 columns
+// of scores and 128 of O each).  1280 rows a head against 32768 keys of E4M3, 8 heads
+// (172 GFLOP): 134 us from cold caches, 1.3 PFLOP/s; 134 MB of codes are read up to
+// five times, out of L2.  A CTA's first scores begin 6 to 7 us after it does (plan,
+// page ids, copies, widening), its second fragment's 4 us after the first one's last.
+// Slower when measured: the codes fetched by the widening warps themselves, a page
+// prefetch into L2, the products issued by a warp per stream, 64 keys a step.
 #pragma once
 
 #include "shared_private.cuh"
@@ -788,6 +799,9 @@ __global__ void __launch_bounds__(896, 1)
             const int row = i * 16 + (wt >> 3);
             c[i] = lds128u(src + row * 128 + ((j ^ (row & 7)) << 4));
           }
+          // (the fence: the loads above are done before a copy may write there.  Without
+          // it a fast copy, out of L2, overtook loads that the products held up.)
+          fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(&code_empty[kv]);
           // A row's 16 values are chunks 2 (j & 3) and the next of half j >> 2; the

@@ -177,6 +177,52 @@ def test_the_result_is_paged_attentions_and_reproducible():
             assert torch.equal(c.run(), a)
 
 
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("B,q_len,prefix", [(64, 5, 20000), (250, 1, 12000), (24, 8, 40000)])
+def test_long_prefixes_of_many_rows_repeat_and_match(fmt, B, q_len, prefix):
+    """Several row tiles read the same keys out of L2, so that copies are fast and every
+    wait of the pipeline is met; every run gives the same bits, and paged_attention's
+    result.  Both round probabilities (and a row-scaled V) to fp16 and the output once:
+    at most 4 halves of a step of the largest |V| each."""
+    pq = require_gpu()
+    gen = torch.Generator(device="cuda").manual_seed(B)
+    hq, hkv, own = 32, 8, 40
+    shared, width = prefix // 16, -(-(prefix + own) // 16)
+    N = shared + B * (width - shared)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")   # noqa: E731
+    pages = pq.new_pages(N, hkv, fmt, "cuda")
+    x = torch.randn(pages.shape, generator=gen, device="cuda")
+    x *= 1 + 4 * (torch.rand(pages.shape, generator=gen, device="cuda") < 0.01)
+    ks = vs = None
+    if fmt == W.FP16:
+        pages.copy_(x)
+    elif fmt == W.FP8_E4M3:
+        ks = vs = torch.full((1,), 1 / 16, device="cuda")
+        pages.copy_((x * 16).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8))
+    else:
+        pages.copy_((x * 5).round().clamp(-127, 127).to(torch.int8).view(torch.uint8))
+        ks = vs = torch.full((1,), 1 / 5, device="cuda")
+        if fmt == W.INT8_ROW:
+            pq.row_scales(pages).copy_(0.2 * (1 + torch.rand(pq.row_scales(pages).shape,
+                                                             generator=gen, device="cuda")))
+    bt = torch.empty((B, width), dtype=torch.int32, device="cuda")
+    perm = torch.randperm(N, generator=gen, device="cuda").int()
+    bt[:, :shared] = perm[:shared]
+    bt[:, shared:] = perm[shared:].view(B, -1)
+    q = torch.randn((B * q_len, hq, 128), generator=gen, device="cuda").half()
+    sl = prefix + q_len + torch.randint(0, own - q_len, (B,), generator=gen, device="cuda").int()
+    want = pq.paged_attention(q, pages, bt, sl, q_len, fmt, ks, vs, torch.empty_like(q))
+    first = None
+    for k in range(6):
+        out = torch.full_like(q, float("nan"))
+        pq.paged_attention_shared_prefix(q, pages, bt, sl, i32([0, B]), i32([prefix]), q_len, fmt,
+                                         ks, vs, out)
+        first = out if first is None else first
+        assert torch.equal(out, first), "run %d differs" % k
+    top = float(x[:, :, 1].abs().max()) * (2 if fmt == W.INT8_ROW else 1) + 1
+    assert float((first.float() - want.float()).abs().max()) <= 4 * 2.0 ** -11 * top
+
+
 def test_large_scores_and_values():
     """Scores far apart (a running maximum that keeps moving, probabilities
     that vanish) and values near the format's end."""
