@@ -97,7 +97,7 @@ constexpr int kUmmaPages = kUmmaKeys / kPageSize;
 // split_cost.  For E4M3 and INT8, where widening decides a small row tile, 3
 // (cycles per key tile: 2940 against 2350; decode of 256: 109 us, with 2: 112).  For
 // FP16, with nothing to widen (2620 against 1500), and INT8_ROW, whose scores cost the
-// softmax more, 2 (verification of 4 groups: 105 us, with 3: 111).
+// softmax more, 2 (verification of 4 groups: 108 us, with 3: 118).
 constexpr int kFullCost = 4;
 __host__ __device__ __forceinline__ int umma_tiles(int rows) {
   return (rows + kUmmaRows - 1) / kUmmaRows;

@@ -24,7 +24,7 @@
 // What bounds it: a stream's chain of scores, softmax and product with V.  The 32
 // products of a tile of 256 rows take 2048 cycles (64 each); a tile takes 2840 for
 // fp16, 3150 for E4M3 and INT8 (whose widening shares the softmax's issue slots) and
-// more for INT8_ROW, which scales its scores; TMEM holds no third stream (128 columns
+// more for INT8_ROW, which scales scores and probabilities; TMEM holds no third stream (128 columns
 // of scores and 128 of O each).  1280 rows a head against 32768 keys of E4M3, 8 heads
 // (172 GFLOP): 134 us from cold caches, 1.3 PFLOP/s; 134 MB of codes are read up to
 // five times, out of L2.  A CTA's first scores begin 6 to 7 us after it does (plan,
@@ -380,7 +380,8 @@ struct UmmaCfg {
   // scores with outliers a step in three had one with 14 and nothing above, one in
   // seven has now.  Probabilities under 2^-11 of the largest are subnormal in
   // fp16 (steps of 2^-24): each is off by at most 2^-25 in units of l >= 2^-3.
-  static constexpr float kRaise = 15.f, kAbove = 3.f;
+  // Row-scaled V: p times a scale of up to 2^8 has to fit fp16 too.
+  static constexpr float kRaise = kRowScaled ? 8.f : 15.f, kAbove = 3.f;
   static constexpr int kHalf = 128 * 128;                 // 16 KB: 128 rows of 64 values
   static constexpr int kTile = 2 * kHalf;
   static constexpr int kQOff = 0;                         // 2 streams
@@ -389,8 +390,8 @@ struct UmmaCfg {
   static constexpr int kCodeOff = kVOff + 2 * kTile;      // staged codes: slabs of 128 rows
   static constexpr int kSlab = 128 * 128;
   static constexpr int kSlabs = kWide ? 0 : 2;
-  static constexpr int kScOff = kCodeOff + kSlabs * kSlab;  // fp16 row scales of K: 4 stages
-  static constexpr int kScBytes = kRowScaled ? 4 * 128 * 2 : 0;
+  static constexpr int kScOff = kCodeOff + kSlabs * kSlab;  // fp16 row scales: 4 stages of K and V
+  static constexpr int kScBytes = kRowScaled ? 4 * 2 * 128 * 2 : 0;
   static constexpr int kBarOff = kScOff + kScBytes;
   static constexpr int kBars = 4 + 8 + 12 + 8;
   // fragments announced by the scheduling warp: a ring of kFrags
@@ -589,9 +590,9 @@ __global__ void __launch_bounds__(896, 1)
         }
         tc_fence_after();
         if (warp_live) {
-          // INT8_ROW: the keys' fp16 row scales
+          // INT8_ROW: the 64 fp16 scales of K, of V 256 bytes on
           const uint32_t sc = sbase + Cfg::kScOff + half * 128 +
-                              (n_tile + (dual ? i : 2 * i + st)) % 4 * 256;
+                              (n_tile + (dual ? i : 2 * i + st)) % 4 * 512;
           // -- the maximum.  The first 32 scores stay in registers, the others are
           // read again below (registers are short)
           uint32_t s[32];
@@ -650,6 +651,7 @@ __global__ void __launch_bounds__(896, 1)
           // while the others are formed
           const uint64_t scale2 = f2(scale, scale), ref2 = f2(-ref, -ref);
           uint64_t sum[2] = {0, 0};
+          [[maybe_unused]] uint4 vs8;
           uint32_t ph[16];
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
@@ -668,6 +670,15 @@ __global__ void __launch_bounds__(896, 1)
               a = ex2(a);
               b = ex2(b);
               sum[k & 1] = add2(sum[k & 1], f2(a, b));
+              if constexpr (Cfg::kRowScaled) {
+                // p * (V row scale) in fp32, rounded once.  As fp16(code * scale) in
+                // the widening the error grew by a half (for 3 us of 108)
+                if (k % 4 == 0) vs8 = lds128u(sc + 256 + (16 * c + 2 * k) * 2);
+                const uint32_t w = k % 4 == 0 ? vs8.x : k % 4 == 1 ? vs8.y
+                                                      : k % 4 == 2 ? vs8.z : vs8.w;
+                const float2 vs = __half22float2(*reinterpret_cast<const __half2*>(&w));
+                unf2(mul2(f2(a, b), f2(vs.x, vs.y)), a, b);
+              }
               ph[8 * (c & 1) + k] = pack_half2(a, b);
             }
             if (c == 0) tmem_ld16(tS + 32, s);         // lands under the second 16
@@ -751,19 +762,18 @@ __global__ void __launch_bounds__(896, 1)
       uint32_t n_tile = 0;
       bool ok = true;
       const UmmaFrag* f;
-      // INT8_ROW: row scale (fp16 bits, K's or V's) of this lane's token of key
-      // tile u, one of the 32 whose codes its warp widens; 0 behind the prefix and
-      // for pages outside the pool
-      const int tok = (lane >> 2) * 16 + (wt >> 5) * 4 + (lane & 3);
-      auto row_scale = [&](int u) -> uint16_t {
-        const int pg = f->page0 + u * kUmmaPages + tok / kPageSize, rr = tok % kPageSize;
-        if (pg >= f->pages) return 0;
+      // INT8_ROW: K and V row scale (fp16 bits) of this thread's token of key
+      // tile u; 0 behind the prefix and for pages outside the pool
+      auto row_scale = [&](int u) -> ushort2 {
+        const int pg = f->page0 + u * kUmmaPages + wt / kPageSize, rr = wt % kPageSize;
+        if (pg >= f->pages) return make_ushort2(0, 0);
         const int id = __ldg(p.block_table + (int64_t)f->seq0 * p.bt_stride + pg);
-        if (id < 0 || (int64_t)id >= p.num_pages) return 0;
-        return __ldg(reinterpret_cast<const uint16_t*>(p.k_scale) +
-                     (((int64_t)id * H + f->h) * 8 + (rr & 7)) * 4 + (rr >> 3) + 2 * kv);
+        if (id < 0 || (int64_t)id >= p.num_pages) return make_ushort2(0, 0);
+        const uint16_t* from = reinterpret_cast<const uint16_t*>(p.k_scale) +
+                               (((int64_t)id * H + f->h) * 8 + (rr & 7)) * 4 + (rr >> 3);
+        return make_ushort2(__ldg(from), __ldg(from + 2));
       };
-      uint16_t ahead = 0;
+      ushort2 ahead = make_ushort2(0, 0);
       for (uint32_t n = 0; ok; ++n) {
         if (!frag_at(n, f)) break;
         const int nt = f->nt;
@@ -772,23 +782,26 @@ __global__ void __launch_bounds__(896, 1)
         for (int u = 0; u < nt; ++u, ++n_tile) {
           const uint32_t stage = n_tile & 1;
           if constexpr (Cfg::kRowScaled)
-            if (u == 0) ahead = row_scale(0);
+            if (kv == 0 && u == 0) ahead = row_scale(0);
           // the codes have landed and the stage is free: a barrier per lane
           const bool odd = (lane & 1) && n_tile >= 2;
           if (!wait(odd ? empty + stage : &code_full[kv], (odd ? (n_tile >> 1) + 1 : n_tile) & 1)) {
             ok = false;
             break;
           }
-          const uint32_t scale = ahead;
           if constexpr (Cfg::kRowScaled) {
-            // The tile's row scales, a token per lane, read a tile ahead.  K's go to
-            // the softmax, which applies them to the fp32 scores: stage n % 4 was last
-            // read for tile n - 4, whose probabilities went into their product before
-            // the scores of tile n - 2, waited for above, were formed.  V's are
-            // applied below.
-            if (!kv)
-              *reinterpret_cast<uint16_t*>(smem + Cfg::kScOff + n_tile % 4 * 256 + tok * 2) = ahead;
-            if (u + 1 < nt) ahead = row_scale(u + 1);
+            // The tile's row scales, a token per thread, read a tile ahead, for the
+            // softmax, which applies them to the fp32 scores and probabilities (and
+            // may do so before V is widened: so V's come from K's warps as well).
+            // Stage n % 4 was last read for tile n - 4, whose probabilities went into
+            // their product before the scores of tile n - 2, waited for above, were
+            // formed.
+            if (kv == 0) {
+              uint16_t* to = reinterpret_cast<uint16_t*>(smem + Cfg::kScOff + n_tile % 4 * 512);
+              to[wt] = ahead.x;
+              to[128 + wt] = ahead.y;
+              if (u + 1 < nt) ahead = row_scale(u + 1);
+            }
           }
           const uint32_t dst = sbase + (kv ? Cfg::kVOff : Cfg::kKOff) + stage * Cfg::kTile;
           // the slab into registers, and it may be filled again
@@ -818,21 +831,6 @@ __global__ void __launch_bounds__(896, 1)
             dequant_word<KVT>(up ? c[i].w : c[i].y, w[2], w[3]);
             dequant_word<KVT>(up ? c[i].x : c[i].z, w[4], w[5]);
             dequant_word<KVT>(up ? c[i].y : c[i].w, w[6], w[7]);
-            if constexpr (Cfg::kRowScaled) {
-              // V as fp16(code * row scale): one rounding (2^-11 of the value) that
-              // keeps P free of the scales.  On P in fp32, before its own rounding,
-              // they cost the softmax more than its exponentials (6500 cycles a tile
-              // against 3200).
-              if (kv) {
-                const uint32_t r = __shfl_sync(0xffffffffu, scale, i * 4 + (lane >> 3));
-                const __half2 r2 = __half2half2(__ushort_as_half((uint16_t)r));
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                  const __half2 x = __hmul2(*reinterpret_cast<const __half2*>(&w[k]), r2);
-                  w[k] = *reinterpret_cast<const uint32_t*>(&x);
-                }
-              }
-            }
             sts128(at + ((c0 ^ (row & 7)) << 4), w[0], w[1], w[2], w[3]);
             sts128(at + ((c1 ^ (row & 7)) << 4), w[4], w[5], w[6], w[7]);
           }

@@ -117,13 +117,11 @@ class SharedCase:
           above the largest score seen, in log2), so that half a step is 2^-11 p, or
           2^-25 / 2^-3 = 2^-22 among the subnormals: sum max(2^-11 p, 2^-22) |v| / l,
           where l = sum p >= 1;
-          INT8_ROW: over the prefix V is fp16(code * scale), another 2^-11 A with
-          A = sum p |v| / l (or 2^-25 for a subnormal value); over private keys the
-          product p * scale is rounded instead of p, with codes of up to 127: at
-          least 127 * 2^-25 a key, the reference being no score's superior there;
+          INT8_ROW: the product p * scale is rounded instead of p, with codes of up
+          to 127: a subnormal one is off by 127 * 2^-25 / 2^-3 = 127 * 2^-22;
           scores summed in fp32 over 128 products, each sum off by at most
           2^-23 of the products' magnitudes: a relative error d of each
-          probability, 2 d A in the quotient;
+          probability, 2 d A in the quotient, with A = sum p |v| / l;
           sums over the keys and merges in fp32: 2^-18 A;
           the output rounded to fp16: 2^-11 |out|."""
         lens = self.lens if lens is None else lens
@@ -138,7 +136,6 @@ class SharedCase:
                 else:
                     a, b = (x[h] if x.size > 1 else x[0] for x in (self.ks, self.vs))
                     unit = 0.0
-                twice = 2.0 ** -11 if unit else 0.0
                 K, V = oracle.gather_kv(self.pool, self.bt[s], L, h, self.fmt, a, b)
                 x = self.q[s * q_len:(s + 1) * q_len, h * G:(h + 1) * G].astype(np.float64)
                 x = x.reshape(q_len * G, DIM)
@@ -149,9 +146,9 @@ class SharedCase:
                 p = np.exp(z - z.max(1, keepdims=True))
                 l = p.sum(1, keepdims=True)
                 o, A = p @ V / l, p @ np.abs(V) / l
-                t = ((twice + 2.0 ** -18 + 2 * d[:, None]) * A + 2.0 ** -11 * np.abs(o)
+                t = ((2.0 ** -18 + 2 * d[:, None]) * A + 2.0 ** -11 * np.abs(o)
                      + np.maximum(2.0 ** -11 * p, 2.0 ** -22) @ np.abs(V) / l
-                     + 2.0 ** -25 * unit * L / l + 2.0 ** -25)
+                     + 2.0 ** -22 * unit * L / l + 2.0 ** -25)
                 rows = slice(s * q_len, (s + 1) * q_len)
                 out[rows, h * G:(h + 1) * G] = o.reshape(q_len, G, DIM)
                 tol[rows, h * G:(h + 1) * G] = t.reshape(q_len, G, DIM)

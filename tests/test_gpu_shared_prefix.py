@@ -182,8 +182,8 @@ def test_the_result_is_paged_attentions_and_reproducible():
 def test_long_prefixes_of_many_rows_repeat_and_match(fmt, B, q_len, prefix):
     """Several row tiles read the same keys out of L2, so that copies are fast and every
     wait of the pipeline is met; every run gives the same bits, and paged_attention's
-    result.  Both round probabilities (and a row-scaled V) to fp16 and the output once:
-    at most 4 halves of a step of the largest |V| each."""
+    result.  Both round the probabilities and the output to fp16: at most 4 halves of
+    a step of the largest |V|."""
     pq = require_gpu()
     gen = torch.Generator(device="cuda").manual_seed(B)
     hq, hkv, own = 32, 8, 40
