@@ -158,6 +158,60 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedP
   if (tid == 0) p.plan.spre[B] = total_s;
 }
 
+struct MergeRow {
+  int64_t pre_slot, suf_slot;   // its first results
+  int n_pre, per;               // the prefix's results, `per` of a CTA
+  int total;                    // with the private ones; 0: no row
+  int pre_r, suf_r;             // its row in either's
+  int h, out;                   // kv-head, output row
+  int pad;
+};
+
+// What a row has to join.  A thread per row finds it for the row's warps: about 600
+// instructions, mostly divisions, that each warp spent beside some 300 for its sums
+// (64 x 5 rows: 177.9 us a call then, 176.0 now).
+__device__ __forceinline__ MergeRow merge_row(const SharedParams& p, int64_t row) {
+  MergeRow m = {};
+  const int H = p.num_kv_heads, M = p.num_groups;
+  if (row >= (int64_t)p.num_seqs * p.q_len * p.num_q_heads) return m;
+  const int hq = (int)(row % p.num_q_heads);
+  const int tok = (int)(row / p.num_q_heads);
+  const int s = tok / p.q_len, i = tok % p.q_len, gq = hq % p.group;
+  const int h = hq / p.group;
+  m.h = h;
+  m.out = (int)row;
+  const int g = p.plan.group[s];
+  const int a0 = p.plan.spre[s], n = p.plan.spre[s + 1] - a0;
+  const int units = p.plan.spre[p.num_seqs], costs = p.plan.gcost(M)[M];
+  // -- the prefix's fragments: CTAs c0 .. c0 + n_pre / per - 1, `per` results each
+  const int np = p.plan.gpages(M)[g], first = p.plan.goff()[g];
+  const int behind = p.plan.goff()[g + 1];
+  const int tiles = p.plan.gtiles(M)[g], nt = p.plan.gtiles(M)[g + 1] - tiles;
+  const int cost = p.plan.gcost(M)[g], C = p.plan.gcost(M)[g + 1] - cost;
+  if (np > 0) {
+    const int nrows = (behind - first) * p.rows;
+    const int R = (s - first) * p.rows + i * p.group + gq;
+    const int rt = R / kUmmaRows, T = (np + kUmmaPages - 1) / kUmmaPages;
+    const bool dual = nrows - rt * kUmmaRows > 128;
+    const int w = dual ? kFullCost : p.split_cost;
+    const int64_t a = (int64_t)cost * H + (int64_t)h * C + (int64_t)rt * kFullCost * T;
+    const Shares sh((int64_t)costs * H, p.pre_workers, kPrefixShare);
+    const int c0 = sh.owner(a);
+    m.per = dual ? 1 : 2;
+    m.n_pre = (sh.owner(a + (int64_t)w * (T - 1)) - c0 + 1) * m.per;
+    m.pre_slot = (int64_t)tiles * H + h * nt + rt + c0;
+    m.pre_r = R % kUmmaRows;
+  }
+  // -- the private ones
+  const int64_t a = (int64_t)a0 * H + (int64_t)h * n;
+  const Shares sh((int64_t)units * H, p.suf_workers, kPrivateShare);
+  const int w0 = sh.owner(a);
+  m.total = m.n_pre + sh.owner(a + n - kSegmentCost - 1) - w0 + 1;
+  m.suf_slot = (int64_t)s * H + h + w0;
+  m.suf_r = i * p.group + gq;
+  return m;
+}
+
 // kWarps warps per output row.  The row's fragments, the prefix's first, are dealt
 // to the row's warps; a warp loads four at once and folds them in with a running
 // maximum, and the warps' results are joined in order (a fixed order throughout,
@@ -170,55 +224,21 @@ template <int kWarps>
 __global__ void __launch_bounds__(256) shared_merge_kernel(const SharedParams p, int scaled) {
   __shared__ float4 s_acc[kWarps > 1 ? 8 : 1][32];
   __shared__ float2 s_ml[8];
+  __shared__ MergeRow s_row[8 / kWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = warp % kWarps;
-  const int64_t row = (int64_t)blockIdx.x * (8 / kWarps) + warp / kWarps;
-  const int H = p.num_kv_heads, M = p.num_groups;
-  const bool in = row < (int64_t)p.num_seqs * p.q_len * p.num_q_heads;
+  if (threadIdx.x < 8 / kWarps)
+    s_row[threadIdx.x] = merge_row(p, (int64_t)blockIdx.x * (8 / kWarps) + threadIdx.x);
+  __syncthreads();
+  const MergeRow row = s_row[warp / kWarps];
+  const bool in = row.total > 0;
   float top = kNoScore, l = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  int h = 0, n_pre = 0, per = 1, pre_r = 0, total = 0, suf_r = 0;
-  int64_t pre_slot = 0, suf_slot = 0;
-  if (in) {
-    const int hq = (int)(row % p.num_q_heads);
-    const int tok = (int)(row / p.num_q_heads);
-    const int s = tok / p.q_len, i = tok % p.q_len, gq = hq % p.group;
-    h = hq / p.group;
-    const int g = p.plan.group[s];
-    const int a0 = p.plan.spre[s], n = p.plan.spre[s + 1] - a0;
-    const int units = p.plan.spre[p.num_seqs], costs = p.plan.gcost(M)[M];
-    // -- the prefix's fragments: CTAs c0 .. c0 + n_pre / per - 1, `per` results each
-    const int np = p.plan.gpages(M)[g], first = p.plan.goff()[g];
-    const int behind = p.plan.goff()[g + 1];
-    const int tiles = p.plan.gtiles(M)[g], nt = p.plan.gtiles(M)[g + 1] - tiles;
-    const int cost = p.plan.gcost(M)[g], C = p.plan.gcost(M)[g + 1] - cost;
-    if (np > 0) {
-      const int nrows = (behind - first) * p.rows;
-      const int R = (s - first) * p.rows + i * p.group + gq;
-      const int rt = R / kUmmaRows, T = (np + kUmmaPages - 1) / kUmmaPages;
-      const bool dual = nrows - rt * kUmmaRows > 128;
-      const int w = dual ? kFullCost : p.split_cost;
-      const int64_t a = (int64_t)cost * H + (int64_t)h * C + (int64_t)rt * kFullCost * T;
-      const Shares sh((int64_t)costs * H, p.pre_workers, kPrefixShare);
-      const int c0 = sh.owner(a);
-      per = dual ? 1 : 2;
-      n_pre = (sh.owner(a + (int64_t)w * (T - 1)) - c0 + 1) * per;
-      pre_slot = (int64_t)tiles * H + h * nt + rt + c0;
-      pre_r = R % kUmmaRows;
-    }
-    // -- the private ones
-    const int64_t a = (int64_t)a0 * H + (int64_t)h * n;
-    const Shares sh((int64_t)units * H, p.suf_workers, kPrivateShare);
-    const int w0 = sh.owner(a);
-    total = n_pre + sh.owner(a + n - kSegmentCost - 1) - w0 + 1;
-    suf_slot = (int64_t)s * H + h + w0;
-    suf_r = i * p.group + gq;
-  }
   // What is above reads the plan only, which was there before the prefix's kernel began
   // (with the wait first, a call took 1 to 2 us longer).
   grid_dependency_wait();
   grid_dependents_launch();
   if (in) {
-    for (int k0 = sub; k0 < total; k0 += 4 * kWarps) {
+    for (int k0 = sub; k0 < row.total; k0 += 4 * kWarps) {
       float m[4], lw[4];
       float4 v[4];
 #pragma unroll
@@ -227,21 +247,21 @@ __global__ void __launch_bounds__(256) shared_merge_kernel(const SharedParams p,
         m[j] = kNoScore;
         lw[j] = 0.f;
         v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (k < n_pre) {
-          const int64_t slot = pre_slot + k / per;
-          const int r = pre_r + (per > 1 ? (k & 1) * (p.pre_rp / 2) : 0);
+        if (k < row.n_pre) {
+          const int64_t slot = row.pre_slot + (k >> (row.per - 1));
+          const int r = row.pre_r + (row.per > 1 ? (k & 1) * (p.pre_rp / 2) : 0);
           const float* ml = p.pre_ml + slot * 3 * p.pre_rp + r;
           m[j] = __ldg(ml);
           lw[j] = __ldg(ml + p.pre_rp) + __ldg(ml + 2 * p.pre_rp);
           v[j] = __ldg(reinterpret_cast<const float4*>(p.pre_o + (slot * p.pre_rp + r) * kHeadDim) +
                        lane);
-        } else if (k < total) {
-          const int64_t slot = suf_slot + (k - n_pre);
-          const float* ml = p.suf_ml + slot * 2 * p.suf_rp + suf_r;
+        } else if (k < row.total) {
+          const int64_t slot = row.suf_slot + (k - row.n_pre);
+          const float* ml = p.suf_ml + slot * 2 * p.suf_rp + row.suf_r;
           m[j] = __ldg(ml);
           lw[j] = __ldg(ml + p.suf_rp);
           v[j] = __ldg(reinterpret_cast<const float4*>(p.suf_o +
-                                                       (slot * p.suf_rp + suf_r) * kHeadDim) +
+                                                       (slot * p.suf_rp + row.suf_r) * kHeadDim) +
                        lane);
         }
       }
@@ -285,13 +305,13 @@ __global__ void __launch_bounds__(256) shared_merge_kernel(const SharedParams p,
   }
   if (!in) return;
   float inv = l > 0.f ? 1.f / l : 0.f;
-  if (scaled) inv *= __ldg(p.v_scale + (p.scale_per_head ? h : 0));
+  if (scaled) inv *= __ldg(p.v_scale + (p.scale_per_head ? row.h : 0));
   __half2 h01 = __floats2half2_rn(acc.x * inv, acc.y * inv);
   __half2 h23 = __floats2half2_rn(acc.z * inv, acc.w * inv);
   uint2 pk;
   pk.x = *reinterpret_cast<uint32_t*>(&h01);
   pk.y = *reinterpret_cast<uint32_t*>(&h23);
-  *reinterpret_cast<uint2*>(p.out + row * kHeadDim + 4 * lane) = pk;
+  *reinterpret_cast<uint2*>(p.out + (int64_t)row.out * kHeadDim + 4 * lane) = pk;
 }
 
 template <int kWarps>

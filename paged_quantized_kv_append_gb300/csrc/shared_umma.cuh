@@ -672,7 +672,7 @@ __global__ void __launch_bounds__(896, 1)
               sum[k & 1] = add2(sum[k & 1], f2(a, b));
               if constexpr (Cfg::kRowScaled) {
                 // p * (V row scale) in fp32, rounded once.  As fp16(code * scale) in
-                // the widening the error grew by a half (for 3 us of 108)
+                // the widening the error grew by a half (for 3 us of 106)
                 if (k % 4 == 0) vs8 = lds128u(sc + 256 + (16 * c + 2 * k) * 2);
                 const uint32_t w = k % 4 == 0 ? vs8.x : k % 4 == 1 ? vs8.y
                                                       : k % 4 == 2 ? vs8.z : vs8.w;
