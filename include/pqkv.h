@@ -151,7 +151,10 @@ int pqkv_kv_append_quant(const void* k, int64_t k_token_stride, const void* v,
  * num_kv_heads) bytes of the workspace are merge counters: they must be zero
  * before the first call, and every call that returns with *status clean
  * leaves them zero again.  Zero the whole workspace once after allocating it
- * (and again after a call that reported PQKV_DEV_TIMEOUT).
+ * (and again after a call that reported PQKV_DEV_TIMEOUT).  Behind them lie
+ * partial results, so calls with more counters than an earlier one need a
+ * workspace of their own, or one that starts so much earlier that all calls'
+ * counters end at the same byte.
  */
 size_t pqkv_paged_attention_workspace_size(int32_t num_seqs, int32_t q_len,
                                            int32_t num_q_heads, int32_t num_kv_heads,

@@ -255,19 +255,28 @@ def workspace_size(num_seqs, q_len, num_q_heads, num_kv_heads, num_splits=0) -> 
 class Workspace:
     """Zero-initialised device scratch for paged_attention, grown on demand.
 
-    The kernels leave the merge counters at its start zeroed again after every
-    call, so one workspace serves any number of calls on one stream."""
+    The kernels leave the merge counters at a call's start zeroed again after
+    every call, so one workspace serves any number of calls on one stream.  How
+    many counters there are depends on the call's num_seqs and num_kv_heads; the
+    counters of every call end at the same byte, ``head``, so that none has its
+    counters where another has had its partial results."""
 
     def __init__(self, device="cuda"):
         self.device = torch.device(device)
+        self.head = 1 << 18
         self.buf = None
 
-    def get(self, nbytes: int):
+    def get(self, nbytes: int, counter_bytes: int = 0):
+        """``nbytes`` of scratch, the first ``counter_bytes`` of them counters."""
         if nbytes == 0:
             return None
-        if self.buf is None or self.buf.numel() < nbytes:
-            self.buf = torch.zeros(max(nbytes, 1 << 20), dtype=torch.uint8, device=self.device)
-        return self.buf
+        counters = -(-counter_bytes // 256) * 256
+        while self.head < counters:
+            self.head, self.buf = 2 * self.head, None
+        need = self.head - counters + nbytes
+        if self.buf is None or self.buf.numel() < need:
+            self.buf = torch.zeros(max(need, 1 << 20), dtype=torch.uint8, device=self.device)
+        return self.buf[self.head - counters:]
 
 
 _default_ws = {}
@@ -320,7 +329,7 @@ def paged_attention(q, pages, block_table, seq_lens, q_len, kv_dtype, k_scale, v
     need = workspace_size(B, q_len, Hq, H, num_splits)
     if workspace is None:
         workspace = _default_workspace(dev)
-    ws = workspace.get(need) if isinstance(workspace, Workspace) else workspace
+    ws = workspace.get(need, 4 * B * H) if isinstance(workspace, Workspace) else workspace
     _on_device(dev, workspace=ws)
     ws_bytes = 0 if ws is None else ws.numel() * ws.element_size()
     lib = load_library()
@@ -384,7 +393,7 @@ def paged_attention_partial(q, pages, block_table, seq_lens, q_pos, q_len, kv_dt
     need = workspace_size(B, q_len, Hq, H, num_splits)
     if workspace is None:
         workspace = _default_workspace(dev)
-    ws = workspace.get(need) if isinstance(workspace, Workspace) else workspace
+    ws = workspace.get(need, 4 * B * H) if isinstance(workspace, Workspace) else workspace
     _on_device(dev, workspace=ws)
     ws_bytes = 0 if ws is None else ws.numel() * ws.element_size()
     lib = load_library()
