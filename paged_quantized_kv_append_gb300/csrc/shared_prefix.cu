@@ -164,7 +164,6 @@ struct MergeRow {
   int total;                    // with the private ones; 0: no row
   int pre_r, suf_r;             // its row in either's
   int h, out;                   // kv-head, output row
-  int pad;
 };
 
 // What a row has to join.  A thread per row finds it for the row's warps: about 600
@@ -352,7 +351,9 @@ struct SharedLayout {
     sms = std::min(sms, kMaxSms);
     pre_workers = sms;
     suf_workers = sms * private_blocks_per_sm(suf_rp / 8) * 8;
-    const int64_t pre_slots = (int64_t)(umma_tiles(B * rows) + M) * hkv + pre_workers;
+    // (groups without a sequence have no row tile)
+    const int64_t pre_slots =
+        (int64_t)(umma_tiles(B * rows) + std::min(M, B)) * hkv + pre_workers;
     const int64_t suf_slots = (int64_t)B * hkv + suf_workers;
     size_t at = up256((size_t)(4 * (B + 1) + 4 * (M + 1)) * 4);
     auto take = [&](size_t bytes) {
