@@ -225,6 +225,8 @@ __global__ void __launch_bounds__(256) shared_merge_kernel(const SharedParams p,
   __shared__ float2 s_ml[8];
   __shared__ MergeRow s_row[8 / kWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = warp % kWarps;
+  grid_dependency_wait();
+  grid_dependents_launch();
   if (threadIdx.x < 8 / kWarps)
     s_row[threadIdx.x] = merge_row(p, (int64_t)blockIdx.x * (8 / kWarps) + threadIdx.x);
   __syncthreads();
@@ -232,10 +234,6 @@ __global__ void __launch_bounds__(256) shared_merge_kernel(const SharedParams p,
   const bool in = row.total > 0;
   float top = kNoScore, l = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  // What is above reads the plan only, which was there before the prefix's kernel began
-  // (with the wait first, a call took 1 to 2 us longer).
-  grid_dependency_wait();
-  grid_dependents_launch();
   if (in) {
     for (int k0 = sub; k0 < row.total; k0 += 4 * kWarps) {
       float m[4], lw[4];

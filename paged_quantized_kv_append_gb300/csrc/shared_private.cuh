@@ -10,8 +10,9 @@
 // file holds at 24 and 32 rows (a third of the issue slots used, DRAM 25 %, the tensor
 // pipe 20 % of the time).  2168 E4M3 pages x 8 heads for 20 rows (71 MB) take 32 us
 // from cold caches, 1494 fp16 pages x 8 for 32 rows (98 MB) 35.  It runs before the
-// prefix's kernel, whose blocks start on the SMs that it leaves: with the prefix first a
-// call took 9 to 13 us longer (64 x 5 rows: 191 against 182 us).
+// prefix's kernel, whose blocks set themselves up on the SMs that it leaves and then
+// wait for its end: with the prefix first a call took up to 5 us longer (64 x 5 rows:
+// 182 against 179.5 us, 45 x 5 of INT8_ROW 116.5 against 111).
 #pragma once
 
 #include <atomic>
