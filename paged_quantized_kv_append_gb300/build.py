@@ -23,7 +23,7 @@ LIB = os.path.join(HERE, "libpqkv.so")
 SOURCES = ["api.cu", "append.cu", "attention_fp16.cu", "attention_e4m3.cu", "attention_int8.cu",
            "attention_int8row.cu", "attention_waittest.cu", "merge.cu", "noalloc.cu", "tables.cu",
            "shared_prefix.cu", "shared_fp16.cu", "shared_e4m3.cu", "shared_int8.cu",
-           "shared_int8row.cu"]
+           "shared_int8row.cu", "shared_waittest_e4m3.cu", "shared_waittest_fp16.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
          "--expt-relaxed-constexpr"]

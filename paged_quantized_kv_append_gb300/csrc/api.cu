@@ -494,6 +494,38 @@ extern "C" int pqkv_lse_merge(const float* part_o, const float* part_lse, int32_
   return e == cudaSuccess ? PQKV_OK : PQKV_ECUDA;
 }
 
+namespace pqkv {
+
+int bind_shared_prefix(AttnArgs* a, const SharedArgs& sa, const void* out, const void* workspace,
+                       size_t workspace_bytes, const int32_t* status, CUtensorMap* prefix_map,
+                       CUtensorMap* map, int* sms) {
+  int rc = check_output_args(*a, !out || !aligned(out, 16));
+  if (rc) return rc;
+  rc = check_attention_args(*a);
+  if (rc) return rc;
+  if (sa.max_prefix_len < 0) return PQKV_EINVAL;
+  if (a->num_seqs == 0) return PQKV_OK;
+  if (sa.num_groups < 1 || !sa.group_offsets || !sa.prefix_lens || !aligned(sa.group_offsets, 4) ||
+      !aligned(sa.prefix_lens, 4) || !aligned(status, 4))
+    return PQKV_EINVAL;
+  if (sa.num_groups > PQKV_MAX_SEQS) return PQKV_ERANGE;
+  const size_t need = shared_prefix_workspace(a->num_seqs, sa.num_groups, a->q_len, a->num_q_heads,
+                                              a->num_kv_heads);
+  if (!workspace || !aligned(workspace, 256) || workspace_bytes < need) return PQKV_EWORKSPACE;
+  rc = current_device_sms(sms);
+  if (rc) return rc;
+  rc = encode_pool_map(*a, map);
+  if (rc) return rc;
+  rc = encode_prefix_map(*a, prefix_map);
+  if (rc) return rc;
+  if (a->kv_dtype == PQKV_KV_INT8_ROW)   // as in the other attention calls: the scale area
+    a->k_scale = reinterpret_cast<const float*>(
+        row_scale_area(const_cast<void*>(a->pages), a->num_pages, a->num_kv_heads));
+  return PQKV_OK;
+}
+
+}  // namespace pqkv
+
 extern "C" size_t pqkv_paged_attention_shared_prefix_workspace_size(
     int32_t num_seqs, int32_t num_groups, int32_t q_len, int32_t num_q_heads, int32_t num_kv_heads,
     int32_t head_dim) {
@@ -513,31 +545,12 @@ extern "C" int pqkv_paged_attention_shared_prefix(
   AttnArgs a{q, pages, num_pages, block_table, max_pages_per_seq, seq_lens, num_seqs, q_len,
              num_q_heads, num_kv_heads, head_dim, page_size, kv_dtype, k_scale, v_scale,
              scale_per_head, 0, max_seq_len};
-  int rc = check_output_args(a, !out || !aligned(out, 16));
-  if (rc) return rc;
-  rc = check_attention_args(a);
-  if (rc) return rc;
-  if (max_prefix_len < 0) return PQKV_EINVAL;
-  if (num_seqs == 0) return PQKV_OK;
-  if (num_groups < 1 || !group_offsets || !prefix_lens || !aligned(group_offsets, 4) ||
-      !aligned(prefix_lens, 4) || !aligned(status, 4))
-    return PQKV_EINVAL;
-  if (num_groups > PQKV_MAX_SEQS) return PQKV_ERANGE;
-  const size_t need =
-      shared_prefix_workspace(num_seqs, num_groups, q_len, num_q_heads, num_kv_heads);
-  if (!workspace || !aligned(workspace, 256) || workspace_bytes < need) return PQKV_EWORKSPACE;
-  int sms = 0;
-  rc = current_device_sms(&sms);
-  if (rc) return rc;
-  CUtensorMap map, prefix_map;
-  rc = encode_pool_map(a, &map);
-  if (rc) return rc;
-  rc = encode_prefix_map(a, &prefix_map);
-  if (rc) return rc;
-  if (kv_dtype == PQKV_KV_INT8_ROW)   // as in the other attention calls: the scale area
-    a.k_scale = reinterpret_cast<const float*>(
-        row_scale_area(const_cast<void*>(pages), num_pages, num_kv_heads));
   const SharedArgs sa{group_offsets, prefix_lens, num_groups, max_prefix_len};
+  CUtensorMap map, prefix_map;
+  int sms = 0;
+  const int rc = bind_shared_prefix(&a, sa, out, workspace, workspace_bytes, status, &prefix_map,
+                                    &map, &sms);
+  if (rc || num_seqs == 0) return rc;
   return launch_shared_prefix(a, sa, out, prefix_map, map, workspace, sms, status,
                               static_cast<cudaStream_t>(stream)) == cudaSuccess
              ? PQKV_OK

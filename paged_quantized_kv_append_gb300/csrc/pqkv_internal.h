@@ -238,6 +238,12 @@ struct SharedArgs {
 // Bytes of workspace of a shared-prefix call of these (valid) sizes.
 size_t shared_prefix_workspace(int32_t num_seqs, int32_t num_groups, int32_t q_len, int32_t hq,
                                int32_t hkv);
+// Validate a shared-prefix call's arguments and workspace, encode its TMA maps and
+// look up the device's SMs; INT8_ROW: a->k_scale becomes the row-scale area.  Queues
+// nothing.  num_seqs == 0 returns PQKV_OK with nothing filled in.
+int bind_shared_prefix(AttnArgs* a, const SharedArgs& sa, const void* out, const void* workspace,
+                       size_t workspace_bytes, const int32_t* status, CUtensorMap* prefix_map,
+                       CUtensorMap* map, int* sms);
 // Queue the kernels of one validated call.
 cudaError_t launch_shared_prefix(const AttnArgs& a, const SharedArgs& sa, void* out,
                                  const CUtensorMap& prefix_map, const CUtensorMap& map,

@@ -319,19 +319,6 @@ cudaError_t launch_merge_t(const SharedParams& p, int scaled, cudaStream_t strea
                     0, stream, p, scaled);
 }
 
-// Warps per row by the partial results a row may have: one warp folds four in the
-// time of one load, so more warps pay from about eight results on.
-cudaError_t launch_merge(const SharedParams& p, int scaled, cudaStream_t stream) {
-  const int64_t rows = (int64_t)p.num_seqs * p.rows;         // of a kv-head
-  const int64_t segs = (int64_t)umma_tiles((int)rows) * p.num_kv_heads;
-  const int64_t results = (p.pre_workers / segs + 1) * (rows <= 128 ? 2 : 1) +
-                          p.suf_workers / ((int64_t)p.num_seqs * p.num_kv_heads) + 1;
-  if (results > 32) return launch_merge_t<8>(p, scaled, stream);
-  if (results > 16) return launch_merge_t<4>(p, scaled, stream);
-  if (results > 8) return launch_merge_t<2>(p, scaled, stream);
-  return launch_merge_t<1>(p, scaled, stream);
-}
-
 size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
 
 constexpr int kMaxSms = 160;   // the workspace holds the partial results of this many SMs
@@ -369,15 +356,31 @@ struct SharedLayout {
 
 }  // namespace
 
+cudaError_t launch_shared_plan(const SharedParams& p, cudaStream_t stream) {
+  return launch_pdl(shared_plan_kernel, 1, kPlanThreads, 0, stream, p);
+}
+
+// Warps per row by the partial results a row may have: one warp folds four in the
+// time of one load, so more warps pay from about eight results on.
+cudaError_t launch_shared_merge(const SharedParams& p, int kv_dtype, cudaStream_t stream) {
+  const int scaled = kv_dtype == PQKV_KV_FP8_E4M3 || kv_dtype == PQKV_KV_INT8;
+  const int64_t rows = (int64_t)p.num_seqs * p.rows;         // of a kv-head
+  const int64_t segs = (int64_t)umma_tiles((int)rows) * p.num_kv_heads;
+  const int64_t results = (p.pre_workers / segs + 1) * (rows <= 128 ? 2 : 1) +
+                          p.suf_workers / ((int64_t)p.num_seqs * p.num_kv_heads) + 1;
+  if (results > 32) return launch_merge_t<8>(p, scaled, stream);
+  if (results > 16) return launch_merge_t<4>(p, scaled, stream);
+  if (results > 8) return launch_merge_t<2>(p, scaled, stream);
+  return launch_merge_t<1>(p, scaled, stream);
+}
+
 size_t shared_prefix_workspace(int32_t num_seqs, int32_t num_groups, int32_t q_len, int32_t hq,
                                int32_t hkv) {
   return SharedLayout(num_seqs, num_groups, q_len, hq, hkv).total;
 }
 
-cudaError_t launch_shared_prefix(const AttnArgs& a, const SharedArgs& sa, void* out,
-                                 const CUtensorMap& prefix_map, const CUtensorMap& map,
-                                 void* workspace, int sms,
-                                 int32_t* status, cudaStream_t stream) {
+SharedParams shared_params(const AttnArgs& a, const SharedArgs& sa, void* out, void* workspace,
+                           int sms, int32_t* status) {
   const int B = a.num_seqs, M = sa.num_groups;
   const SharedLayout lay(B, M, a.q_len, a.num_q_heads, a.num_kv_heads, sms);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
@@ -431,8 +434,14 @@ cudaError_t launch_shared_prefix(const AttnArgs& a, const SharedArgs& sa, void* 
       (int)std::min<int64_t>(lay.suf_workers, (units / kPrivateShare + 7) / 8 * 8);
   p.split_cost = a.kv_dtype == PQKV_KV_FP8_E4M3 || a.kv_dtype == PQKV_KV_INT8 ? 3 : 2;
   p.sm_scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)a.head_dim));
+  return p;
+}
 
-  cudaError_t e = launch_pdl(shared_plan_kernel, 1, kPlanThreads, 0, stream, p);
+cudaError_t launch_shared_prefix(const AttnArgs& a, const SharedArgs& sa, void* out,
+                                 const CUtensorMap& prefix_map, const CUtensorMap& map,
+                                 void* workspace, int sms, int32_t* status, cudaStream_t stream) {
+  const SharedParams p = shared_params(a, sa, out, workspace, sms, status);
+  cudaError_t e = launch_shared_plan(p, stream);
   if (e != cudaSuccess) return e;
   switch (a.kv_dtype) {
     case PQKV_KV_FP16: e = launch_shared_fp16(p, prefix_map, map, stream); break;
@@ -441,8 +450,7 @@ cudaError_t launch_shared_prefix(const AttnArgs& a, const SharedArgs& sa, void* 
     default: e = launch_shared_int8(p, prefix_map, map, stream); break;
   }
   if (e != cudaSuccess) return e;
-  const int scaled = a.kv_dtype == PQKV_KV_FP8_E4M3 || a.kv_dtype == PQKV_KV_INT8;
-  return launch_merge(p, scaled, stream);
+  return launch_shared_merge(p, a.kv_dtype, stream);
 }
 
 }  // namespace pqkv

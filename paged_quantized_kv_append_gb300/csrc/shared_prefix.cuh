@@ -68,6 +68,15 @@ struct SharedParams {
   float sm_scale_log2;      // log2(e) / sqrt(head_dim)
 };
 
+// Test mode of the bounded waits: one copy is never issued, and waits give up after
+// about 1 ms.  Built only into the testing entry point.
+struct SharedWaitTestParams : SharedParams {
+  int32_t skip_block;       // CTA of the prefix launch, or warp of the private keys' launch
+  int32_t skip_part;        // 0: a key tile of K, 1: of V, 2: a private page
+  int32_t skip_tile;        // which one of the block's (warp's) share
+};
+constexpr long long kTestWaitCycles = 1ll << 21;
+
 // Equal contiguous shares of U units over at most `most` workers, at least
 // `min_share` units each (fewer, larger shares where there is little to do: each
 // share ends in a partial result that the merge has to read).  Every share is
@@ -114,6 +123,13 @@ __host__ __device__ __forceinline__ int umma_weight(int rows, int split_cost) {
 constexpr int kSegmentCost = 2;
 constexpr int kPrivateShare = 2;             // units, the least of a warp
 constexpr int kPrefixShare = kFullCost;      // a key tile, the least of a CTA
+
+// The steps of one validated call: its parameters (queues nothing), the plan and the
+// merge.
+SharedParams shared_params(const AttnArgs& a, const SharedArgs& sa, void* out, void* workspace,
+                           int sms, int32_t* status);
+cudaError_t launch_shared_plan(const SharedParams& p, cudaStream_t stream);
+cudaError_t launch_shared_merge(const SharedParams& p, int kv_dtype, cudaStream_t stream);
 
 // A call's two halves, per KV format (shared_<format>.cu).  prefix_map: see
 // encode_prefix_map; map: the attention's own.

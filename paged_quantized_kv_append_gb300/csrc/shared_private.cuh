@@ -43,10 +43,12 @@ struct WarpCfg {
   static_assert(smem_bytes(PQKV_MAX_SEQS) <= 232448, "shared memory of the largest launch");
 };
 
-template <int KVT, int NT>
+template <int KVT, int NT, class PP = SharedParams>
 __global__ void __launch_bounds__(WarpCfg<KVT, NT>::kThreads, WarpCfg<KVT, NT>::kMinBlocks)
-    private_kernel(const __grid_constant__ CUtensorMap map, const SharedParams p) {
+    private_kernel(const __grid_constant__ CUtensorMap map, const PP p) {
   using Cfg = WarpCfg<KVT, NT>;
+  constexpr bool kWaitTest = std::is_same<PP, SharedWaitTestParams>::value;
+  constexpr uint64_t kLimitNs = kWaitTest ? kTestWaitLimitNs : kWaitLimitNs;
   constexpr int W = Cfg::kW, S = Cfg::kStages, RP = Cfg::kRP;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -173,7 +175,10 @@ __global__ void __launch_bounds__(WarpCfg<KVT, NT>::kThreads, WarpCfg<KVT, NT>::
       u += 1;
     }
     const int id = __shfl_sync(0xffffffffu, cur_id, at);
-    if (lane == 0) {
+    bool copy = true;
+    if constexpr (kWaitTest)
+      copy = worker != p.skip_block || p.skip_part != 2 || issued != p.skip_tile;
+    if (copy && lane == 0) {
       const int stage = issued % S;
       const bool id_ok = id >= 0 && (int64_t)id < p.num_pages;
       if constexpr (Cfg::kRowScaled) {
@@ -241,7 +246,7 @@ __global__ void __launch_bounds__(WarpCfg<KVT, NT>::kThreads, WarpCfg<KVT, NT>::
     for (int j = 0; j < npg; ++j) {
       const int stage = consumed % S;
       if (!dead) {
-        bool ok = mbar_wait(&full[stage], (consumed / S) & 1);
+        bool ok = mbar_wait<kLimitNs>(&full[stage], (consumed / S) & 1);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) {
           dead = true;
@@ -367,18 +372,21 @@ __global__ void __launch_bounds__(WarpCfg<KVT, NT>::kThreads, WarpCfg<KVT, NT>::
   }
   // after a wait that ran out: never leave with a copy in flight
   if (dead && lane == 0)
-    for (int u = consumed; u < issued; ++u) (void)mbar_wait(&full[u % S], (u / S) & 1);
+    for (int u = consumed; u < issued; ++u) {
+      if constexpr (kWaitTest)
+        if (worker == p.skip_block && p.skip_part == 2 && u == p.skip_tile) continue;
+      (void)mbar_wait(&full[u % S], (u / S) & 1);
+    }
 }
 
-template <int KVT, int NT>
-cudaError_t launch_private_t(const SharedParams& p, const CUtensorMap& map,
-                                 cudaStream_t stream) {
+template <int KVT, int NT, class PP>
+cudaError_t launch_private_t(const PP& p, const CUtensorMap& map, cudaStream_t stream) {
   using Cfg = WarpCfg<KVT, NT>;
   static std::atomic<uint64_t> done{0};
-  const cudaError_t e = opt_in_smem(private_kernel<KVT, NT>,
+  const cudaError_t e = opt_in_smem(private_kernel<KVT, NT, PP>,
                                     Cfg::smem_bytes(PQKV_MAX_SEQS), done);
   if (e != cudaSuccess) return e;
-  return launch_pdl(private_kernel<KVT, NT>, p.suf_workers / Cfg::kW, Cfg::kThreads,
+  return launch_pdl(private_kernel<KVT, NT, PP>, p.suf_workers / Cfg::kW, Cfg::kThreads,
                     Cfg::smem_bytes(p.num_seqs), stream, map, p);
 }
 

@@ -338,35 +338,6 @@ __device__ __forceinline__ void regs_down() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-// The two warps of a row meet at a barrier in every step, and a warp whose wait ran out
-// would leave the other there.  So a warp says when it leaves (place -1), and after a
-// wait that ran out (anywhere in the CTA) it only does once the other has left too.
-// Until then it joins the other (in a raise, whose three barriers both pass) when the
-// other says that it joins (place: the step), or has not left for 50 ms: then the other
-// is at the barrier, or will say so at its own next wait.
-static __device__ __noinline__ void leave_pair(volatile int* place, int warp, int pair, int joined,
-                                        volatile int* abort_flag, long long limit) {
-  const int lane = threadIdx.x & 31;
-  const long long t0 = clock64();
-  long long t = t0;
-  for (;;) {
-    const long long now = clock64();
-    int other = *abort_flag && now - t0 < limit ? place[warp ^ 4] : -1;
-    if (other == 0 && now - t > 100000000) other = joined + 1;
-    other = __shfl_sync(0xffffffffu, other, 0);
-    if (other < 0) break;
-    if (other > joined) {
-      joined += 1;
-      if (lane == 0) place[warp] = joined;
-      (void)pair_any(pair, true);
-      pair_sync(pair);
-      pair_sync(pair);
-      if (lane == 0) place[warp] = -1;
-      t = clock64();
-    }
-  }
-}
-
 template <int KVT>
 struct UmmaCfg {
   static constexpr bool kWide = KVT == PQKV_KV_FP16;      // rows need no widening
@@ -397,8 +368,8 @@ struct UmmaCfg {
   // fragments announced by the scheduling warp: a ring of kFrags
   static constexpr int kFrags = 4;
   static constexpr int kReaders = kWide ? 19 : 27;         // warps that read them
-  static constexpr int kAtOff = kBarOff + kBars * 8 + 8;   // softmax warps' places, see leave_pair
-  static constexpr int kFragOff = kAtOff + 16 * 4;
+  static constexpr int kLeftOff = kBarOff + kBars * 8 + 8;  // softmax warps' last meetings
+  static constexpr int kFragOff = kLeftOff + 16 * 4;
   static constexpr int kSmemBytes = kFragOff + kFrags * (int)sizeof(UmmaFrag);
   static_assert(kSmemBytes <= 232448, "shared memory of a block");
   // registers per thread of the softmax, widening and issuing warps, of the
@@ -411,10 +382,12 @@ struct UmmaCfg {
 // ---------------------------------------------------------------------------
 // The kernel
 // ---------------------------------------------------------------------------
-template <int KVT>
+template <int KVT, class PP = SharedParams>
 __global__ void __launch_bounds__(896, 1)
-    shared_umma_kernel(const __grid_constant__ CUtensorMap map, const SharedParams p) {
+    shared_umma_kernel(const __grid_constant__ CUtensorMap map, const PP p) {
   using Cfg = UmmaCfg<KVT>;
+  constexpr bool kWaitTest = std::is_same<PP, SharedWaitTestParams>::value;
+  constexpr long long kWaitCycles = kWaitTest ? kTestWaitCycles : Cfg::kWaitCycles;
   extern __shared__ __align__(1024) uint8_t smem[];       // the swizzle's atoms are 1 KB
   const uint32_t sbase = smem_u32(smem);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Cfg::kBarOff);
@@ -458,7 +431,7 @@ __global__ void __launch_bounds__(896, 1)
     *abort_flag = 0;
     fence_barrier_init();
   }
-  if (tid < 16) reinterpret_cast<int*>(smem + Cfg::kAtOff)[tid] = 0;
+  if (tid < 16) reinterpret_cast<int*>(smem + Cfg::kLeftOff)[tid] = 0;
   if (warp == 25) tmem_alloc_512(tmem_slot);
   if (warp == 24 && lane == 0) prefetch_tensormap(&map);
   // The wait is for the private keys' kernel, of which this one needs nothing but that
@@ -480,7 +453,7 @@ __global__ void __launch_bounds__(896, 1)
     for (uint32_t n = 1;; ++n) {
       if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
       if ((n & 63u) == 0) {
-        const bool late = clock64() - t0 > Cfg::kWaitCycles;
+        const bool late = clock64() - t0 > kWaitCycles;
         if (__any_sync(0xffffffffu, late || *abort_flag)) {
           if (lane == 0) {
             if (!*abort_flag) report(p.status, PQKV_DEV_TIMEOUT);
@@ -512,7 +485,15 @@ __global__ void __launch_bounds__(896, 1)
     // this thread's 64 scores, over them its 64 probabilities, and 64 values of O
     const uint32_t tS = tmem + lane_sel + st * 128 + half * 64;
     const uint32_t tO = tmem + lane_sel + 256 + st * 128 + half * 64;
-    const int pair = 1 + st * 4 + wq;                       // barrier of the row's two warps
+    // Barrier of the row's two warps: meeting k is step k's, if the fragment has a row
+    // for them.  A warp that leaves, for whatever reason, notes the meeting that would
+    // come next, as its last, and joins one more; the other finds the note there and
+    // leaves as well.  A note of a later meeting is not for this one: the other wrote it
+    // after it had passed here.  So every meeting has both warps or is both's last, and a
+    // warp waits at one no longer than the other's own waits last.
+    const int pair = 1 + st * 4 + wq;
+    volatile uint32_t* left = reinterpret_cast<volatile uint32_t*>(smem + Cfg::kLeftOff);
+    bool alone = true;               // the last meeting is still to come
     const uint32_t tPeer = tS + 31 + (half ? -64 : 64);     // the other half's maximum
     uint32_t n_step = 0;             // steps of this stream so far
     uint32_t n_last = 0;             // its fragments with a step
@@ -619,6 +600,11 @@ __global__ void __launch_bounds__(896, 1)
             m2 = max3(fmaxf(m[0], m[1]), m[2], m[3]) * scale;
           }
           if (pair_any(pair, m2 > ref + Cfg::kRaise)) {
+            const uint32_t last = left[warp ^ 4];
+            if (last && last <= n_step + 1) {        // the other warp has left
+              ok = alone = false;
+              break;
+            }
             // -- raise: the two warps tell each other their rows' maxima (over the
             // last of the scores that are in registers) and rescale half of O each.
             // O is still: the last product with V came before these scores
@@ -749,10 +735,11 @@ __global__ void __launch_bounds__(896, 1)
       }
       tc_fence_before();
     }
-    __syncwarp();
-    volatile int* place = reinterpret_cast<volatile int*>(smem + Cfg::kAtOff);
-    if (lane == 0) place[warp] = -1;
-    if (*abort_flag) leave_pair(place, warp, pair, (int)n_step, abort_flag, 2 * Cfg::kWaitCycles);
+    if (alone) {
+      if (lane == 0) left[warp] = n_step + 1;
+      __syncwarp();
+      (void)pair_any(pair, true);
+    }
   } else if (warp < 24) {
     // ================= widen the codes =================
     regs_down<Cfg::kRegWiden>();
@@ -887,7 +874,10 @@ __global__ void __launch_bounds__(896, 1)
         const uint32_t stage = n_tile % kStages;
         ok = n_tile < kStages || wait(empty + stage, (n_tile / kStages + 1) & 1);
         if (!ok) break;
-        if (elect_one()) {
+        bool copy = true;
+        if constexpr (kWaitTest)
+          copy = (int)blockIdx.x != p.skip_block || kv != p.skip_part || (int)n_tile != p.skip_tile;
+        if (copy && elect_one()) {
           mbar_arrive_expect_tx(full + stage, kBytes);
 #pragma unroll
           for (int i = 0; i < kUmmaPages; ++i)
@@ -902,8 +892,11 @@ __global__ void __launch_bounds__(896, 1)
     }
     // no copy may be in flight when the CTA ends, after a wait that ran out either
     if (lane == 0)
-      for (uint32_t i = n_tile > kStages ? n_tile - kStages : 0; i < n_tile; ++i)
+      for (uint32_t i = n_tile > kStages ? n_tile - kStages : 0; i < n_tile; ++i) {
+        if constexpr (kWaitTest)
+          if ((int)blockIdx.x == p.skip_block && kv == p.skip_part && (int)i == p.skip_tile) continue;
         (void)mbar_wait(full + i % kStages, (i / kStages) & 1);
+      }
   } else if (warp == 25) {
     // ================= products =================
     // The streams take turns: a stream's product with V and its next scores, then
@@ -1034,23 +1027,22 @@ __global__ void __launch_bounds__(896, 1)
   if (warp == 25) tmem_free_512(tmem);
 }
 
-template <int KVT>
-cudaError_t launch_shared_umma_t(const SharedParams& p, const CUtensorMap& map,
-                                 cudaStream_t stream) {
+template <int KVT, class PP>
+cudaError_t launch_shared_umma_t(const PP& p, const CUtensorMap& map, cudaStream_t stream) {
   using Cfg = UmmaCfg<KVT>;
   if (p.pre_workers == 0) return cudaSuccess;
   static std::atomic<uint64_t> done{0};
-  const cudaError_t e = opt_in_smem(shared_umma_kernel<KVT>, Cfg::kSmemBytes, done);
+  const cudaError_t e = opt_in_smem(shared_umma_kernel<KVT, PP>, Cfg::kSmemBytes, done);
   if (e != cudaSuccess) return e;
   // the register split needs the 72 registers per thread that the launch
   // bounds allow; a build that used fewer would wait for them forever
   static const int regs = [] {
     cudaFuncAttributes at;
-    return cudaFuncGetAttributes(&at, shared_umma_kernel<KVT>) == cudaSuccess ? at.numRegs : 0;
+    return cudaFuncGetAttributes(&at, shared_umma_kernel<KVT, PP>) == cudaSuccess ? at.numRegs : 0;
   }();
   if (regs < Cfg::kRegLaunch) return cudaErrorLaunchOutOfResources;
-  return launch_pdl(shared_umma_kernel<KVT>, p.pre_workers, Cfg::kThreads, Cfg::kSmemBytes, stream,
-                    map, p);
+  return launch_pdl(shared_umma_kernel<KVT, PP>, p.pre_workers, Cfg::kThreads, Cfg::kSmemBytes,
+                    stream, map, p);
 }
 
 }  // namespace pqkv
