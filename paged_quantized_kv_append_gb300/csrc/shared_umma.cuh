@@ -345,14 +345,16 @@ struct UmmaCfg {
   static constexpr int kThreads = 896;
   static constexpr int kRegLaunch = 72;
   static constexpr long long kWaitCycles = 1ll << 31;     // 1.04 s at 2.07 GHz
-  // A row's reference is raised when a score passes it by more than kRaise (log2),
-  // to kAbove above that score: probabilities stay <= 2^15, within fp16's 2^16, and
-  // between two raises lie 18.  A raise holds its stream up by about 500 cycles; on
-  // scores with outliers a step in three had one with 14 and nothing above, one in
-  // seven has now.  Probabilities under 2^-11 of the largest are subnormal in
-  // fp16 (steps of 2^-24): each is off by at most 2^-25 in units of l >= 2^-3.
-  // Row-scaled V: p times a scale of up to 2^8 has to fit fp16 too.
-  static constexpr float kRaise = kRowScaled ? 8.f : 15.f, kAbove = 3.f;
+  // A row's reference is raised when a score passes it by more than kRaise (log2), to
+  // that score: probabilities stay <= 2^15.9, within fp16's 2^16 (with 8: times a row
+  // scale of V of up to 2^8), and the largest key's is 1 or more.  So each is off by half a
+  // step, 2^-11 of it or, under 2^-14 (INT8_ROW: with its scale), 2^-25 of the largest
+  // at most, as in the other attention calls.  A raise holds its stream up by about 500
+  // cycles.  With the reference 3 above the score they were fewer (64 x 5 rows of scores
+  // with outliers: 181.5 us a call, now 185, with 15 instead of 15.9 186.5), but what a
+  // large score leaves of the others was rounded eight times as coarsely: a tail 2^-22
+  // under it was lost.
+  static constexpr float kRaise = kRowScaled ? 8.f : 15.9f;
   static constexpr int kHalf = 128 * 128;                 // 16 KB: 128 rows of 64 values
   static constexpr int kTile = 2 * kHalf;
   static constexpr int kQOff = 0;                         // 2 streams
@@ -614,7 +616,7 @@ __global__ void __launch_bounds__(896, 1)
             pair_sync(pair);
             tc_fence_after();
             const float both = fmaxf(m2, __uint_as_float(tmem_ld1_wait(tPeer)));
-            const float nref = both > ref + Cfg::kRaise ? both + Cfg::kAbove : ref;
+            const float nref = both > ref + Cfg::kRaise ? both : ref;
             const float fct = ex2(ref - nref);
             ref = nref;
             l *= fct;
