@@ -328,14 +328,14 @@ struct SharedLayout {
   int pre_rp, suf_rp, pre_workers, suf_workers;
   size_t pre_o, pre_ml, suf_o, suf_ml, total;   // offsets
 
-  SharedLayout(int B, int M, int q_len, int hq, int hkv, int sms = kMaxSms) {
+  SharedLayout(int B, int M, int q_len, int hq, int hkv, int kv_dtype, int sms) {
     const int rows = hq / hkv * q_len;
     // a slot holds a row tile, or twice a tile of at most 128 rows
     pre_rp = (int)std::min<int64_t>(kUmmaRows, 2 * (((int64_t)B * rows + 7) / 8 * 8));
     suf_rp = rows_padded(rows);
     sms = std::min(sms, kMaxSms);
     pre_workers = sms;
-    suf_workers = sms * private_blocks_per_sm(suf_rp / 8) * 8;
+    suf_workers = sms * private_blocks_per_sm(kv_dtype, suf_rp / 8) * 8;
     // (groups without a sequence have no row tile)
     const int64_t pre_slots =
         (int64_t)(umma_tiles(B * rows) + std::min(M, B)) * hkv + pre_workers;
@@ -376,13 +376,14 @@ cudaError_t launch_shared_merge(const SharedParams& p, int kv_dtype, cudaStream_
 
 size_t shared_prefix_workspace(int32_t num_seqs, int32_t num_groups, int32_t q_len, int32_t hq,
                                int32_t hkv) {
-  return SharedLayout(num_seqs, num_groups, q_len, hq, hkv).total;
+  // of any format: of one with the most blocks
+  return SharedLayout(num_seqs, num_groups, q_len, hq, hkv, PQKV_KV_INT8, kMaxSms).total;
 }
 
 SharedParams shared_params(const AttnArgs& a, const SharedArgs& sa, void* out, void* workspace,
                            int sms, int32_t* status) {
   const int B = a.num_seqs, M = sa.num_groups;
-  const SharedLayout lay(B, M, a.q_len, a.num_q_heads, a.num_kv_heads, sms);
+  const SharedLayout lay(B, M, a.q_len, a.num_q_heads, a.num_kv_heads, a.kv_dtype, sms);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   SharedParams p = {};
   p.q = static_cast<const uint16_t*>(a.q);

@@ -142,7 +142,12 @@ cudaError_t launch_shared_int8(const SharedParams& p, const CUtensorMap& prefix_
 cudaError_t launch_shared_int8_row(const SharedParams& p, const CUtensorMap& prefix_map,
                                    const CUtensorMap& map, cudaStream_t st);
 
-// blocks per SM of the private-key launch for rows padded to 8 nt
-constexpr int private_blocks_per_sm(int nt) { return nt == 1 ? 2 : 1; }
+// Blocks per SM of the private-key launch for rows padded to 8 nt: two where registers
+// and shared memory hold them (8 rows; an fp16 block's ring takes 128 KB, and a grid of
+// two for an SM that holds one made two waves: 64 fp16 sequences of 4K shared and up to
+// 1K private tokens 75.9 us, with one 71.3).
+constexpr int private_blocks_per_sm(int kv_dtype, int nt) {
+  return nt == 1 && kv_dtype != PQKV_KV_FP16 ? 2 : 1;
+}
 
 }  // namespace pqkv

@@ -25,7 +25,7 @@ namespace pqkv {
 template <int KVT, int NT>
 struct WarpCfg {
   static constexpr int kW = 8;
-  static constexpr int kMinBlocks = NT == 1 ? 2 : 1;
+  static constexpr int kMinBlocks = private_blocks_per_sm(KVT, NT);
   static constexpr int kThreads = kW * 32;
   static constexpr int kTileBytes = (KVT == PQKV_KV_FP16) ? 8192 : 4096;
   static constexpr int kStages = (KVT == PQKV_KV_FP16 || NT == 1) ? 2 : 4;   // per warp
@@ -47,6 +47,8 @@ template <int KVT, int NT, class PP = SharedParams>
 __global__ void __launch_bounds__(WarpCfg<KVT, NT>::kThreads, WarpCfg<KVT, NT>::kMinBlocks)
     private_kernel(const __grid_constant__ CUtensorMap map, const PP p) {
   using Cfg = WarpCfg<KVT, NT>;
+  static_assert(Cfg::kMinBlocks * (Cfg::smem_bytes(PQKV_MAX_SEQS) + 1024) <= 228 * 1024,
+                "the blocks that the launch counts on, with the 1 KB that each takes besides");
   constexpr bool kWaitTest = std::is_same<PP, SharedWaitTestParams>::value;
   constexpr uint64_t kLimitNs = kWaitTest ? kTestWaitLimitNs : kWaitLimitNs;
   constexpr int W = Cfg::kW, S = Cfg::kStages, RP = Cfg::kRP;
