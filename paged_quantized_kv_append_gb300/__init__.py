@@ -486,8 +486,8 @@ def paged_attention_shared_prefix(q, pages, block_table, seq_lens, group_offsets
     the whole pages of that length.  Everything else, and the result, as in
     paged_attention.  ``max_seq_len`` / ``max_prefix_len`` are upper bounds of
     the lengths (0: unknown) that size the launches.  The default
-    workspace is taken from the caching allocator for the call; a uint8 tensor
-    of shared_prefix_workspace_size() bytes may be given instead."""
+    workspace is taken from the caching allocator for the call; a Workspace, or
+    a tensor of shared_prefix_workspace_size() bytes, may be given instead."""
     kd = _dtype_id(kv_dtype)
     _check_pages(pages, kd)
     idx = pages.get_device()
@@ -510,21 +510,26 @@ def paged_attention_shared_prefix(q, pages, block_table, seq_lens, group_offsets
         ks, vs = k_scale.data_ptr(), v_scale.data_ptr()
     if status is not None:
         _check_status(status, pages.device)
-    if workspace is None:
+    ws = workspace
+    if ws is None:
         need = shared_prefix_workspace_size(B, M, q_len, Hq, H)
         if stream is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=pages.device)
+            ws = torch.empty(need, dtype=torch.uint8, device=pages.device)
         else:                            # owned by the stream it is used on
             with torch.cuda.stream(stream):
-                workspace = torch.empty(need, dtype=torch.uint8, device=pages.device)
-    elif workspace.get_device() != idx:
-        raise ValueError("workspace must be on cuda:%d, got %s" % (idx, workspace.device))
+                ws = torch.empty(need, dtype=torch.uint8, device=pages.device)
+    elif isinstance(ws, Workspace):
+        ws = ws.get(shared_prefix_workspace_size(B, M, q_len, Hq, H))
+    if ws is not None and (not isinstance(ws, torch.Tensor) or ws.get_device() != idx
+                           or not ws.is_contiguous()):
+        raise ValueError("workspace must be a Workspace or a contiguous tensor on cuda:%d" % idx)
     rc = _call_on(
         idx, stream, load_library().pqkv_paged_attention_shared_prefix, q.data_ptr(),
         out.data_ptr(), pages.data_ptr(), N, block_table.data_ptr(), W, seq_lens.data_ptr(), B,
         group_offsets.data_ptr(), prefix_lens.data_ptr(), M, q_len, Hq, H, HEAD_DIM, PAGE_SIZE, kd,
-        ks, vs, sph, max_seq_len, max_prefix_len, workspace.data_ptr(),
-        workspace.numel() * workspace.element_size(), None if status is None else status.data_ptr())
+        ks, vs, sph, max_seq_len, max_prefix_len, None if ws is None else ws.data_ptr(),
+        0 if ws is None else ws.numel() * ws.element_size(),
+        None if status is None else status.data_ptr())
     if rc:
         _check(rc, "paged_attention_shared_prefix")
     return out

@@ -42,3 +42,32 @@ def test_batches_of_many_sizes_through_one_workspace(fmt):
         for _ in range(2):
             got = pq.paged_attention(*args, torch.full_like(q, float("nan")), workspace=shared)
             assert torch.equal(got, want), (B, hkv, L)
+
+
+@pytest.mark.gpu
+def test_shared_prefix_attention_takes_a_workspace_like_the_other_calls():
+    """One Workspace for both attention calls in turn, whose merge counters the shared
+    call leaves alone; anything that is no workspace is refused as a ValueError."""
+    require_gpu()
+    from tests.shared_case import SharedCase
+    ws = pq.Workspace("cuda")
+    c = SharedCase([(300, [20, 9, 33]), (0, [40])], 16, 4, 2, W.FP8_E4M3, seed=3)
+    g = c.upload()
+    args = [g[k] for k in ("q", "pages", "block_table", "seq_lens", "q_len", "kv_dtype", "k_scale",
+                           "v_scale")]
+    want, plain = c.run().clone(), pq.paged_attention(*args, torch.empty_like(g["q"]))
+    for _ in range(3):
+        assert torch.equal(c.run(workspace=ws), want)
+        got = pq.paged_attention(*args, torch.full_like(g["q"], float("nan")), workspace=ws)
+        assert torch.equal(got, plain)
+    need = pq.shared_prefix_workspace_size(4, 2, 2, 16, 4)
+    whole = torch.empty(2 * need, dtype=torch.uint8, device="cuda")
+    assert torch.equal(c.run(workspace=whole), want)
+    for bad in (17, "ws", [whole], whole.cpu(), whole[::2], whole.data_ptr()):
+        with pytest.raises(ValueError, match="workspace"):
+            c.run(workspace=bad)
+    with pytest.raises(ValueError, match="size"):            # sizes the call refuses
+        c.run(q=g["q"].repeat(1, 3, 1).contiguous(), out=torch.empty_like(g["q"]).repeat(1, 3, 1),
+              q_len=2, workspace=pq.Workspace("cuda"), group_offsets=torch.zeros(
+                  3000, dtype=torch.int32, device="cuda"),
+              prefix_lens=torch.zeros(2999, dtype=torch.int32, device="cuda"))
