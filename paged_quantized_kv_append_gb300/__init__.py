@@ -265,6 +265,7 @@ class Workspace:
         self.device = torch.device(device)
         self.head = 1 << 18
         self.buf = None
+        self._parts = {}
 
     def get(self, nbytes: int, counter_bytes: int = 0):
         """``nbytes`` of scratch, the first ``counter_bytes`` of them counters."""
@@ -276,7 +277,11 @@ class Workspace:
         need = self.head - counters + nbytes
         if self.buf is None or self.buf.numel() < need:
             self.buf = torch.zeros(max(need, 1 << 20), dtype=torch.uint8, device=self.device)
-        return self.buf[self.head - counters:]
+            self._parts.clear()
+        part = self._parts.get(counters)
+        if part is None:                     # a slice costs a call more than a microsecond
+            part = self._parts[counters] = self.buf[self.head - counters:]
+        return part
 
 
 _default_ws = {}

@@ -22,6 +22,16 @@ def test_the_counters_of_every_call_end_at_the_same_byte():
     assert part.numel() >= 9 << 20 and not part.any()
 
 
+def test_a_call_like_an_earlier_one_makes_no_new_view():
+    """(The attention calls' own path: a slice a call is a microsecond of the host's.)"""
+    ws = pq.Workspace("cpu")
+    a, b = ws.get(9000, 4), ws.get(9000, 4 * 64 * 8)
+    assert ws.get(9000, 4) is a and ws.get(5000, 250) is a and ws.get(9000, 4 * 64 * 8) is b
+    grown = ws.get(8 << 20, 4)                              # a new buffer: no view of the old one
+    assert grown.numel() >= 8 << 20 and grown.data_ptr() == ws.buf.data_ptr() + ws.head - 256
+    assert ws.get(9000, 4 * 64 * 8).data_ptr() == ws.buf.data_ptr() + ws.head - 2048
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("fmt", [W.FP16, W.FP8_E4M3])
 def test_batches_of_many_sizes_through_one_workspace(fmt):
