@@ -458,6 +458,11 @@ def _check_ints(idx, dtype, named):
             _refuse(name, x, dtype, shape, idx)
 
 
+def _size(x, axis=0):
+    """An axis' size, -1 (no tensor's) where there is no such axis."""
+    return x.shape[axis] if x.dim() > axis else -1
+
+
 def _cuda_index(name, x):
     """The device index of a CUDA tensor (the host's cost per call counts: a
     step's bookkeeping is a few microseconds of GPU time)."""
@@ -497,14 +502,12 @@ def paged_attention_shared_prefix(q, pages, block_table, seq_lens, group_offsets
     _check_pages(pages, kd)
     idx = pages.get_device()
     N, H = pages.shape[0], pages.shape[1]
-    B, M = seq_lens.shape[0], prefix_lens.shape[0]
-    Hq = q.shape[1]
-    rows = (B * q_len, Hq, HEAD_DIM)
-    _check_ints(idx, torch.float16, (("q", q, rows), ("out", out, rows)))
-    W = block_table.shape[-1]
+    B, M, W, Hq = _size(seq_lens), _size(prefix_lens), _size(block_table, 1), _size(q, 1)
     _check_ints(idx, torch.int32, (("seq_lens", seq_lens, (B,)), ("block_table", block_table, (B, W)),
                                    ("prefix_lens", prefix_lens, (M,)),
                                    ("group_offsets", group_offsets, (M + 1,))))
+    rows = (B * q_len, Hq, HEAD_DIM)
+    _check_ints(idx, torch.float16, (("q", q, rows), ("out", out, rows)))
     sph, ks, vs = 0, None, None
     if kd in _SCALED:
         sph = _check_scale(k_scale, H, "k_scale")
@@ -555,11 +558,11 @@ def extend_block_tables(seq_lens, new_tokens, block_table, free_pages, free_coun
     ``status``).  ``seq_lens_out`` / ``free_count_out`` may be the inputs
     themselves.  Returns slot_mapping."""
     idx = _cuda_index("block_table", block_table)
-    B, W = seq_lens.shape[0], block_table.shape[-1]
-    T, cap = slot_mapping.shape[0], free_pages.shape[0]
+    B, W = _size(seq_lens), _size(block_table, 1)
+    T, cap = _size(slot_mapping), _size(free_pages)
     row, one = (B,), (1,)
     _check_ints(idx, torch.int32, (
-        ("block_table", block_table, (B, W)), ("seq_lens", seq_lens, row),
+        ("seq_lens", seq_lens, row), ("block_table", block_table, (B, W)),
         ("new_tokens", new_tokens, row), ("free_pages", free_pages, (cap,)),
         ("free_count", free_count, one), ("seq_lens_out", seq_lens_out, row),
         ("free_count_out", free_count_out, one)))
@@ -594,10 +597,10 @@ def truncate_block_tables(seq_lens, keep_lens, block_table, free_pages, free_cou
     changed.  ``seq_lens_out`` / ``free_count_out`` may be the inputs
     themselves.  Returns seq_lens_out."""
     idx = _cuda_index("block_table", block_table)
-    B, W, cap = seq_lens.shape[0], block_table.shape[-1], free_pages.shape[0]
+    B, W, cap = _size(seq_lens), _size(block_table, 1), _size(free_pages)
     row, one = (B,), (1,)
     _check_ints(idx, torch.int32, (
-        ("block_table", block_table, (B, W)), ("seq_lens", seq_lens, row),
+        ("seq_lens", seq_lens, row), ("block_table", block_table, (B, W)),
         ("keep_lens", keep_lens, row), ("free_pages", free_pages, (cap,)),
         ("free_count", free_count, one), ("seq_lens_out", seq_lens_out, row),
         ("free_count_out", free_count_out, one)))
