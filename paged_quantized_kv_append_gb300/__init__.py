@@ -208,8 +208,10 @@ def _check_pages(pages, kd):
 
 
 def _check_scale(x, H, name):
-    if x.dtype != torch.float32 or not x.is_cuda or x.numel() not in (1, H):
-        raise ValueError("%s must be a float32 CUDA tensor of 1 or num_kv_heads elements" % name)
+    if x.dtype != torch.float32 or not x.is_cuda or x.numel() not in (1, H) \
+            or not x.is_contiguous():
+        raise ValueError("%s must be a contiguous float32 CUDA tensor of 1 or num_kv_heads elements"
+                         % name)
     return 1 if (x.numel() == H and H > 1) else 0
 
 
@@ -226,8 +228,9 @@ def kv_append_quant(k, v, slot_mapping, kv_dtype, k_scale, v_scale, pages, statu
         if x.stride(2) != 1 or x.stride(1) != HEAD_DIM or not x.is_cuda:
             raise ValueError("%s: heads and dims must be contiguous on the GPU" % name)
     T = k.shape[0]
-    if v.shape[0] != T or slot_mapping.dtype != torch.int64 or slot_mapping.shape != (T,):
-        raise ValueError("v / slot_mapping do not match k's token count")
+    if v.shape[0] != T or slot_mapping.dtype != torch.int64 or slot_mapping.shape != (T,) \
+            or not slot_mapping.is_contiguous():
+        raise ValueError("v / slot_mapping (contiguous int64) do not match k's token count")
     sph = 0
     if kd in _SCALED:
         sph = _check_scale(k_scale, H, "k_scale")
@@ -313,8 +316,8 @@ def paged_attention(q, pages, block_table, seq_lens, q_len, kv_dtype, k_scale, v
     if out.shape != q.shape or out.dtype != torch.float16 or not out.is_contiguous():
         raise ValueError("out must be contiguous fp16 shaped like q")
     B = seq_lens.shape[0]
-    if seq_lens.dtype != torch.int32 or seq_lens.dim() != 1:
-        raise ValueError("seq_lens must be int32 [num_seqs]")
+    if seq_lens.dtype != torch.int32 or seq_lens.dim() != 1 or not seq_lens.is_contiguous():
+        raise ValueError("seq_lens must be contiguous int32 [num_seqs]")
     if block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.shape[0] != B \
             or not block_table.is_contiguous():
         raise ValueError("block_table must be contiguous int32 [num_seqs, max_pages_per_seq]")
@@ -377,8 +380,8 @@ def paged_attention_partial(q, pages, block_table, seq_lens, q_pos, q_len, kv_dt
         raise ValueError("out_lse must be contiguous fp32 [num_seqs*q_len, Hq]")
     B = seq_lens.shape[0]
     for name, x in (("seq_lens", seq_lens), ("q_pos", q_pos)):
-        if x.dtype != torch.int32 or x.shape != (B,):
-            raise ValueError("%s must be int32 [num_seqs]" % name)
+        if x.dtype != torch.int32 or x.shape != (B,) or not x.is_contiguous():
+            raise ValueError("%s must be contiguous int32 [num_seqs]" % name)
     if block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.shape[0] != B \
             or not block_table.is_contiguous():
         raise ValueError("block_table must be contiguous int32 [num_seqs, max_pages_per_seq]")
@@ -425,8 +428,9 @@ def lse_merge(parts_o, parts_lse, out, out_lse=None, stream=None):
         raise ValueError("parts_lse must be contiguous fp32 [P, rows...]")
     if out.dtype != torch.float16 or not out.is_contiguous() or out.numel() != rows * HEAD_DIM:
         raise ValueError("out must be contiguous fp16 with rows * 128 elements")
-    if out_lse is not None and (out_lse.dtype != torch.float32 or out_lse.numel() != rows):
-        raise ValueError("out_lse must be fp32 with one value per row")
+    if out_lse is not None and (out_lse.dtype != torch.float32 or out_lse.numel() != rows
+                                or not out_lse.is_contiguous()):
+        raise ValueError("out_lse must be contiguous fp32 with one value per row")
     dev = out.device
     _on_device(dev, parts_o=parts_o, parts_lse=parts_lse, out=out, out_lse=out_lse)
     lib = load_library()
@@ -641,8 +645,8 @@ def paged_attention_noalloc(q, pages, block_table, seq_lens, q_len, kv_dtype, k_
     if out.shape != q.shape or out.dtype != torch.float16 or not out.is_contiguous():
         raise ValueError("out must be contiguous fp16 shaped like q")
     B = seq_lens.shape[0]
-    if seq_lens.dtype != torch.int32 or seq_lens.dim() != 1:
-        raise ValueError("seq_lens must be int32 [num_seqs]")
+    if seq_lens.dtype != torch.int32 or seq_lens.dim() != 1 or not seq_lens.is_contiguous():
+        raise ValueError("seq_lens must be contiguous int32 [num_seqs]")
     if block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.shape[0] != B \
             or not block_table.is_contiguous():
         raise ValueError("block_table must be contiguous int32 [num_seqs, max_pages_per_seq]")
