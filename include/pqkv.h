@@ -90,7 +90,8 @@ enum {
   PQKV_DEV_BAD_SCALE = 4,     /* a scale is not finite and > 0; work skipped        */
   PQKV_DEV_TIMEOUT = 8,       /* a pipeline wait ran out (about 1 s); outputs invalid */
   PQKV_DEV_PAGE_RANGE = 16    /* attention: block-table entry outside [0, num_pages); read as
-                                 zeros.  block tables: its token gets no slot           */
+                                 zeros.  extend: a token's page, which gets no slot.  truncate:
+                                 an entry below 0, pushed all the same                     */
 };
 
 /* Largest supported sizes. */
@@ -440,6 +441,9 @@ int pqkv_extend_block_tables(const int32_t* seq_lens, const int32_t* new_tokens,
  * A request with keep < 0, keep > seq_lens[s], or seq_lens[s] beyond its row
  * is left as it is (PQKV_DEV_SEQ_RANGE).  Pages that find no room on the stack
  * (free_count would exceed max_free_pages) are dropped (PQKV_DEV_SLOT_RANGE).
+ * Page ids are pushed as the row has them; one below 0, which no pool has, is
+ * reported (PQKV_DEV_PAGE_RANGE).  The pool's size is not known here: an id
+ * beyond it is reported by the extend that hands it out.
  *
  *   owned_pages  int32 [num_seqs] or NULL (all 0): the row's first page that
  *                belongs to this request; the pages before it are another's

@@ -88,6 +88,8 @@ def truncate(seq_lens, keep_lens, block_table, free_pages, free_count, owned_pag
                 bits |= SLOT_RANGE
                 break
             stack[count] = block_table[s, j]
+            if stack[count] < 0:
+                bits |= PAGE_RANGE
             count += 1
         lens[s] = keep
     return np.array(lens, np.int32), count, stack, bits

@@ -262,13 +262,16 @@ __global__ void __launch_bounds__(kThreads) truncate_tables_kernel(const Truncat
   __syncthreads();                                   // also: every read precedes the next write
   if (state && tid == 0) *p.free_count_out = fc + pushed;
   if (!p.write_pages) return;
+  int bad = 0;
   for (int64_t e64 = (int64_t)blockIdx.x * kThreads + tid; e64 < pushed;
        e64 += (int64_t)gridDim.x * kThreads) {
     const int e = (int)e64;
     const int s = request_of(s_off, B, e);
-    p.free_pages[fc + e] =
-        p.block_table[(int64_t)s * p.max_pages_per_seq + s_first[s] + (e - s_off[s])];
+    const int page = p.block_table[(int64_t)s * p.max_pages_per_seq + s_first[s] + (e - s_off[s])];
+    p.free_pages[fc + e] = page;
+    if (page < 0) bad = 1;
   }
+  if (bad) report(p.status, PQKV_DEV_PAGE_RANGE);
 }
 
 bool overlap(const void* a, size_t an, const void* b, size_t bn) {

@@ -56,3 +56,12 @@ def test_pages_are_neither_lost_nor_held_twice(seed):
         assert bits == 0
         held = [int(table[s, j]) for s in range(B) for j in range(-(-int(lens[s]) // 16))]
         assert sorted(held + stack[:count].tolist()) == list(range(N))
+
+
+def test_truncate_reports_pages_below_zero_where_it_pushes_them():
+    table = np.array([[5, -1, 6]], np.int32)
+    stack = np.zeros(4, np.int32)
+    assert T.truncate([48], [10], table, stack, 0)[1] == 2
+    assert T.truncate([48], [10], table, stack, 0)[3] == T.PAGE_RANGE
+    assert T.truncate([48], [20], table, stack, 0)[3] == 0            # page 1 is kept
+    assert T.truncate([48], [10], table, stack, 0, [2])[3] == 0       # page 1 is another's
