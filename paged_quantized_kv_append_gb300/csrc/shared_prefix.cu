@@ -5,6 +5,7 @@
 #include <cmath>
 
 #include "attention_impl.cuh"
+#include "block_scan.cuh"
 #include "shared_prefix.cuh"
 
 namespace pqkv {
@@ -12,38 +13,6 @@ namespace {
 
 constexpr int kPlanThreads = 512;
 constexpr int kPlanEach = PQKV_MAX_SEQS / kPlanThreads;
-
-__device__ __forceinline__ int last_at_most(const int* a, int n, int x) {
-  int lo = 0, hi = n - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (a[mid] <= x) lo = mid; else hi = mid - 1;
-  }
-  return lo;
-}
-
-// exclusive sum over the block's threads; `total` gets the sum
-__device__ __forceinline__ int block_scan(int v, int& total) {
-  __shared__ int w[kPlanThreads / 32];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int x = v;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int u = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += u;
-  }
-  __syncthreads();
-  if (lane == 31) w[warp] = x;
-  __syncthreads();
-  int before = 0;
-  total = 0;
-#pragma unroll
-  for (int i = 0; i < kPlanThreads / 32; ++i) {
-    if (i == warp) before = total;
-    total += w[i];
-  }
-  return before + x - v;
-}
 
 // One block, 3 us: three dependent rounds of loads and two scans.  Every later kernel
 // needs all of it, so it is worth a launch of its own: repeated by each of 152 CTAs
@@ -119,8 +88,8 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedP
     psum += costs[i];
     s_min[g] = pages;
   }
-  int total_t, total_p;
-  int at_t = block_scan(tsum, total_t), at_p = block_scan(psum, total_p);
+  int at_t = tsum, at_p = psum, total_t, total_p;
+  block_scan2<kPlanThreads>(at_t, at_p, total_t, total_p);
 #pragma unroll
   for (int i = 0; i < kPlanEach; ++i) {
     const int g = tid * gper + i;
@@ -137,14 +106,14 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedP
   }
   __syncthreads();
   // -- the private pages
-  int own = 0, total_s;
+  int at = 0, none = 0, total_s, total_none;
 #pragma unroll
   for (int i = 0; i < kPlanEach; ++i) {
     const int s = tid * per + i;
     if (i >= per || s >= B) continue;
-    own += (len[i] + kPageSize - 1) / kPageSize - s_min[grp[i]] + kSegmentCost;
+    at += (len[i] + kPageSize - 1) / kPageSize - s_min[grp[i]] + kSegmentCost;
   }
-  int at = block_scan(own, total_s);
+  block_scan2<kPlanThreads>(at, none, total_s, total_none);
 #pragma unroll
   for (int i = 0; i < kPlanEach; ++i) {
     const int s = tid * per + i;

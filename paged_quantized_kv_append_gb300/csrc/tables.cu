@@ -29,6 +29,7 @@
 // host's part is about 7.
 #include <algorithm>
 
+#include "block_scan.cuh"
 #include "pqkv_common.cuh"
 
 namespace pqkv {
@@ -40,55 +41,6 @@ static_assert(kPerThread * kThreads == PQKV_MAX_SEQS, "whole requests per thread
 
 __device__ __forceinline__ int page_count(int tokens) {
   return (int)(((unsigned)tokens + (kPageSize - 1)) / kPageSize);
-}
-
-// Exclusive sums over the block's threads of two per-thread values; the totals
-// come back in ta and tb.
-__device__ __forceinline__ void block_scan2(int64_t& a, int& b, int64_t& ta, int& tb) {
-  __shared__ int64_t wa[kThreads / 32];
-  __shared__ int wb[kThreads / 32];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int64_t ia = a;
-  int ib = b;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t ua = __shfl_up_sync(0xffffffffu, ia, o);
-    const int ub = __shfl_up_sync(0xffffffffu, ib, o);
-    if (lane >= o) {
-      ia += ua;
-      ib += ub;
-    }
-  }
-  if (lane == 31) {
-    wa[warp] = ia;
-    wb[warp] = ib;
-  }
-  __syncthreads();
-  int64_t ba = 0;
-  int bb = 0;
-  ta = 0;
-  tb = 0;
-#pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) {
-    if (w == warp) {
-      ba = ta;
-      bb = tb;
-    }
-    ta += wa[w];
-    tb += wb[w];
-  }
-  a = ba + ia - a;
-  b = bb + ib - b;
-}
-
-// The last request whose offset is at most x (offs ascending, offs[0] == 0 <= x).
-__device__ __forceinline__ int request_of(const int* offs, int n, int x) {
-  int lo = 0, hi = n - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (offs[mid] <= x) lo = mid; else hi = mid - 1;
-  }
-  return lo;
 }
 
 __device__ __forceinline__ int checked_count(const int32_t* free_count, int cap, bool tell,
@@ -131,7 +83,7 @@ __global__ void __launch_bounds__(kThreads) extend_tables_kernel(const ExtendPar
     tok += n[i];
     pages += need[i];
   }
-  block_scan2(tok, pages, tok_total, pages_total);
+  block_scan2<kThreads>(tok, pages, tok_total, pages_total);
   const bool tell = first && p.write_tokens, state = first && p.write_state;
   int taken = 0;                                     // pages of this thread's served requests
 #pragma unroll
@@ -182,7 +134,7 @@ __global__ void __launch_bounds__(kThreads) extend_tables_kernel(const ExtendPar
     int64_t slot = -1;
     int pos = -1;
     if (t < live) {
-      const int s = request_of(s_off, B, t);
+      const int s = last_at_most(s_off, B, t);
       const int len = s_len[s];
       if (len >= 0) {
         const int at = len + (t - s_off[s]);
@@ -238,9 +190,8 @@ __global__ void __launch_bounds__(kThreads) truncate_tables_kernel(const Truncat
     gone[i] = max(page_count(L) - from[i], 0);
     pages += gone[i];
   }
-  int64_t unused = 0, unused_total;
-  int total;
-  block_scan2(unused, pages, unused_total, total);
+  int unused = 0, unused_total, total;
+  block_scan2<kThreads>(unused, pages, unused_total, total);
   const int room = p.max_free - fc;                  // places left on the stack
   const int pushed = min(total, room);
   const bool state = first && p.write_state;
@@ -266,7 +217,7 @@ __global__ void __launch_bounds__(kThreads) truncate_tables_kernel(const Truncat
   for (int64_t e64 = (int64_t)blockIdx.x * kThreads + tid; e64 < pushed;
        e64 += (int64_t)gridDim.x * kThreads) {
     const int e = (int)e64;
-    const int s = request_of(s_off, B, e);
+    const int s = last_at_most(s_off, B, e);
     const int page = p.block_table[(int64_t)s * p.max_pages_per_seq + s_first[s] + (e - s_off[s])];
     p.free_pages[fc + e] = page;
     if (page < 0) bad = 1;
