@@ -1,6 +1,7 @@
 // Shared-prefix attention: the plan (which keys are shared, who has how many
 // pages), the merge of the partial results, and the launch of one call.  The
-// attention over the prefix and over the private keys is in shared_prefix.cuh.
+// attention over the prefix is in shared_umma.cuh, over the private keys in
+// shared_private.cuh.
 #include <algorithm>
 #include <cmath>
 
