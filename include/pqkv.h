@@ -175,7 +175,10 @@ size_t pqkv_paged_attention_workspace_size(int32_t num_seqs, int32_t q_len,
  * hq / (num_q_heads / num_kv_heads).  With K_j = dec(kcode_j) * k_scale and
  * V_j = dec(vcode_j) * v_scale:
  *     out[s*q_len + i][hq][:] = sum_j softmax_j(q . K_j / sqrt(head_dim)) V_j
- * computed in fp32 with fp16 tensor-core products, and rounded to fp16.
+ * computed in fp32 with fp16 tensor-core products (probabilities rounded to fp16, each
+ * off by at most 2^-11 of it or 2^-25 of the row's largest; INT8_ROW: their products
+ * with V's row scales), and rounded to fp16.  A V that is not finite in one of the
+ * q_len new tokens also reaches the rows of the queries before it, as 0 times it.
  *
  *   q, out            fp16 [num_seqs*q_len][num_q_heads][head_dim], contiguous.
  *   pages             the pool (layout above), num_pages pages, 16-byte aligned.
@@ -327,8 +330,8 @@ int pqkv_paged_attention_noalloc(const void* q, void* out, const void* pages, in
 /*
  * pqkv_paged_attention_shared_prefix -- pqkv_paged_attention for a batch whose
  * sequences share prefixes (a system prompt, a long document): the keys of a
- * shared prefix are read once for all the sequences that share it, instead of
- * once per sequence.  (ReVolta README, "Quick start": 8 concurrent requests
+ * shared prefix are read once per 256 query rows of a kv-head of the sequences that
+ * share it, instead of once per sequence.  (ReVolta README, "Quick start": 8 concurrent requests
  * with prefix caching; the pages describe no kernel for it.)
  *
  * The sequences come in groups of neighbours: group g holds sequences
@@ -339,9 +342,14 @@ int pqkv_paged_attention_noalloc(const void* q, void* out, const void* pages, in
  * the same arguments (up to the order of the sums).  Shared are the whole pages
  * of min(prefix_lens[g], min over the group of seq_lens[s] - q_len): a prefix
  * that ends inside a page, and the q_len new tokens, stay private.
- * prefix_lens[g] < 16 shares nothing; groups may be empty.  A sequence of a
- * group without a prefix is what pqkv_paged_attention would make of it, at the
- * speed of short caches.
+ * prefix_lens[g] < 16 shares nothing; groups may be empty.
+ * When it pays (one GB300, 32 query heads on 8, one group): a call has four launches,
+ * 24 to 30 us at least, and private keys run at about a quarter of the memory's rate.
+ * Against pqkv_paged_attention on the same tables, decode gains from about 64K tokens
+ * saved on (sequences times prefix; 32K for FP16 pools), verification of 5 positions
+ * from the smallest batches on; below, or with private parts longer than the prefix, a
+ * decode call takes up to 20 us more, and a batch that shares nothing is better off
+ * with pqkv_paged_attention.
  *
  *   q, out, pages, block_table, seq_lens, k_scale, v_scale, status and the
  *   size arguments as in pqkv_paged_attention.

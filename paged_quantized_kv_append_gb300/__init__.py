@@ -492,7 +492,9 @@ def paged_attention_shared_prefix(q, pages, block_table, seq_lens, group_offsets
                                   q_len, kv_dtype, k_scale, v_scale, out, max_seq_len=0,
                                   max_prefix_len=0, workspace=None, status=None, stream=None):
     """paged_attention of a batch whose sequences share prefixes, each prefix's
-    keys read once for all the sequences that share it.
+    keys read once per 256 query rows (of a kv-head) of the sequences that share
+    it.  Decode gains over paged_attention from some 64K tokens saved on
+    (sequences times prefix), verification much earlier: include/pqkv.h.
 
     Sequences ``group_offsets[g]`` .. ``group_offsets[g + 1] - 1`` (int32
     [num_groups + 1]) start with the same ``prefix_lens[g]`` tokens (int32

@@ -138,7 +138,7 @@ struct MergeRow {
 
 // What a row has to join.  A thread per row finds it for the row's warps: about 600
 // instructions, mostly divisions, that each warp spent beside some 300 for its sums
-// (64 x 5 rows: 177.9 us a call then, 176.0 now).
+// (64 x 5 rows: 2 us more a call).
 __device__ __forceinline__ MergeRow merge_row(const SharedParams& p, int64_t row) {
   MergeRow m = {};
   const int H = p.num_kv_heads, M = p.num_groups;
@@ -186,9 +186,9 @@ __device__ __forceinline__ MergeRow merge_row(const SharedParams& p, int64_t row
 // maximum, and the warps' results are joined in order (a fixed order throughout,
 // so the result is deterministic).  A lane owns four dims.  Bound by the latency of its
 // loads out of L2 in three or four waves of blocks: 10240 rows with 8 results each (42
-// MB) take about 10 us behind the prefix's kernel, 18 from cold caches.  A block per
-// sequence and head that walked its rows in one wave was slower (64 x 5: 184 against
-// 178 us): the rows' loads then wait for the join before them.
+// MB) take about 10 us behind the prefix's kernel, 17 from cold caches.  A block per
+// sequence and head that walked its rows in one wave was slower (64 x 5: 6 us): the
+// rows' loads then wait for the join before them.
 template <int kWarps>
 __global__ void __launch_bounds__(256) shared_merge_kernel(const SharedParams p, int scaled) {
   __shared__ float4 s_acc[kWarps > 1 ? 8 : 1][32];

@@ -24,8 +24,8 @@
 // Nothing here is near the memory's rate: the bytes of the largest step (777 prompts,
 // 1.0 M tokens, 12.6 MB of slots and positions) take 1.9 us of it, of the others
 // nothing.  What is left is a launch and the scan's chain of loads and barriers: a call
-// (the next one queued behind it) takes 9.3 us for 8 requests of one token, 9.7 to 12
-// for 2048 of 5, 10.8 for the 777 prompts, 8 to 8.6 for a truncation, of which the
+// (the next one queued behind it) takes 9.7 us for 8 requests of one token, 9.9 to 12
+// for 2048 of 5, 10.8 for the 777 prompts, 8.4 to 8.9 for a truncation, of which the
 // host's part is about 7.
 #include <algorithm>
 
