@@ -350,10 +350,11 @@ struct UmmaCfg {
   // scale of V of up to 2^8), and the largest key's is 1 or more.  So each is off by half a
   // step, 2^-11 of it or, under 2^-14 (INT8_ROW: with its scale), 2^-25 of the largest
   // at most, as in the other attention calls.  A raise holds its stream up by about 500
-  // cycles.  With the reference 3 above the score they were fewer (64 x 5 rows of scores
-  // with outliers: 181.5 us a call, now 185, with 15 instead of 15.9 186.5), but what a
-  // large score leaves of the others was rounded eight times as coarsely: a tail 2^-22
-  // under it was lost.
+  // cycles and takes all rows of its warps to their largest scores, so that they need
+  // none soon (64 x 5 rows of scores with outliers: 181.8 us a call; only the rows that
+  // passed kRaise 185.3, and with 15 186.5).  With the reference 3 above the score it was
+  // 181.5, but what a large score leaves of the others was rounded eight times as
+  // coarsely: a tail 2^-22 under it was lost.
   static constexpr float kRaise = kRowScaled ? 8.f : 15.9f;
   static constexpr int kHalf = 128 * 128;                 // 16 KB: 128 rows of 64 values
   static constexpr int kTile = 2 * kHalf;
@@ -580,7 +581,7 @@ __global__ void __launch_bounds__(896, 1)
           // -- the maximum.  The first 32 scores stay in registers, the others are
           // read again below (registers are short)
           uint32_t s[32];
-          float m2;
+          float top;
           {
             uint32_t v[32];
             tmem_ld32(tS, s);
@@ -599,24 +600,26 @@ __global__ void __launch_bounds__(896, 1)
               m[k & 2] = max3(m[k & 2], __uint_as_float(v[k]), __uint_as_float(v[k + 1]));
               m[1 + (k & 2)] = max3(m[1 + (k & 2)], __uint_as_float(s[k]), __uint_as_float(s[k + 1]));
             }
-            m2 = max3(fmaxf(m[0], m[1]), m[2], m[3]) * scale;
+            top = max3(fmaxf(m[0], m[1]), m[2], m[3]);
           }
-          if (pair_any(pair, m2 > ref + Cfg::kRaise)) {
+          // (the largest exponent as it will be formed below: no probability can be more)
+          if (pair_any(pair, fmaf(top, scale, -ref) > Cfg::kRaise)) {
             const uint32_t last = left[warp ^ 4];
             if (last && last <= n_step + 1) {        // the other warp has left
               ok = alone = false;
               break;
             }
-            // -- raise: the two warps tell each other their rows' maxima (over the
-            // last of the scores that are in registers) and rescale half of O each.
+            // -- raise, of every row to its largest score so far: the two warps tell each
+            // other their rows' maxima (over the last of the scores that are in
+            // registers) and rescale half of O each.
             // O is still: the last product with V came before these scores
-            tmem_st1(tS + 31, __float_as_uint(m2));
+            top *= scale;
+            tmem_st1(tS + 31, __float_as_uint(top));
             tmem_wait_st();
             tc_fence_before();
             pair_sync(pair);
             tc_fence_after();
-            const float both = fmaxf(m2, __uint_as_float(tmem_ld1_wait(tPeer)));
-            const float nref = both > ref + Cfg::kRaise ? both : ref;
+            const float nref = max3(ref, top, __uint_as_float(tmem_ld1_wait(tPeer)));
             const float fct = ex2(ref - nref);
             ref = nref;
             l *= fct;

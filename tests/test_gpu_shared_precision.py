@@ -101,3 +101,38 @@ def test_errors_of_small_values(fmt, v_amp):
             expected2 += (step ** 2 @ V ** 2 / l ** 2 + ulp ** 2).sum() / 12
     ratio = (err2 / expected2) ** 0.5
     assert ratio <= 2.0, "%.3g times the expected rms error" % ratio
+
+
+def test_a_maximum_that_climbs_among_large_scores():
+    """Scores of 2^21 (log2 units; 127 of the 128 products are large), where fp32 holds
+    quarters: the second half of the prefix lies 15.94 above the first, so that whether a
+    row's probabilities still fit fp16 hangs on how its exponents are rounded.  Every
+    output is the second half's V, 1, up to a weight of 2^-15 and fp16's rounding."""
+    pq = require_gpu()
+    B, q_len, hq, hkv, prefix, own = 160, 8, 32, 8, 2048, 11
+    shared = prefix // 16
+    # raw scores: 124 * 362 * 367 + 2 r + 100 + (0 or 125), all whole and under 2^24
+    pages = pq.new_pages(shared + B, hkv, W.FP16, "cuda", fill=0)
+    k = pages[:, :, 0]
+    k[..., :124] = 367.0
+    k[..., 124] = 2.0                                       # varies with the query row
+    k[..., 125] = 1.0
+    k[:shared // 2, ..., 126] = 0.0
+    k[shared // 2:, ..., 126] = 125.0
+    pages[shared // 2:, :, 1] = 1.0
+    q = torch.zeros((B * q_len, hq, 128), dtype=torch.float16, device="cuda")
+    q[..., :124] = 362.0
+    q[..., 124] = torch.arange(B * q_len * hq, device="cuda").view(B * q_len, hq) % 997
+    q[..., 125] = 100.0
+    q[..., 126] = 1.0
+    raw = 124 * 362 * 367 + 2 * 996 + 100 + 125
+    assert raw < 2 ** 24 and raw * np.log2(np.e) / 128 ** 0.5 > 2 ** 21
+    bt = torch.empty((B, shared + 1), dtype=torch.int32, device="cuda")
+    bt[:, :shared] = torch.arange(shared, device="cuda")
+    bt[:, shared] = shared + torch.arange(B, device="cuda")
+    lens = torch.full((B,), prefix + own, dtype=torch.int32, device="cuda")
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")   # noqa: E731
+    out = pq.paged_attention_shared_prefix(q, pages, bt, lens, i32([0, B]), i32([prefix]), q_len,
+                                           W.FP16, None, None, torch.full_like(q, float("nan")))
+    worst = (out.float() - 1).abs().max().item()
+    assert worst <= 2.0 ** -15 + 2.0 ** -11, worst
