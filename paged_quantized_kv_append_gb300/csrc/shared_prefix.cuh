@@ -104,9 +104,9 @@ constexpr int kUmmaPages = kUmmaKeys / kPageSize;
 // kv-head are full ones, then the rest.  A key tile costs a row tile of more than
 // 128 rows kFullCost, a smaller one (half the products, the same codes to widen)
 // split_cost.  For E4M3 and INT8, where widening decides a small row tile, 3
-// (cycles per key tile: 2940 against 2350; decode of 256: 112 us, with 2: 116).  For
+// (cycles per key tile: 2940 against 2350; decode of 256: 111 us, with 2: 116).  For
 // FP16, with nothing to widen (2620 against 1500), and INT8_ROW, whose scores cost the
-// softmax more, 2 (verification of 4 groups: 113 us, with 3: 121).
+// softmax more, 2 (verification of 4 groups: 112 us, with 3: 120).
 constexpr int kFullCost = 4;
 __host__ __device__ __forceinline__ int umma_tiles(int rows) {
   return (rows + kUmmaRows - 1) / kUmmaRows;
@@ -119,7 +119,7 @@ __host__ __device__ __forceinline__ int umma_weight(int rows, int split_cost) {
 // then kSegmentCost that stand for its query rows and its partial result: a share in
 // sequences of one or two private pages holds many segments, and by pages alone one SM
 // worked 99K cycles where the others took 61K (13 us of a call: fp16 verification of
-// 32 x 8; with 1 119.5 us, 2 116.9, 6 117.5, E4M3 decode of 256 114, 112 and 114).
+// 32 x 8; with 1 119 us, 2 116, 6 117, E4M3 decode of 256 113, 111 and 113).
 constexpr int kSegmentCost = 2;
 constexpr int kPrivateShare = 2;             // units, the least of a warp
 constexpr int kPrefixShare = kFullCost;      // a key tile, the least of a CTA
