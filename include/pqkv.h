@@ -342,7 +342,9 @@ int pqkv_paged_attention_noalloc(const void* q, void* out, const void* pages, in
  * the same arguments (up to the order of the sums).  Shared are the whole pages
  * of min(prefix_lens[g], min over the group of seq_lens[s] - q_len): a prefix
  * that ends inside a page, and the q_len new tokens, stay private.
- * prefix_lens[g] < 16 shares nothing; groups may be empty.
+ * prefix_lens[g] < 16 shares nothing; groups may be empty.  One sequence shorter than
+ * the prefix (the padding of a batch, say) cuts what its whole group shares: it belongs
+ * in a group of its own, without a prefix.
  * When it pays (one GB300, 32 query heads on 8, one group): a call has four launches,
  * 24 to 30 us at least, and private keys run at about a quarter of the memory's rate.
  * Against pqkv_paged_attention on the same tables, decode gains from about 64K tokens
