@@ -35,7 +35,6 @@ PAGE = 16
 DIM = 128
 GROUP = 32                       # values that share a scale in a 4-bit pool
 MOST_SCALE = 2720.0              # its largest scale
-FORMATS = {"fp16": 0, "fp8_e4m3": 1, "int8": 2, "int8_row": 3, "int4_group": 4}
 ROW_BYTES = {"fp16": 256, "fp8_e4m3": 128, "int8": 128, "int8_row": 130, "int4_group": 72}
 
 
@@ -115,7 +114,7 @@ def draw(rng):
                        longest, window)
     batch = _log(rng, 1, 256)
     longest = _log(rng, 16, max(64, min(131072, MOST_ROWS // 8 // hkv // batch)))
-    return _read(rng.choice(sorted(FORMATS)), batch, hkv, longest, rng.random() < 0.5)
+    return _read(rng.choice(sorted(ROW_BYTES)), batch, hkv, longest, rng.random() < 0.5)
 
 
 def _case_rng(case):
