@@ -30,6 +30,17 @@
  * V row i and V row i+8 of page p, kv-head h -- the order in which the
  * attention kernel's matrix fragments consume them.  That is 64 bytes per
  * (page, kv-head); the allocation is num_pages*num_kv_heads*4160 bytes.
+ * PQKV_KV_INT4_GROUP pools hold 4-bit codes with an fp16 scale per group of 32
+ * consecutive values of a row:
+ *   pages[num_pages][num_kv_heads][2][1152 bytes]
+ * (0.5625 of an 8-bit pool).  Of the 1152 bytes of a K or V tile the first 1024
+ * are codes, 64 bytes a row: row r's group c is the 16-byte chunk
+ * (4 (r % 2) + c) ^ (0, 5, 2, 7)[i % 4] of the 128-byte line i = r / 2.  Value
+ * 8 w + 2 f + e of the group is in 32-bit word w of the chunk, half e, field f:
+ * the bits of code + 8 at 6-9, 2-5, 10-13, and (lowest first) 14, 15, 0, 1 of the half
+ * for f = 0 .. 3.  Behind them: fp16 scale[4 groups][16 rows].  A page is
+ * contiguous with its scales, so pages may be copied as they are; tokens are
+ * taken out again by pqkv_kv_read.
  *
  * Conventions for every entry point:
  *   - All tensor arguments are DEVICE pointers owned by the caller.  Nothing
@@ -64,11 +75,15 @@ typedef enum {
   PQKV_KV_FP16 = 0,     /* fp16 values, scales ignored                          */
   PQKV_KV_FP8_E4M3 = 1, /* OCP E4M3 ("FN": max 448, no Inf), value = dec(c)*scale */
   PQKV_KV_INT8 = 2,     /* symmetric int8 in [-127, 127], value = c*scale         */
-  PQKV_KV_INT8_ROW = 3  /* int8 with its own scale per (token, kv-head) row of K
+  PQKV_KV_INT8_ROW = 3, /* int8 with its own scale per (token, kv-head) row of K
                            and of V, computed when the row is written (ReVolta
                            README, "Weight and KV formats", "INT8 KV": scales
                            derived from the data at run time, no calibration);
                            value = c * row_scale.  Scale area: see the layout. */
+  PQKV_KV_INT4_GROUP = 5 /* 4-bit codes in [-7, 7] with an fp16 scale per group of 32
+                           consecutive values of a (token, kv-head) row, computed
+                           when the row is written; value = c * scale.  (No counterpart
+                           on the ReVolta pages.  4 is not a format.) */
 } pqkv_kv_dtype;
 
 /* Host-side return codes. */
@@ -125,6 +140,12 @@ enum {
  * gives 0/0 = NaN -> code 0 and +-x/0 -> +-127, all worth 0.  k_scale /
  * v_scale are ignored (may be NULL).  V rows with amax above 32512 exceed what the attention kernel's
  * fp16 products hold (probability <= 256 times the row scale).
+ * INT4_GROUP: for each group of 32 values the scale s = min(fp16(bf16(amax/7)), 2720),
+ * amax the largest |x| of the group (NaNs ignored, at most 65504) and bf16 and fp16
+ * the roundings to nearest even, is stored in its tile; the codes are
+ * fp32(x)/s rounded half to even and clamped to [-7, 7] (NaN -> 0; all 0 for s = 0).
+ * A scale has 8 significant bits, so every value code * s is an fp16 value.
+ * Values beyond +-19040 saturate.  k_scale / v_scale are ignored (may be NULL).
  *
  *   k, v            fp16 [num_tokens][num_kv_heads][head_dim]; heads and dims
  *                   contiguous, tokens `k_token_stride` / `v_token_stride`
@@ -143,6 +164,45 @@ int pqkv_kv_append_quant(const void* k, int64_t k_token_stride, const void* v,
                          int32_t kv_dtype, const float* k_scale, const float* v_scale,
                          int32_t scale_per_head, void* pages, int64_t num_pages,
                          int32_t page_size, int32_t* status, void* stream);
+
+/*
+ * pqkv_kv_read -- the tokens of requests out of the pool, as contiguous fp16
+ * rows: a request's cached context for a dense attention over it (the chunk of a
+ * prompt that follows), or on its way to another pool, format or machine.  (The
+ * ReVolta pages describe no such kernel.)
+ *
+ * For request s and token_offsets[s] <= t < token_offsets[s+1], with
+ * pos = first_pos[s] + t - token_offsets[s], row t of k and of v receives the
+ * values of the request's token pos, kv-heads and dims in order:
+ *   FP16        the bits;
+ *   E4M3, INT8  fp16(fp32(dec(code) * scale));
+ *   INT8_ROW    fp16(code * row scale), rounded once;
+ *   INT4_GROUP  code * group scale, exact.
+ * Rows behind token_offsets[num_seqs] are left as they are.  So are rows whose
+ * pos lies outside the request's block-table row (PQKV_DEV_SEQ_RANGE) or whose
+ * scale is not finite and > 0 (PQKV_DEV_BAD_SCALE).  A block-table entry outside
+ * [0, num_pages) reads as zeros (PQKV_DEV_PAGE_RANGE).  token_offsets that do
+ * not start at 0, fall, or end beyond num_tokens are reported
+ * (PQKV_DEV_SEQ_RANGE); then which rows are written is unspecified, but no
+ * others than the num_tokens rows of k and v.
+ *
+ *   block_table    int32 [num_seqs][max_pages_per_seq].
+ *   first_pos      int32 [num_seqs] or NULL (all 0): the first position read.
+ *   token_offsets  int32 [num_seqs+1] (as pqkv_extend_block_tables writes them).
+ *   k, v           fp16 [num_tokens][num_kv_heads][head_dim]; tokens
+ *                  `k_token_stride` / `v_token_stride` ELEMENTS apart
+ *                  (>= num_kv_heads*head_dim, multiples of 16), so they may be
+ *                  column slices of a wider buffer.  32-byte aligned.
+ *   k_scale, v_scale, scale_per_head  as in pqkv_kv_append_quant.
+ * num_seqs <= 2048, head_dim == 128, page_size == 16, pages 16-byte aligned.
+ * num_seqs == 0 or num_tokens == 0 is a no-op.  Stateless: no workspace.
+ */
+int pqkv_kv_read(const void* pages, int64_t num_pages, const int32_t* block_table,
+                 int32_t max_pages_per_seq, const int32_t* first_pos, const int32_t* token_offsets,
+                 int32_t num_seqs, int32_t num_tokens, int32_t num_kv_heads, int32_t head_dim,
+                 int32_t page_size, int32_t kv_dtype, const float* k_scale, const float* v_scale,
+                 int32_t scale_per_head, void* k, int64_t k_token_stride, void* v,
+                 int64_t v_token_stride, int32_t* status, void* stream);
 
 /*
  * pqkv_paged_attention_workspace_size -- bytes of device workspace that
@@ -185,8 +245,8 @@ size_t pqkv_paged_attention_workspace_size(int32_t num_seqs, int32_t q_len,
  *   block_table       int32 [num_seqs][max_pages_per_seq]: the pool page of
  *                     each logical 16-token page of the sequence.
  *   seq_lens          int32 [num_seqs] (device), q_len <= L <= max_pages_per_seq*16.
- *   k_scale, v_scale  fp32 [1] or [num_kv_heads] (device); ignored for FP16
- *                     and INT8_ROW (whose K_j, V_j use the row scales stored
+ *   k_scale, v_scale  fp32 [1] or [num_kv_heads] (device); ignored for FP16,
+ *                     INT8_ROW and INT4_GROUP (the last two use the scales stored
  *                     at token j's slot).
  *   num_splits        0: balanced split -- the key pages of all sequences and
  *                     kv-heads are cut into one equal contiguous share per
@@ -371,6 +431,7 @@ int pqkv_paged_attention_noalloc(const void* q, void* out, const void* pages, in
  *                   nothing between calls.  Calls that share a workspace must
  *                   not overlap on the device.
  * 1 <= num_groups <= 2048.  Bitwise reproducible run to run on one device.
+ * INT4_GROUP pools: PQKV_EUNSUPPORTED.
  */
 int pqkv_paged_attention_shared_prefix(
     const void* q, void* out, const void* pages, int64_t num_pages, const int32_t* block_table,

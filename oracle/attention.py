@@ -30,11 +30,14 @@ from __future__ import annotations
 
 import numpy as np
 
-from .codec import INT8_TOKEN, dequantize, int8_row_scale, quantize
+from .codec import (INT4_GROUP, INT8_TOKEN, dequantize, int4_decode, int4_encode,
+                    int4_group_scale, int4_tile, int4_untile, int8_row_scale, quantize)
 
 
 def new_pool(num_pages, num_kv_heads, head_dim, kv_dtype, page_size=16, fill=0):
     dt = np.uint16 if kv_dtype == 0 else np.uint8
+    if kv_dtype == INT4_GROUP:
+        head_dim = 72                      # bytes of a row, scales among them
     return np.full((num_pages, num_kv_heads, 2, page_size, head_dim), fill, dtype=dt)
 
 
@@ -54,10 +57,12 @@ def kv_append_quant(k, v, slot_mapping, kv_dtype, k_scale, v_scale, pages):
     Format 3 (INT8 with a scale per row): k_scale and v_scale are the scale
     pools [num_pages, Hkv, P]; every written row's scale is computed from the
     row and stored at its slot, and (pages, k_scale, v_scale) copies are
-    returned.
+    returned.  Format 5 (4 bits) takes no scales: they lie in the pool.
     """
     if kv_dtype == INT8_TOKEN:
         return _append_row_scaled(k, v, slot_mapping, k_scale, v_scale, pages)
+    if kv_dtype == INT4_GROUP:
+        return _append_int4(k, v, slot_mapping, pages)
     k = np.asarray(k, dtype=np.float16)
     v = np.asarray(v, dtype=np.float16)
     out = np.array(pages, copy=True)
@@ -107,6 +112,29 @@ def _append_row_scaled(k, v, slot_mapping, k_pool, v_pool, pages):
     return out, kp, vp
 
 
+def _append_int4(k, v, slot_mapping, pages):
+    """Format 5: the tiles that rows fall in are taken apart, the rows replaced, and
+    the tiles put together again."""
+    out = np.array(pages, copy=True)
+    P = out.shape[3]
+    slots = np.asarray(slot_mapping, dtype=np.int64).reshape(-1)
+    if slots.size and slots.max() >= out.shape[0] * P:
+        raise IndexError("slot %d outside the pool" % slots.max())
+    ids = np.unique(slots[slots >= 0] // P)
+    tiles = out[ids].reshape(len(ids), out.shape[1], 2, P * out.shape[4])
+    codes, scale = int4_untile(tiles)
+    for kv, x in enumerate((k, v)):
+        x = np.asarray(x, dtype=np.float16)
+        s = int4_group_scale(x)
+        c = int4_encode(x, s)
+        for t, slot in enumerate(slots):
+            if slot >= 0:
+                at = np.searchsorted(ids, slot // P)
+                codes[at, :, kv, slot % P], scale[at, :, kv, slot % P] = c[t], s[t]
+    out[ids] = int4_tile(codes, scale).reshape(out[ids].shape)
+    return out
+
+
 def gather_kv(pages, block_row, L, h, kv_dtype, k_scale, v_scale):
     """Dequantized float64 K and V [L, D] of one sequence and kv-head, read
     page by page through its block-table row.  For format 3 the scales are the
@@ -114,12 +142,36 @@ def gather_kv(pages, block_row, L, h, kv_dtype, k_scale, v_scale):
     P = pages.shape[3]
     n = (L + P - 1) // P
     ids = np.asarray(block_row[:n], dtype=np.int64)
+    if kv_dtype == INT4_GROUP:
+        codes, scale = int4_untile(pages[ids, h].reshape(n, 2, -1))
+        both = int4_decode(codes, scale)                         # [n, 2, P, D]
+        return both[:, 0].reshape(n * P, -1)[:L], both[:, 1].reshape(n * P, -1)[:L]
     kc = pages[ids, h, 0].reshape(n * P, -1)[:L]
     vc = pages[ids, h, 1].reshape(n * P, -1)[:L]
     if kv_dtype == INT8_TOKEN:
         k_scale = np.asarray(k_scale)[ids, h].reshape(-1)[:L]
         v_scale = np.asarray(v_scale)[ids, h].reshape(-1)[:L]
     return dequantize(kc, k_scale, kv_dtype), dequantize(vc, v_scale, kv_dtype)
+
+
+def kv_read(pages, block_table, first_pos, token_offsets, kv_dtype, k_scale, v_scale):
+    """float64 K and V [token_offsets[-1], Hkv, D]: rows token_offsets[s] .. of request s
+    are its tokens from position first_pos[s] on."""
+    T, H = int(token_offsets[-1]), pages.shape[1]
+    out = np.zeros((2, T, H, 128))
+    for s in range(len(token_offsets) - 1):
+        a, b = int(token_offsets[s]), int(token_offsets[s + 1])
+        f = int(first_pos[s]) if first_pos is not None else 0
+        if b == a:
+            continue
+        for h in range(H):
+            if kv_dtype in (INT8_TOKEN, INT4_GROUP):
+                K, V = gather_kv(pages, block_table[s], f + b - a, h, kv_dtype, k_scale, v_scale)
+            else:
+                K, V = gather_kv(pages, block_table[s], f + b - a, h, kv_dtype,
+                                 _scale_of(k_scale, h), _scale_of(v_scale, h))
+            out[0, a:b, h], out[1, a:b, h] = K[f:], V[f:]
+    return out[0], out[1]
 
 
 def _scale_of(scale, h):
@@ -197,7 +249,7 @@ def paged_attention(q, pages, block_table, seq_lens, q_len, kv_dtype, k_scale, v
         limits = np.repeat(L - q_len + np.arange(q_len), G)
         lower = limits - window + 1 if window > 0 else None
         for h in (range(H) if heads is None else heads):
-            if kv_dtype == INT8_TOKEN:
+            if kv_dtype in (INT8_TOKEN, INT4_GROUP):
                 K, V = gather_kv(pages, block_table[s], L, h, kv_dtype, k_scale, v_scale)
             else:
                 K, V = gather_kv(pages, block_table[s], L, h, kv_dtype,
@@ -230,7 +282,7 @@ def paged_attention_partial(q, pages, block_table, seq_lens, q_pos, q_len, kv_dt
         for h in range(H):
             if L == 0:
                 continue
-            if kv_dtype == INT8_TOKEN:
+            if kv_dtype in (INT8_TOKEN, INT4_GROUP):
                 K, V = gather_kv(pages, block_table[s], L, h, kv_dtype, k_scale, v_scale)
             else:
                 K, V = gather_kv(pages, block_table[s], L, h, kv_dtype,

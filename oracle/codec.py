@@ -19,6 +19,10 @@ Formats
   for each token and head instead of from a calibration.  The scale is the
   row's largest |x| (NaNs ignored; 0 for a row of zeros) divided by 127,
   rounded once to binary32; each element is then encoded as above under it.
+* 4 bits with a scale per group of 32 values (format 5): code = x / s rounded half
+  to even, clamped to [-7, 7]; s = the group's largest |x| / 7 rounded to
+  binary32, bfloat16 and binary16 in turn, at most 2720.  The bytes of a K or V tile
+  are laid out as include/pqkv.h says: `int4_tile` and `int4_untile`.
 
 Rounding is to nearest with ties to even everywhere; encoding saturates.
 For non-finite inputs the oracle takes the reading that E4M3 maps NaN to the
@@ -32,6 +36,8 @@ import numpy as np
 E4M3_MAX = 448.0
 INT8_MAX = 127
 INT8_TOKEN = 3          # kv format code: INT8 with a scale per (token, kv-head) row
+INT4_GROUP = 5          # kv format code: 4 bits with a scale per group of 32 values
+INT4_ROWS, INT4_DIMS, INT4_PER = 16, 128, 32
 
 
 def e4m3_decode(codes) -> np.ndarray:
@@ -148,3 +154,86 @@ def dequantize(codes, scale, kv_dtype: int) -> np.ndarray:
     if kv_dtype == INT8_TOKEN:
         return int8_decode(codes.astype(np.uint8).view(np.int8)) * s[..., None]
     raise ValueError(kv_dtype)
+
+
+# ---------------------------------------------------------------------------
+# Format 5: 4 bits with a scale per group of 32 values
+# ---------------------------------------------------------------------------
+def _round_bits(x, bits):
+    """x (finite, >= 0, float64) rounded to `bits` significant bits, ties to even."""
+    m, e = np.frexp(x)
+    return np.ldexp(np.rint(np.ldexp(m, bits)), e - bits)
+
+
+def int4_group_scale(x16) -> np.ndarray:
+    """Scales [..., 4] (float64, binary16 values) of rows [..., 128]."""
+    a = np.abs(np.asarray(x16, dtype=np.float16).astype(np.float64))
+    a = np.minimum(np.where(np.isnan(a), 0.0, a), 65504.0)
+    amax = a.reshape(a.shape[:-1] + (INT4_DIMS // INT4_PER, INT4_PER)).max(axis=-1)
+    q = (amax / 7.0).astype(np.float32).astype(np.float64)
+    s = _round_bits(q, 8)                                # bfloat16 (no q is that small)
+    s = np.where(s < 2.0 ** -14, np.rint(s * 2.0 ** 24) * 2.0 ** -24, s)   # binary16
+    return np.minimum(s, 2720.0)
+
+
+def int4_encode(x16, scale) -> np.ndarray:
+    """Codes [..., 128] in [-7, 7] of rows under their groups' scales [..., 4]."""
+    x = np.asarray(x16, dtype=np.float16).astype(np.float64)
+    s = np.repeat(np.asarray(scale, dtype=np.float64), INT4_PER, axis=-1)
+    with np.errstate(divide="ignore", invalid="ignore"):
+        # (the exact quotient of 11 by 8 bits is no nearer to a half-integer than its
+        # binary64 rounding, unless it is one)
+        v = np.where(s > 0, x / s, 0.0)
+    v = np.where(np.isnan(x), 0.0, v)
+    return np.clip(np.rint(np.clip(v, -100, 100)), -7, 7).astype(np.int8)
+
+
+def int4_decode(codes, scale) -> np.ndarray:
+    return np.asarray(codes, np.float64) * np.repeat(np.asarray(scale, np.float64), INT4_PER, -1)
+
+
+def _int4_places():
+    """For (row, dim): byte offset of the half (16 bits) that holds the code, and the
+    positions of the code's bits in it, lowest first."""
+    half = np.zeros((INT4_ROWS, INT4_DIMS), np.int64)
+    field = np.zeros((INT4_ROWS, INT4_DIMS), np.int64)
+    for r in range(INT4_ROWS):
+        line = r // 2
+        for d in range(INT4_DIMS):
+            g, in_group = divmod(d, INT4_PER)
+            w, in_word = divmod(in_group, 8)
+            f, e = divmod(in_word, 2)
+            chunk = (4 * (r % 2) + g) ^ (0, 5, 2, 7)[line % 4]
+            half[r, d] = 128 * line + 16 * chunk + 4 * w + 2 * e
+            field[r, d] = f
+    bits = np.array([[6, 7, 8, 9], [2, 3, 4, 5], [10, 11, 12, 13], [14, 15, 0, 1]])[field]
+    return half, bits
+
+
+_HALF, _BITS = _int4_places()
+
+
+def int4_tile(codes, scale) -> np.ndarray:
+    """The 1152 bytes [..., 1152] of tiles of codes [..., 16, 128] and scales [..., 16, 4]."""
+    n = np.asarray(codes).astype(np.int64) + 8
+    lead = n.shape[:-2]
+    halves = np.zeros(lead + (512,), np.int64)
+    for k in range(4):
+        bit = ((n >> k) & 1) << _BITS[..., k]
+        for r in range(INT4_ROWS):
+            for d in range(INT4_DIMS):
+                halves[..., _HALF[r, d] // 2] |= bit[..., r, d]
+    sc = np.swapaxes(np.asarray(scale), -1, -2).astype(np.float16)       # [..., 4, 16]
+    return np.concatenate([halves.astype("<u2").view(np.uint8).reshape(lead + (1024,)),
+                           np.ascontiguousarray(sc).view(np.uint8).reshape(lead + (128,))], -1)
+
+
+def int4_untile(tile):
+    """Codes [..., 16, 128] and scales [..., 16, 4] of tiles' bytes [..., 1152]."""
+    tile = np.ascontiguousarray(np.asarray(tile, np.uint8))
+    lead = tile.shape[:-1]
+    halves = np.ascontiguousarray(tile[..., :1024]).view("<u2").astype(np.int64)
+    at = halves[..., _HALF // 2]
+    n = sum(((at >> _BITS[..., k]) & 1) << k for k in range(4))
+    sc = np.ascontiguousarray(tile[..., 1024:]).view(np.float16).reshape(lead + (4, 16))
+    return (n - 8).astype(np.int8), np.swapaxes(sc, -1, -2).astype(np.float64)

@@ -11,7 +11,10 @@ library's CUDA kernels; there is no fallback path.
 
 Pool layout: ``pages`` is [num_pages, num_kv_heads, 2, 16, 128] -- for each
 page and kv-head a 16-token K tile followed by a V tile -- of uint8 codes
-(E4M3 / INT8) or float16 values.
+(E4M3 / INT8) or float16 values.  A 4-bit pool ("int4_group") is uint8
+[num_pages, num_kv_heads, 2, 16, 72]: 64 bytes of codes and 8 of scales a row.
+
+    kv_read(pages, block_table, first_pos, token_offsets, kv_dtype, k_scale, v_scale, k, v)
 """
 from __future__ import annotations
 
@@ -26,11 +29,14 @@ FP16 = 0
 FP8_E4M3 = 1
 INT8 = 2
 INT8_ROW = 3          # int8 with a scale per (token, kv-head) row, computed at append time
-KV_DTYPES = {"fp16": FP16, "fp8_e4m3": FP8_E4M3, "int8": INT8, "int8_row": INT8_ROW}
+INT4_GROUP = 5        # 4-bit codes with a scale per group of 32 values, computed at append time
+KV_DTYPES = {"fp16": FP16, "fp8_e4m3": FP8_E4M3, "int8": INT8, "int8_row": INT8_ROW,
+             "int4_group": INT4_GROUP}
 _SCALED = (FP8_E4M3, INT8)   # formats that take k_scale / v_scale arguments
 
 HEAD_DIM = 128
 PAGE_SIZE = 16
+INT4_ROW_BYTES = 72   # of a row's codes and scales in a 4-bit pool
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libpqkv.so")
@@ -65,6 +71,10 @@ def load_library(path: str | None = None):
         lib.pqkv_kv_append_quant.argtypes = [c_vp, c_i64, c_vp, c_i64, c_vp, c_i32, c_i32, c_i32,
                                              c_i32, c_vp, c_vp, c_i32, c_vp, c_i64, c_i32, c_vp,
                                              c_vp]
+        lib.pqkv_kv_read.restype = ctypes.c_int
+        lib.pqkv_kv_read.argtypes = [c_vp, c_i64, c_vp, c_i32, c_vp, c_vp, c_i32, c_i32, c_i32,
+                                     c_i32, c_i32, c_i32, c_vp, c_vp, c_i32, c_vp, c_i64, c_vp,
+                                     c_i64, c_vp, c_vp]
         lib.pqkv_paged_attention_workspace_size.restype = c_sz
         lib.pqkv_paged_attention_workspace_size.argtypes = [c_i32] * 6
         lib.pqkv_paged_attention.restype = ctypes.c_int
@@ -152,15 +162,20 @@ def _row_scale_bytes(num_pages, num_kv_heads):
     return num_pages * num_kv_heads * 2 * PAGE_SIZE * 2          # fp16 scales
 
 
+def _row_elems(kd):
+    return INT4_ROW_BYTES if kd == INT4_GROUP else HEAD_DIM
+
+
 def new_pages(num_pages: int, num_kv_heads: int, kv_dtype, device="cuda", fill=None):
     """Allocate a pool [num_pages, num_kv_heads, 2, 16, 128] for ``kv_dtype``.
 
     An INT8_ROW pool is the code tensor followed, in the same allocation, by
-    its row-scale area (zeroed); ``row_scales(pages)`` views that area.
+    its row-scale area (zeroed); ``row_scales(pages)`` views that area.  An
+    INT4_GROUP pool's rows are 72 bytes, scales among them: [..., 16, 72].
     """
     kd = _dtype_id(kv_dtype)
     dt = torch.float16 if kd == FP16 else torch.uint8
-    shape = (num_pages, num_kv_heads, 2, PAGE_SIZE, HEAD_DIM)
+    shape = (num_pages, num_kv_heads, 2, PAGE_SIZE, _row_elems(kd))
     if kd == INT8_ROW:
         codes = num_pages * num_kv_heads * 2 * PAGE_SIZE * HEAD_DIM
         buf = torch.zeros(codes + _row_scale_bytes(num_pages, num_kv_heads), dtype=torch.uint8,
@@ -195,9 +210,10 @@ def _row_scale_view(area: torch.Tensor, num_pages: int, num_kv_heads: int) -> to
 
 def _check_pages(pages, kd):
     want = torch.float16 if kd == FP16 else torch.uint8
-    if pages.dtype != want or pages.dim() != 5 or pages.shape[2:] != (2, PAGE_SIZE, HEAD_DIM):
-        raise ValueError("pages must be %s [num_pages, Hkv, 2, 16, 128], got %s %s"
-                         % (want, pages.dtype, tuple(pages.shape)))
+    n = _row_elems(kd)
+    if pages.dtype != want or pages.dim() != 5 or pages.shape[2:] != (2, PAGE_SIZE, n):
+        raise ValueError("pages must be %s [num_pages, Hkv, 2, 16, %d], got %s %s"
+                         % (want, n, pages.dtype, tuple(pages.shape)))
     if not pages.is_contiguous() or not pages.is_cuda:
         raise ValueError("pages must be a contiguous CUDA tensor")
     if kd == INT8_ROW:
@@ -248,6 +264,50 @@ def kv_append_quant(k, v, slot_mapping, kv_dtype, k_scale, v_scale, pages, statu
             sph, _ptr(pages), pages.shape[0], PAGE_SIZE, _ptr(status), _stream(pages, stream))
     _check(rc, "kv_append_quant")
     return pages
+
+
+def kv_read(pages, block_table, first_pos, token_offsets, kv_dtype, k_scale, v_scale, k, v,
+            status=None, stream=None):
+    """The inverse of kv_append_quant for whole requests: rows
+    ``token_offsets[s]`` .. ``token_offsets[s + 1] - 1`` (int32 [B + 1], from 0)
+    of ``k`` and ``v`` ([T, Hkv, 128] fp16, token rows may be strided) receive the
+    values of request s's tokens from position ``first_pos[s]`` on (int32 [B];
+    None: 0), found through ``block_table`` (int32 [B, max_pages_per_seq]).  Rows
+    behind the last request's are left as they are.  Returns (k, v)."""
+    kd = _dtype_id(kv_dtype)
+    _check_pages(pages, kd)
+    idx = pages.get_device()
+    H, B, T = pages.shape[1], _size(block_table), _size(k)
+    ints = [("block_table", block_table, (B, _size(block_table, 1))),
+            ("token_offsets", token_offsets, (B + 1,))]
+    if first_pos is not None:
+        ints.append(("first_pos", first_pos, (B,)))
+    _check_ints(idx, torch.int32, ints)
+    for name, x in (("k", k), ("v", v)):
+        if x.dtype is not torch.float16 or x.shape != (T, H, HEAD_DIM) or x.get_device() != idx \
+                or x.stride(2) != 1 or (H > 1 and x.stride(1) != HEAD_DIM):
+            raise ValueError("%s must be fp16 [T, %d, 128] on cuda:%d with contiguous heads and "
+                             "dims, got %s %s (strides %s) on %s" % (
+                                 name, H, idx, x.dtype, list(x.shape), list(x.stride()), x.device))
+    sph, ks, vs = 0, None, None
+    if kd in _SCALED:
+        sph = _check_scale(k_scale, H, "k_scale")
+        if _check_scale(v_scale, H, "v_scale") != sph:
+            raise ValueError("k_scale and v_scale must have the same shape")
+        if k_scale.get_device() != idx or v_scale.get_device() != idx:
+            raise ValueError("k_scale and v_scale must be on cuda:%d" % idx)
+        ks, vs = k_scale.data_ptr(), v_scale.data_ptr()
+    if status is not None:
+        _check_status(status, pages.device)
+    rc = _call_on(
+        idx, stream, load_library().pqkv_kv_read, pages.data_ptr(), pages.shape[0],
+        block_table.data_ptr(), _size(block_table, 1),
+        None if first_pos is None else first_pos.data_ptr(), token_offsets.data_ptr(), B, T, H,
+        HEAD_DIM, PAGE_SIZE, kd, ks, vs, sph, k.data_ptr(), k.stride(0), v.data_ptr(), v.stride(0),
+        None if status is None else status.data_ptr())
+    if rc:
+        _check(rc, "kv_read")
+    return k, v
 
 
 def workspace_size(num_seqs, q_len, num_q_heads, num_kv_heads, num_splits=0) -> int:

@@ -83,6 +83,7 @@ int blocks_per_sm(int kv_dtype, int nt, bool pair, int num_seqs) {
     case PQKV_KV_FP8_E4M3: return attention_blocks_per_sm_e4m3(nt, pair, num_seqs);
     case PQKV_KV_INT8: return attention_blocks_per_sm_int8(nt, pair, num_seqs);
     case PQKV_KV_INT8_ROW: return attention_blocks_per_sm_int8_row(nt, pair, num_seqs);
+    case PQKV_KV_INT4_GROUP: return attention_blocks_per_sm_int4_group(nt, pair, num_seqs);
   }
   return 0;
 }
@@ -112,7 +113,9 @@ int plan_attention(int32_t num_seqs, int32_t q_len, int32_t hq, int32_t hkv, int
 }
 
 int validate_common(int32_t head_dim, int32_t page_size, int32_t kv_dtype) {
-  if (kv_dtype < PQKV_KV_FP16 || kv_dtype > PQKV_KV_INT8_ROW) return PQKV_EINVAL;
+  if (kv_dtype != PQKV_KV_INT4_GROUP &&      // (4 stands for no format)
+      (kv_dtype < PQKV_KV_FP16 || kv_dtype > PQKV_KV_INT8_ROW))
+    return PQKV_EINVAL;
   if (head_dim != kHeadDim || page_size != kPageSize) return PQKV_EUNSUPPORTED;
   return PQKV_OK;
 }
@@ -192,6 +195,58 @@ extern "C" int pqkv_kv_append_quant(const void* k, int64_t k_token_stride, const
   if (launch_append(p, kv_dtype, grid, static_cast<cudaStream_t>(stream)) != cudaSuccess)
     return PQKV_ECUDA;
   return PQKV_OK;
+}
+
+extern "C" int pqkv_kv_read(const void* pages, int64_t num_pages, const int32_t* block_table,
+                            int32_t max_pages_per_seq, const int32_t* first_pos,
+                            const int32_t* token_offsets, int32_t num_seqs, int32_t num_tokens,
+                            int32_t num_kv_heads, int32_t head_dim, int32_t page_size,
+                            int32_t kv_dtype, const float* k_scale, const float* v_scale,
+                            int32_t scale_per_head, void* k, int64_t k_token_stride, void* v,
+                            int64_t v_token_stride, int32_t* status, void* stream) {
+  int rc = validate_common(head_dim, page_size, kv_dtype);
+  if (rc) return rc;
+  if (num_seqs < 0 || num_tokens < 0 || num_kv_heads < 1) return PQKV_EINVAL;
+  if (num_seqs > PQKV_MAX_SEQS) return PQKV_ERANGE;
+  if (num_seqs == 0 || num_tokens == 0) return PQKV_OK;
+  if (!pages || !block_table || !token_offsets || !k || !v) return PQKV_EINVAL;
+  if (uses_scale_args(kv_dtype) && (!k_scale || !v_scale)) return PQKV_EINVAL;
+  if (num_pages < 1 || num_pages > INT32_MAX || max_pages_per_seq < 1) return PQKV_EINVAL;
+  if ((int64_t)max_pages_per_seq * page_size > PQKV_MAX_SEQ_LEN + page_size) return PQKV_ERANGE;
+  if (k_token_stride < (int64_t)num_kv_heads * head_dim ||
+      v_token_stride < (int64_t)num_kv_heads * head_dim || k_token_stride % 16 ||
+      v_token_stride % 16)
+    return PQKV_EINVAL;
+  if (!aligned(pages, 16) || !aligned(k, 32) || !aligned(v, 32) || !aligned(block_table, 4) ||
+      !aligned(first_pos, 4) || !aligned(token_offsets, 4) || !aligned(status, 4))
+    return PQKV_EINVAL;
+  int sms = 0;
+  rc = current_device_sms(&sms);
+  if (rc) return rc;
+  ReadParams p = {};
+  p.pages = static_cast<const uint8_t*>(pages);
+  p.row_scales = kv_dtype == PQKV_KV_INT8_ROW
+                     ? row_scale_area(const_cast<void*>(pages), num_pages, num_kv_heads)
+                     : nullptr;
+  p.block_table = block_table;
+  p.first_pos = first_pos;
+  p.token_offsets = token_offsets;
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  p.k = static_cast<uint16_t*>(k);
+  p.v = static_cast<uint16_t*>(v);
+  p.status = status;
+  p.num_pages = num_pages;
+  p.k_stride = k_token_stride;
+  p.v_stride = v_token_stride;
+  p.scale_per_head = scale_per_head ? 1 : 0;
+  p.num_seqs = num_seqs;
+  p.num_tokens = num_tokens;
+  p.num_kv_heads = num_kv_heads;
+  p.bt_stride = max_pages_per_seq;
+  return launch_read(p, kv_dtype, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? PQKV_OK
+             : PQKV_ECUDA;
 }
 
 extern "C" size_t pqkv_paged_attention_workspace_size(int32_t num_seqs, int32_t q_len,
@@ -317,19 +372,25 @@ int bind_attention(const AttnArgs& a, const AttnLaunch& L, void* workspace,
     if (!aligned(workspace, 256) || workspace_bytes < pl.total) return PQKV_EWORKSPACE;
   }
 
-  const int rc = encode_pool_map(a, mapp);
-  if (rc) return rc;
+  if (a.kv_dtype == PQKV_KV_INT4_GROUP) {
+    std::memset(mapp, 0, sizeof(*mapp));     // its tiles are contiguous: copied untiled
+  } else {
+    const int rc = encode_pool_map(a, mapp);
+    if (rc) return rc;
+  }
 
   AttnParams& p = *pp;
   p.q = static_cast<const uint16_t*>(a.q);
   p.out = nullptr;
   p.block_table = a.block_table;
   p.seq_lens = a.seq_lens;
-  // INT8_ROW reads no scale arguments: its k_scale slot carries the row-scale area
+  // INT8_ROW and INT4_GROUP read no scale arguments: their k_scale slot carries the
+  // row-scale area, and the pool
   p.k_scale = a.kv_dtype == PQKV_KV_INT8_ROW
                   ? reinterpret_cast<const float*>(
                         row_scale_area(const_cast<void*>(a.pages), a.num_pages, a.num_kv_heads))
-                  : a.k_scale;
+              : a.kv_dtype == PQKV_KV_INT4_GROUP ? static_cast<const float*>(a.pages)
+                                                 : a.k_scale;
   p.v_scale = a.v_scale;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   p.counters = pl.total ? reinterpret_cast<int32_t*>(ws) : nullptr;
@@ -358,6 +419,7 @@ cudaError_t launch_attention(int kv_dtype, const AttnParams& p, const CUtensorMa
     case PQKV_KV_FP16: return launch_attention_fp16(p, map, grid, nt, pair, st);
     case PQKV_KV_FP8_E4M3: return launch_attention_e4m3(p, map, grid, nt, pair, st);
     case PQKV_KV_INT8_ROW: return launch_attention_int8_row(p, map, grid, nt, pair, st);
+    case PQKV_KV_INT4_GROUP: return launch_attention_int4_group(p, map, grid, nt, pair, st);
     default: return launch_attention_int8(p, map, grid, nt, pair, st);
   }
 }
@@ -439,6 +501,7 @@ extern "C" int pqkv_paged_attention_window(const void* q, void* out, const void*
     case PQKV_KV_FP16: e = launch_attention_window_fp16(p, map, L.grid, L.nt, st); break;
     case PQKV_KV_FP8_E4M3: e = launch_attention_window_e4m3(p, map, L.grid, L.nt, st); break;
     case PQKV_KV_INT8_ROW: e = launch_attention_window_int8_row(p, map, L.grid, L.nt, st); break;
+    case PQKV_KV_INT4_GROUP: e = launch_attention_window_int4_group(p, map, L.grid, L.nt, st); break;
     default: e = launch_attention_window_int8(p, map, L.grid, L.nt, st); break;
   }
   return e == cudaSuccess ? PQKV_OK : PQKV_ECUDA;
@@ -473,6 +536,9 @@ extern "C" int pqkv_paged_attention_partial(
     case PQKV_KV_FP16: e = launch_attention_partial_fp16(p, map, L.grid, L.nt, L.pair, st); break;
     case PQKV_KV_FP8_E4M3: e = launch_attention_partial_e4m3(p, map, L.grid, L.nt, L.pair, st); break;
     case PQKV_KV_INT8_ROW: e = launch_attention_partial_int8_row(p, map, L.grid, L.nt, L.pair, st); break;
+    case PQKV_KV_INT4_GROUP:
+      e = launch_attention_partial_int4_group(p, map, L.grid, L.nt, L.pair, st);
+      break;
     default: e = launch_attention_partial_int8(p, map, L.grid, L.nt, L.pair, st); break;
   }
   return e == cudaSuccess ? PQKV_OK : PQKV_ECUDA;
@@ -503,6 +569,7 @@ int bind_shared_prefix(AttnArgs* a, const SharedArgs& sa, const void* out, const
   if (rc) return rc;
   rc = check_attention_args(*a);
   if (rc) return rc;
+  if (a->kv_dtype == PQKV_KV_INT4_GROUP) return PQKV_EUNSUPPORTED;
   if (sa.max_prefix_len < 0) return PQKV_EINVAL;
   if (a->num_seqs == 0) return PQKV_OK;
   if (sa.num_groups < 1 || !sa.group_offsets || !sa.prefix_lens || !aligned(sa.group_offsets, 4) ||

@@ -41,7 +41,13 @@
 // the nearest fp16 value, encode under that scale and the row's first thread
 // stores the fp16 scale at the row's place in the scale area that follows the
 // codes.
+//
+// 4 bits with a scale per group of 32 values (PQKV_KV_INT4_GROUP): the two lanes of a
+// group exchange their maxima, and each writes the 8 bytes of its 16 codes and one of
+// the group's two scales.
 #include <atomic>
+
+#include <cuda_bf16.h>
 
 #include "pqkv_common.cuh"
 
@@ -221,14 +227,67 @@ __device__ __forceinline__ uint4 quantize16(const uint4& a, const uint4& b, floa
   return make_uint4(out[0], out[1], out[2], out[3]);
 }
 
+// 4 bits: the larger of the two lanes that hold a group of 32 values (an even lane and
+// the next one; their row is wholly in range, see the kernel's loop)
+__device__ __forceinline__ float group_max2(float m) {
+  return fmaxf(m, __shfl_xor_sync(3u << (threadIdx.x & 30), m, 1));
+}
+
+// 4 bits: the scale of a group whose largest |x| is amax: amax / 7 with 8 significant
+// bits (bfloat16's), as an fp16 value, at most 2720
+__device__ __forceinline__ float int4_scale(float amax) {
+  const float q = __fdiv_rn(fminf(amax, 65504.f), 7.f);
+  const float s = __bfloat162float(__float2bfloat16_rn(q));
+  return fminf(__half2float(__float2half_rn(s)), 2720.f);
+}
+
+// 4 bits: the codes (+ 8) of 16 values, in the fields that int4_pair reads.  The code of
+// x is x / s rounded to a whole number, ties to even, within +-7.  z = x RN(1 / s) is
+// within 2^-22.9 of x / s (for scales whose reciprocal is a normal number: all but 0, s being at
+// least 2^-24), so c = rint(z) is the code or, next to a half-integer, its neighbour.
+// There |x| is compared with s (c -+ 1/2), an exact product (8 and 4 bits); a tie goes to the
+// even code.  Infinities saturate, NaN has code 0; under a scale of 0 every code is 0.
+__device__ __forceinline__ uint2 int4_pack16(const uint4& a, const uint4& b, float s) {
+  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  const float r = s > 0.f ? __frcp_rn(s) : 0.f;
+  constexpr float kMagic = 12582912.0f;   // 1.5 * 2^23: adding it leaves rint in the low bits
+  uint32_t out[2] = {0, 0};
+#pragma unroll
+  for (int k = 0; k < 16; ++k) {
+    const float x = half_of(w, k);
+    // (a NaN is dropped by the maximum: it becomes -7.5 and is mended below)
+    const float z = fminf(fmaxf(__fmul_rn(x, r), -7.5f), 7.5f);
+    const float y = __fadd_rn(z, kMagic);
+    const float c = __fsub_rn(y, kMagic), d = __fsub_rn(z, c);
+    uint32_t n = (__float_as_uint(y) + 8u) & 31u;       // code + 8, in 0 .. 16
+    if (!(fabsf(d) <= 0.5f - 0x1p-14f) || !(fabsf(z) < 7.5f)) {
+      const float za = fabsf(z), ca = fabsf(c);
+      const float m = za > ca ? ca + 0.5f : ca - 0.5f;  // the half-integer near za
+      const float sm = __fmul_rn(s, m), xa = fabsf(x);
+      const int lo = (int)(m - 0.5f);
+      int mag = xa > sm || (xa == sm && (lo & 1)) ? lo + 1 : lo;
+      mag = x != x || s == 0.f ? 0 : min(mag, 7);
+      n = 8u + (uint32_t)(x < 0.f ? -mag : mag);
+    }
+    constexpr int kTurn[4] = {6, 2, 10, 14};
+    const int f = (k >> 1) & 3, e = (k & 1) * 16;
+    uint32_t& o = out[k >> 3];
+    if (f < 3) o |= n << (e + kTurn[f]);
+    else o |= ((n & 3u) << (e + 14)) | ((n >> 2) << e);
+  }
+  return make_uint2(out[0], out[1]);
+}
+
 // Six resident blocks per SM (40 registers) for the formats with one scale;
 // the row-scale format keeps its registers (it would spill under that cap).
 template <int KVT>
-__global__ void __launch_bounds__(kAppendThreads, KVT == PQKV_KV_INT8_ROW ? 1 : 6)
+__global__ void __launch_bounds__(kAppendThreads, KVT == PQKV_KV_INT8_ROW || KVT == PQKV_KV_INT4_GROUP ? 1 : 6)
     append_kernel(const AppendParams p) {
   constexpr int kVecPerRow = kHeadDim / 16;
   constexpr int kElem = (KVT == PQKV_KV_FP16) ? 2 : 1;
-  constexpr int64_t kTile = (int64_t)kPageSize * kHeadDim * kElem;  // one K (or V) tile
+  constexpr bool kInt4 = KVT == PQKV_KV_INT4_GROUP;
+  constexpr int64_t kTile =                                         // one K (or V) tile
+      kInt4 ? kInt4Tile : (int64_t)kPageSize * kHeadDim * kElem;
   constexpr int U = kAppendUnroll;
   grid_dependency_wait();
   grid_dependents_launch();
@@ -275,9 +334,21 @@ __global__ void __launch_bounds__(kAppendThreads, KVT == PQKV_KV_INT8_ROW ? 1 : 
       const int64_t page = slot[u] / kPageSize;
       const int off = (int)(slot[u] % kPageSize);
       uint8_t* tile = p.pages + (page * p.num_kv_heads + h[u]) * 2 * kTile;
-      uint8_t* kd = tile + (int64_t)off * kHeadDim * kElem + c[u] * 16 * kElem;
+      // (4 bits: half of the 16 bytes of a group)
+      uint8_t* kd = tile + (kInt4 ? int4_chunk(off >> 1, off & 1, c[u] >> 1) + (c[u] & 1) * 8
+                                  : off * kHeadDim * kElem + c[u] * 16 * kElem);
       uint8_t* vd = kd + kTile;
-      if (KVT == PQKV_KV_FP16) {
+      if constexpr (kInt4) {
+        // two lanes share a group
+        const float kscale = int4_scale(group_max2(amax16(k0[u], k1[u])));
+        const float vscale = int4_scale(group_max2(amax16(v0[u], v1[u])));
+        *reinterpret_cast<uint2*>(kd) = int4_pack16(k0[u], k1[u], kscale);
+        *reinterpret_cast<uint2*>(vd) = int4_pack16(v0[u], v1[u], vscale);
+        // the lane of a group's first half writes K's scale, the other one V's
+        uint16_t* sc = reinterpret_cast<uint16_t*>(tile + ((c[u] & 1) ? kTile : 0) + kInt4Codes) +
+                       (c[u] >> 1) * kPageSize + off;
+        *sc = __half_as_ushort(__float2half_rn((c[u] & 1) ? vscale : kscale));   // exact
+      } else if (KVT == PQKV_KV_FP16) {
         reinterpret_cast<uint4*>(kd)[0] = k0[u];
         reinterpret_cast<uint4*>(kd)[1] = k1[u];
         reinterpret_cast<uint4*>(vd)[0] = v0[u];
@@ -320,9 +391,9 @@ __global__ void __launch_bounds__(kAppendThreads, KVT == PQKV_KV_INT8_ROW ? 1 : 
 // Resident blocks per SM of the append kernel for `kv_dtype` on the current
 // device (register-limited), cached per device ordinal 0..63; 0 on error.
 int append_blocks_per_sm(int kv_dtype) {
-  static std::atomic<int> cache[4][64];
+  static std::atomic<int> cache[PQKV_KV_INT4_GROUP + 1][64];
   int dev = 0;
-  if (kv_dtype < 0 || kv_dtype > 3 || cudaGetDevice(&dev) != cudaSuccess) return 0;
+  if (kv_dtype < 0 || kv_dtype > PQKV_KV_INT4_GROUP || cudaGetDevice(&dev) != cudaSuccess) return 0;
   const bool cached = dev >= 0 && dev < 64;
   if (cached) {
     const int n = cache[kv_dtype][dev].load(std::memory_order_relaxed);
@@ -341,6 +412,10 @@ int append_blocks_per_sm(int kv_dtype) {
       break;
     case PQKV_KV_INT8:
       e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, append_kernel<PQKV_KV_INT8>,
+                                                        kAppendThreads, 0);
+      break;
+    case PQKV_KV_INT4_GROUP:
+      e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, append_kernel<PQKV_KV_INT4_GROUP>,
                                                         kAppendThreads, 0);
       break;
     default:
@@ -363,6 +438,8 @@ cudaError_t launch_append(const AppendParams& p, int kv_dtype, int grid, cudaStr
       return launch_pdl(append_kernel<PQKV_KV_INT8>, grid, kAppendThreads, 0, stream, p);
     case PQKV_KV_INT8_ROW:
       return launch_pdl(append_kernel<PQKV_KV_INT8_ROW>, grid, kAppendThreads, 0, stream, p);
+    case PQKV_KV_INT4_GROUP:
+      return launch_pdl(append_kernel<PQKV_KV_INT4_GROUP>, grid, kAppendThreads, 0, stream, p);
     default:
       return cudaErrorInvalidValue;
   }

@@ -1,5 +1,5 @@
-// Paged decode / speculative-verify attention over an FP16, E4M3, INT8 or
-// INT8-with-row-scales KV pool, with split-KV partitions merged by
+// Paged decode / speculative-verify attention over an FP16, E4M3, INT8,
+// INT8-with-row-scales or 4-bit KV pool, with split-KV partitions merged by
 // log-sum-exp; a partial mode gives one rank's share of a decode context
 // parallel split as O / l and LSE per row.
 //
@@ -76,9 +76,11 @@ struct AttnCfg {
   static_assert(!kPair || (NT == 1 && KVT != PQKV_KV_FP16), "paired blocks: 8-row 8-bit decode only");
   static constexpr int kThreads = kW * 32;
   static constexpr int kLines = (KVT == PQKV_KV_FP16) ? 64 : 32;   // 128-B lines per tile
-  static constexpr int kTileBytes = kLines * 128;
+  static constexpr bool kInt4 = (KVT == PQKV_KV_INT4_GROUP);
+  static constexpr int kTileBytes = kInt4 ? 2 * kInt4Tile : kLines * 128;
   static constexpr int kStagesPerWarp =
-      (KVT == PQKV_KV_FP16 || kPair || (kWideTree && (NT == 2 || NT == 3 || NT == 4)))
+      kInt4 ? (NT == 1 ? 3 : 4)
+      : (KVT == PQKV_KV_FP16 || kPair || (kWideTree && (NT == 2 || NT == 3 || NT == 4)))
           ? 2
           : (kW <= 8 ? 4 : (kW == 12 ? 3 : 2));
   static constexpr int kStages = kW * kStagesPerWarp;
@@ -118,6 +120,7 @@ struct AttnCfg {
   static constexpr int kQfOff = kQOff + kRP * kHeadDim * 2;
   // INT8_ROW: the 32 fp16 row scales (16 K, 16 V) of each stage's (page, kv-head)
   static constexpr bool kRowScaled = (KVT == PQKV_KV_INT8_ROW);
+  static constexpr bool kRefillEarly = kRowScaled || kInt4;
   static constexpr int kScOff = kQfOff + kQfBytes;
   static constexpr int kScBytes = kRowScaled ? kStages * 64 : 0;
   static constexpr int kBarOff = kScOff + kScBytes;
@@ -363,6 +366,10 @@ __device__ __forceinline__ uint4 lds128(const uint8_t* base, int line, int chunk
 // The Q^T B-fragments live in a shared table [4][NT][32] of 16-byte entries:
 // a lane's fragments of k-steps 2*k2 and 2*k2 + 1 of one row tile side by
 // side, so one 16-byte load serves two k-steps.
+// the formats whose k_scale / v_scale arguments are read
+template <int KVT>
+constexpr bool kScaleArgs = KVT == PQKV_KV_FP8_E4M3 || KVT == PQKV_KV_INT8;
+
 template <int NT>
 struct QFrags {
   const uint4* tab;
@@ -395,6 +402,26 @@ __device__ __forceinline__ void page_qk(const uint8_t* T, int g, int t, int lane
         const uint4 b = qf.get2(q, nt, lane);
         mma_16816(sc[nt], x.x, y.x, x.y, y.y, b.x, b.y);
         mma_16816(sc[nt], x.z, y.z, x.w, y.w, b.z, b.w);
+      }
+    }
+  } else if constexpr (KVT == PQKV_KV_INT4_GROUP) {
+    // the lane's 32 dims are group t: one scale for row g, one for row g + 8
+    const int at = int4_chunk(g >> 1, g & 1, t);
+    const uint4 x = *reinterpret_cast<const uint4*>(T + at);
+    const uint4 y = *reinterpret_cast<const uint4*>(T + at + 512);
+    const __half* scale = reinterpret_cast<const __half*>(T + kInt4Codes) + 16 * t + g;
+    const Int4Scale sx(__half2half2(scale[0])), sy(__half2half2(scale[8]));
+    const uint32_t wx[4] = {x.x, x.y, x.z, x.w}, wy[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      uint32_t a[4], b[4];
+      int4_word(wx[j], sx, a);
+      int4_word(wy[j], sy, b);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const uint4 q = qf.get2(j, nt, lane);
+        mma_16816(sc[nt], a[0], b[0], a[1], b[1], q.x, q.y);
+        mma_16816(sc[nt], a[2], b[2], a[3], b[3], q.z, q.w);
       }
     }
   } else {
@@ -464,6 +491,29 @@ __device__ __forceinline__ void page_pv(const uint8_t* T, int g, int t,
       for (int j = 0; j < 4; ++j)
         mma_mt(4 * hh + j, __byte_perm(a[j], b[j], 0x5410), __byte_perm(a[j], b[j], 0x7632),
                __byte_perm(c[j], d[j], 0x5410), __byte_perm(c[j], d[j], 0x7632));
+    }
+  } else if constexpr (KVT == PQKV_KV_INT4_GROUP) {
+    // the lane's 16 dims are half of group g / 2: a scale per token
+    const uint8_t* V = T + kInt4Tile;
+    const int at = int4_chunk(t, 0, g >> 1) + 8 * (g & 1), odd = at ^ 64;
+    const uint2 A = *reinterpret_cast<const uint2*>(V + at);
+    const uint2 B = *reinterpret_cast<const uint2*>(V + odd);
+    const uint2 C = *reinterpret_cast<const uint2*>(V + at + 512);
+    const uint2 D = *reinterpret_cast<const uint2*>(V + odd + 512);
+    const __half2* scale =
+        reinterpret_cast<const __half2*>(V + kInt4Codes) + 8 * (g >> 1) + t;
+    const Int4Scale s01(scale[0]), s89(scale[4]);
+    const uint32_t a[2] = {A.x, A.y}, b[2] = {B.x, B.y}, c[2] = {C.x, C.y}, d[2] = {D.x, D.y};
+    after_loads();
+#pragma unroll
+    for (int wi = 0; wi < 2; ++wi) {
+      uint32_t x0[4], x1[4], x2[4], x3[4];
+      int4_pair(__byte_perm(a[wi], b[wi], 0x5410), __byte_perm(a[wi], b[wi], 0x4501), s01, x0);
+      int4_pair(__byte_perm(a[wi], b[wi], 0x7632), __byte_perm(a[wi], b[wi], 0x6723), s01, x1);
+      int4_pair(__byte_perm(c[wi], d[wi], 0x5410), __byte_perm(c[wi], d[wi], 0x4501), s89, x2);
+      int4_pair(__byte_perm(c[wi], d[wi], 0x7632), __byte_perm(c[wi], d[wi], 0x6723), s89, x3);
+#pragma unroll
+      for (int f = 0; f < 4; ++f) mma_mt(4 * wi + f, x0[f], x1[f], x2[f], x3[f]);
     }
   } else {
     const uint4 A = lds128(T, 16 + 2 * t, g), B = lds128(T, 17 + 2 * t, g);
@@ -668,7 +718,7 @@ __global__ void __launch_bounds__(AttnCfg<KVT, NT, kPair>::kThreads,
         h0 = seg % H;
       }
       early_seg = s0 * H + h0;
-      if constexpr (KVT != PQKV_KV_FP16 && KVT != PQKV_KV_INT8_ROW) {
+      if constexpr (kScaleArgs<KVT>) {
         const int sh = p.scale_per_head ? h0 : 0;
         ks0 = __ldg(p.k_scale + sh);
         vs0 = __ldg(p.v_scale + sh);
@@ -694,7 +744,8 @@ __global__ void __launch_bounds__(AttnCfg<KVT, NT, kPair>::kThreads,
   // different blocks at about the same time; they stay in L2 for the second
   uint64_t scale_policy = policy;
   if constexpr (Cfg::kRowScaled) scale_policy = l2_evict_last_policy();
-  if (tid == 0) prefetch_tensormap(&map);
+  if constexpr (!Cfg::kInt4)
+    if (tid == 0) prefetch_tensormap(&map);
   auto lookup = [&](int u, int& id, int& h) {
     const int i = warp + u * W;
     id = 0;
@@ -740,7 +791,26 @@ __global__ void __launch_bounds__(AttnCfg<KVT, NT, kPair>::kThreads,
         return;
       }
     }
-    if (lane == 0) {
+    if constexpr (Cfg::kInt4) {
+      // codes and scales of a page's kv-head are 2304 bytes on end; a page id outside
+      // the pool (reported) reads as zeros, which the warp writes itself
+      const int stage = i % S;
+      uint8_t* dst = ring + stage * Cfg::kTileBytes;
+      if (id >= 0 && (int64_t)id < p.num_pages) {
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&full[stage], Cfg::kTileBytes);
+          bulk_load(dst,
+                    reinterpret_cast<const uint8_t*>(p.k_scale) +
+                        ((int64_t)id * p.num_kv_heads + h) * Cfg::kTileBytes,
+                    Cfg::kTileBytes, &full[stage], policy);
+        }
+      } else {
+        for (int k = lane; k < Cfg::kTileBytes / 16; k += 32)
+          reinterpret_cast<uint4*>(dst)[k] = make_uint4(0, 0, 0, 0);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&full[stage]);
+      }
+    } else if (lane == 0) {
       const int stage = i % S;
       if constexpr (Cfg::kRowScaled) {
         // the page's 32 fp16 row scales travel with its tile (one bulk copy on
@@ -816,7 +886,7 @@ __global__ void __launch_bounds__(AttnCfg<KVT, NT, kPair>::kThreads,
           vs_e = vs0;
           qpos_e = qpos0;
         } else {
-          if constexpr (KVT != PQKV_KV_FP16 && KVT != PQKV_KV_INT8_ROW) {
+          if constexpr (kScaleArgs<KVT>) {
             const int sh = p.scale_per_head ? f_h : 0;
             ks_e = __ldg(p.k_scale + sh);
             vs_e = __ldg(p.v_scale + sh);
@@ -846,8 +916,8 @@ __global__ void __launch_bounds__(AttnCfg<KVT, NT, kPair>::kThreads,
         }
       }
       const int sh = p.scale_per_head ? f_h : 0;
-      if constexpr (KVT == PQKV_KV_FP16 || KVT == PQKV_KV_INT8_ROW) {
-        // FP16 has no scale; INT8_ROW applies its row scales per token
+      if constexpr (!kScaleArgs<KVT>) {
+        // FP16 has no scale; INT8_ROW and INT4_GROUP apply the pool's own
         qk_scale = p.sm_scale_log2;
         v_mult = 1.f;
       } else {
@@ -1031,7 +1101,7 @@ __global__ void __launch_bounds__(AttnCfg<KVT, NT, kPair>::kThreads,
         const bool tail = pos0 + kPageSize > cur_L;
         VMask vm;
         vm.init(t, cur_L - pos0);
-        if constexpr (Cfg::kRowScaled) {
+        if constexpr (Cfg::kRefillEarly) {
           // the stage is free once its V codes are in registers: refill it
           // with this warp's page S ahead before the PV products
           page_pv<KVT, NT>(T, g, t, pb, tail, vm, o, [&]() {
@@ -1044,7 +1114,7 @@ __global__ void __launch_bounds__(AttnCfg<KVT, NT, kPair>::kThreads,
           page_pv<KVT, NT>(T, g, t, pb, tail, vm, o, []() {});
         }
       }
-      if constexpr (!Cfg::kRowScaled) {
+      if constexpr (!Cfg::kRefillEarly) {
         // the stage is free again: refill it with this warp's page S ahead
         __syncwarp();
         fence_proxy_async_smem();

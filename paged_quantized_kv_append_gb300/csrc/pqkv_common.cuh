@@ -289,4 +289,55 @@ __device__ __forceinline__ void int8_word(uint32_t w, uint32_t& lo, uint32_t& hi
   hi = *reinterpret_cast<uint32_t*>(&hh);
 }
 
+// ---------------------------------------------------------------------------
+// 4-bit codes -> fp16 (include/pqkv.h: PQKV_KV_INT4_GROUP)
+// ---------------------------------------------------------------------------
+constexpr int kInt4Group = 32;        // values that share a scale
+constexpr int kInt4Codes = 1024;      // bytes of a K or V tile's codes; its scales follow
+constexpr int kInt4Tile = 1152;       // bytes of a K or V tile
+
+// Where row `line` * 2 + odd of a 4-bit K or V tile keeps the 16 bytes of its group c.
+// The chunks of a 128-byte line (two rows) are turned by f = 0, 5, 2, 7 from line to
+// line: the eight lanes of a phase then read eight different chunks both where they
+// share a line (K here), where they hold rows of four lines at one group (a row per
+// thread), and where they read 8 bytes of two groups in four lines (V here).
+__device__ __forceinline__ int int4_chunk(int line, int odd, int c) {
+  const int f = ((line & 1) * 5) ^ (line & 2);
+  return line * 128 + (((odd * 4 + c) ^ f) << 4);
+}
+
+// The value of code c under the scale s is c s: c has 3 bits and a sign, s 8 bits, so
+// the product is an fp16 value.  A field of the word, n = c + 8, placed in the upper
+// mantissa bits under the exponent of 16 reads as 16 + n, and (16 + n) s - 24 s = c s is one
+// fused multiply-add without a rounding (24 s has at most 10 bits, and s at most 2720
+// keeps it finite).
+struct Int4Scale {
+  __half2 s, b;                       // s and -24 s
+  __device__ __forceinline__ explicit Int4Scale(__half2 scale) : s(scale) {
+    b = __hmul2(scale, __half2(__half(-24.0f), __half(-24.0f)));
+  }
+};
+
+__device__ __forceinline__ uint32_t int4_field(uint32_t w, const Int4Scale& sc) {
+  const uint32_t v = (w & 0x03C003C0u) | 0x4C004C00u;
+  const __half2 h = __hfma2(*reinterpret_cast<const __half2*>(&v), sc.s, sc.b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// The four fields of a word: field f of its halves is values 2 f and 2 f + 1 of the
+// word's eight (or, with halves of two rows' words, one value of either row).  Fields 0
+// to 2 lie at bits 6, 2 and 10 of a half, field 3 at bits 14, 15, 0, 1, so that swapping
+// the half's bytes (`swapped`) puts it at bit 6.
+__device__ __forceinline__ void int4_pair(uint32_t w, uint32_t swapped, const Int4Scale& sc,
+                                          uint32_t (&out)[4]) {
+  out[0] = int4_field(w, sc);
+  out[1] = int4_field(w << 4, sc);
+  out[2] = int4_field(w >> 4, sc);
+  out[3] = int4_field(swapped, sc);
+}
+
+__device__ __forceinline__ void int4_word(uint32_t w, const Int4Scale& sc, uint32_t (&out)[4]) {
+  int4_pair(w, __byte_perm(w, 0, 0x2301), sc, out);
+}
+
 }  // namespace pqkv

@@ -36,7 +36,8 @@ struct AttnParams {
   uint16_t* out;
   const int32_t* block_table;
   const int32_t* seq_lens;
-  const float* k_scale;     // INT8_ROW: the fp16 row scales [num_pages][Hkv][8][4]
+  const float* k_scale;     // INT8_ROW: the fp16 row scales [num_pages][Hkv][8][4];
+                            // INT4_GROUP: the pool itself (its tiles are copied untiled)
   const float* v_scale;
   int32_t* counters;        // [B*Hkv] merge tickets (workspace)
   float* part_o;            // [slots][RP][128] unnormalised partial outputs
@@ -90,6 +91,8 @@ cudaError_t launch_attention_int8(const AttnParams& p, const CUtensorMap& map, i
                                   int nt, bool pair, cudaStream_t stream);
 cudaError_t launch_attention_int8_row(const AttnParams& p, const CUtensorMap& map, int grid,
                                       int nt, bool pair, cudaStream_t stream);
+cudaError_t launch_attention_int4_group(const AttnParams& p, const CUtensorMap& map, int grid,
+                                        int nt, bool pair, cudaStream_t stream);
 // Resident blocks per SM of the attention kernel for a KV format, n-tile
 // count, block shape (pair: the 8-row decode as two 8-warp blocks per SM)
 // and number of sequences (0 if the query fails).
@@ -97,6 +100,7 @@ int attention_blocks_per_sm_fp16(int nt, bool pair, int num_seqs);
 int attention_blocks_per_sm_e4m3(int nt, bool pair, int num_seqs);
 int attention_blocks_per_sm_int8(int nt, bool pair, int num_seqs);
 int attention_blocks_per_sm_int8_row(int nt, bool pair, int num_seqs);
+int attention_blocks_per_sm_int4_group(int nt, bool pair, int num_seqs);
 
 cudaError_t launch_attention_partial_fp16(const AttnPartialParams& p, const CUtensorMap& map,
                                           int grid, int nt, bool pair,
@@ -110,6 +114,8 @@ cudaError_t launch_attention_partial_int8(const AttnPartialParams& p, const CUte
 cudaError_t launch_attention_partial_int8_row(const AttnPartialParams& p, const CUtensorMap& map,
                                               int grid, int nt, bool pair,
                                           cudaStream_t stream);
+cudaError_t launch_attention_partial_int4_group(const AttnPartialParams& p, const CUtensorMap& map,
+                                                int grid, int nt, bool pair, cudaStream_t stream);
 cudaError_t launch_attention_window_fp16(const AttnWindowParams& p, const CUtensorMap& map,
                                          int grid, int nt, cudaStream_t stream);
 cudaError_t launch_attention_window_e4m3(const AttnWindowParams& p, const CUtensorMap& map,
@@ -118,6 +124,8 @@ cudaError_t launch_attention_window_int8(const AttnWindowParams& p, const CUtens
                                          int grid, int nt, cudaStream_t stream);
 cudaError_t launch_attention_window_int8_row(const AttnWindowParams& p, const CUtensorMap& map,
                                              int grid, int nt, cudaStream_t stream);
+cudaError_t launch_attention_window_int4_group(const AttnWindowParams& p, const CUtensorMap& map,
+                                               int grid, int nt, cudaStream_t stream);
 cudaError_t launch_attention_wait_test_e4m3(const AttnWaitTestParams& p, const CUtensorMap& map,
                                             int grid, int nt, cudaStream_t stream);
 cudaError_t launch_lse_merge(const float* part_o, const float* part_lse, int num_parts,
@@ -130,6 +138,29 @@ constexpr int kAppendThreads = 256;
 constexpr int kAppendUnroll = 1;
 cudaError_t launch_append(const AppendParams& p, int kv_dtype, int grid, cudaStream_t stream);
 int append_blocks_per_sm(int kv_dtype);
+
+// Tokens of requests read out of the pool into contiguous fp16 rows.
+struct ReadParams {
+  const uint8_t* pages;
+  const uint16_t* row_scales;    // INT8_ROW: as in AppendParams
+  const int32_t* block_table;
+  const int32_t* first_pos;      // may be null (all 0)
+  const int32_t* token_offsets;  // [num_seqs + 1]
+  const float* k_scale;
+  const float* v_scale;
+  uint16_t* k;                   // fp16 bits
+  uint16_t* v;
+  int32_t* status;
+  int64_t num_pages;
+  int64_t k_stride;              // elements between tokens
+  int64_t v_stride;
+  int32_t scale_per_head;
+  int32_t num_seqs;
+  int32_t num_tokens;
+  int32_t num_kv_heads;
+  int32_t bt_stride;             // max_pages_per_seq
+};
+cudaError_t launch_read(const ReadParams& p, int kv_dtype, int sms, cudaStream_t stream);
 
 // Block tables grown (extend) and shortened (truncate) on the device.
 struct ExtendParams {

@@ -49,6 +49,7 @@ FP16 = 0
 FP8_E4M3 = 1
 INT8 = 2
 INT8_ROW = 3          # INT8 with a scale per (token, kv-head) row, computed at append time
+INT4_GROUP = 5        # 4 bits with a scale per group of 32 values, computed at append time
 DTYPE_NAMES = {FP16: "fp16", FP8_E4M3: "fp8_e4m3", INT8: "int8"}
 
 _TABLE_CACHE = {}
@@ -181,12 +182,16 @@ class Workload:
         """Algorithmic KV bytes one attention pass must read: K and V of every
         cached token of every sequence and kv-head (with their row scales)."""
         rows = sum(self.seq_lens) * self.num_kv_heads
+        if self.kv_dtype == INT4_GROUP:
+            return rows * 2 * 72                 # 64 bytes of codes and 8 of scales
         return rows * (self.head_dim * 2 * self.elem_bytes + self.row_scale_bytes)
 
     def append_bytes(self, tokens: int) -> int:
         """Algorithmic bytes of one append of ``tokens`` tokens: fp16 K and V
         read, codes (and row scales) written, int64 slots read."""
         n = tokens * self.num_kv_heads * self.head_dim * 2
+        if self.kv_dtype == INT4_GROUP:
+            return n * 2 + tokens * self.num_kv_heads * 2 * 72 + tokens * 8
         return (n * 2 + n * self.elem_bytes + tokens * self.num_kv_heads * self.row_scale_bytes
                 + tokens * 8)
 
@@ -328,12 +333,12 @@ def calibrated_scales(w: Workload, device="cpu"):
     """Per-layer (or per-kv-head for INT8) scales: amax of the layer's fp16 K
     (resp. V) over every cached token, divided by the format's largest value.
 
-    Returns float32 tensors of shape [1] or [Hkv] on ``device``.  FP16 and
-    INT8_ROW pools take no scale argument; ones are returned so callers can
-    pass something.
+    Returns float32 tensors of shape [1] or [Hkv] on ``device``.  FP16,
+    INT8_ROW and INT4_GROUP pools take no scale argument; ones are returned so
+    callers can pass something.
     """
     H = w.num_kv_heads
-    if w.kv_dtype in (FP16, INT8_ROW):
+    if w.kv_dtype in (FP16, INT8_ROW, INT4_GROUP):
         one = torch.ones(H if w.scale_per_head else 1, dtype=torch.float32, device=device)
         return one, one.clone()
     qmax = 448.0 if w.kv_dtype == FP8_E4M3 else 127.0
