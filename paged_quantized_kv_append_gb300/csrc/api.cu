@@ -302,9 +302,10 @@ int plan_attention_launch(const AttnArgs& a, AttnLaunch* L) {
       lmax = std::min<int64_t>(lmax, (int64_t)a.window + a.q_len - 1 + a.page_size);
     const int64_t units =
         (int64_t)a.num_seqs * a.num_kv_heads * ((lmax + a.page_size - 1) / a.page_size);
-    pair = nt == 1 && a.kv_dtype != PQKV_KV_FP16 && a.window == 0 &&
+    pair = nt == 1 && a.kv_dtype != PQKV_KV_FP16 && a.kv_dtype != PQKV_KV_INT4_GROUP && a.window == 0 &&
            units <= kPairMaxUnitsPerSm * sms;
-    const int per_sm = blocks_per_sm(a.kv_dtype, nt, pair, a.num_seqs);
+    const int per_sm =
+        a.kv_dtype == PQKV_KV_INT4_GROUP ? 1 : blocks_per_sm(a.kv_dtype, nt, pair, a.num_seqs);
     if (per_sm <= 0) return PQKV_ECUDA;
     const int64_t want = (units + kMinPagesPerBlock - 1) / kMinPagesPerBlock;
     const int64_t cap = std::min<int64_t>((int64_t)sms * per_sm, (int64_t)kMaxGrid);

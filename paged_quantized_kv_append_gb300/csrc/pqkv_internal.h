@@ -126,6 +126,12 @@ cudaError_t launch_attention_window_int8_row(const AttnWindowParams& p, const CU
                                              int grid, int nt, cudaStream_t stream);
 cudaError_t launch_attention_window_int4_group(const AttnWindowParams& p, const CUtensorMap& map,
                                                int grid, int nt, cudaStream_t stream);
+// 4-bit pools, balanced calls: the tcgen05 kernels (int4_umma.cuh), at most one block per SM
+cudaError_t launch_int4_umma_plain(const AttnParams& p, int grid, int nt, cudaStream_t stream);
+cudaError_t launch_int4_umma_partial(const AttnPartialParams& p, int grid, int nt,
+                                     cudaStream_t stream);
+cudaError_t launch_int4_umma_window(const AttnWindowParams& p, int grid, int nt,
+                                    cudaStream_t stream);
 cudaError_t launch_attention_wait_test_e4m3(const AttnWaitTestParams& p, const CUtensorMap& map,
                                             int grid, int nt, cudaStream_t stream);
 cudaError_t launch_lse_merge(const float* part_o, const float* part_lse, int num_parts,

@@ -29,13 +29,6 @@ struct ReadPiece {
   uint16_t* out;                       // null: the row is left as it is
 };
 
-// 32 bytes, a whole sector per lane
-__device__ __forceinline__ void stg256(uint16_t* dst, const uint32_t (&v)[8]) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(v[0]),
-               "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-               : "memory");
-}
-
 template <int KVT>
 __global__ void __launch_bounds__(kReadThreads) read_kernel(const ReadParams p) {
   using Piece = ReadPiece<KVT>;
