@@ -83,7 +83,7 @@ int blocks_per_sm(int kv_dtype, int nt, bool pair, int num_seqs) {
     case PQKV_KV_FP8_E4M3: return attention_blocks_per_sm_e4m3(nt, pair, num_seqs);
     case PQKV_KV_INT8: return attention_blocks_per_sm_int8(nt, pair, num_seqs);
     case PQKV_KV_INT8_ROW: return attention_blocks_per_sm_int8_row(nt, pair, num_seqs);
-    case PQKV_KV_INT4_GROUP: return attention_blocks_per_sm_int4_group(nt, pair, num_seqs);
+    case PQKV_KV_INT4_GROUP: return 1;      // of the tcgen05 kernel
   }
   return 0;
 }
@@ -302,10 +302,10 @@ int plan_attention_launch(const AttnArgs& a, AttnLaunch* L) {
       lmax = std::min<int64_t>(lmax, (int64_t)a.window + a.q_len - 1 + a.page_size);
     const int64_t units =
         (int64_t)a.num_seqs * a.num_kv_heads * ((lmax + a.page_size - 1) / a.page_size);
-    pair = nt == 1 && a.kv_dtype != PQKV_KV_FP16 && a.kv_dtype != PQKV_KV_INT4_GROUP && a.window == 0 &&
+    pair = nt == 1 && a.kv_dtype != PQKV_KV_FP16 && a.kv_dtype != PQKV_KV_INT4_GROUP &&
+           a.window == 0 &&
            units <= kPairMaxUnitsPerSm * sms;
-    const int per_sm =
-        a.kv_dtype == PQKV_KV_INT4_GROUP ? 1 : blocks_per_sm(a.kv_dtype, nt, pair, a.num_seqs);
+    const int per_sm = blocks_per_sm(a.kv_dtype, nt, pair, a.num_seqs);
     if (per_sm <= 0) return PQKV_ECUDA;
     const int64_t want = (units + kMinPagesPerBlock - 1) / kMinPagesPerBlock;
     const int64_t cap = std::min<int64_t>((int64_t)sms * per_sm, (int64_t)kMaxGrid);

@@ -73,7 +73,8 @@ struct AttnCfg {
   // and the 32-row one gained nothing.
   static constexpr int kFragUnits =
       kPair ? 60 : ((KVT == PQKV_KV_INT8_ROW && NT == 3) ? 120 : (kWideTree ? 60 : 0));
-  static_assert(!kPair || (NT == 1 && KVT != PQKV_KV_FP16), "paired blocks: 8-row 8-bit decode only");
+  static_assert(!kPair || (NT == 1 && KVT != PQKV_KV_FP16 && KVT != PQKV_KV_INT4_GROUP),
+                "paired blocks: 8-row 8-bit decode only");
   static constexpr int kThreads = kW * 32;
   static constexpr int kLines = (KVT == PQKV_KV_FP16) ? 64 : 32;   // 128-B lines per tile
   static constexpr bool kInt4 = (KVT == PQKV_KV_INT4_GROUP);

@@ -1,5 +1,6 @@
-// Paged attention instantiations for 4-bit codes with a scale per group of 32
-// values (kept in its own translation unit so the formats compile in parallel).
+// Paged attention over 4-bit codes with a scale per group of 32 values: balanced calls run
+// on tcgen05 (int4_umma.cuh), fixed splits, whose blocks each take one partition, in the
+// kernel that the other formats use.
 #include "attention_launch.cuh"
 
 namespace pqkv {
@@ -8,10 +9,6 @@ cudaError_t launch_attention_int4_group(const AttnParams& p, const CUtensorMap& 
                                       int nt, bool pair, cudaStream_t stream) {
   if (p.num_splits == 0) return launch_int4_umma_plain(p, grid, nt, stream);
   return launch_attention_dtype<PQKV_KV_INT4_GROUP>(p, map, grid, nt, pair, stream);
-}
-
-int attention_blocks_per_sm_int4_group(int nt, bool pair, int num_seqs) {
-  return blocks_per_sm_dtype<PQKV_KV_INT4_GROUP>(nt, pair, num_seqs);
 }
 
 cudaError_t launch_attention_partial_int4_group(const AttnPartialParams& p, const CUtensorMap& map,

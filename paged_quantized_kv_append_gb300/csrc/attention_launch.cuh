@@ -101,13 +101,14 @@ cudaError_t launch_attention_window_dtype(const AttnWindowParams& p, const CUten
   }
 }
 
-// pair: the 8-row decode as two 8-warp blocks per SM (8-bit formats only)
+// pair: the 8-row decode as two 8-warp blocks per SM (8-bit formats only; 4-bit pools come
+// here with fixed splits alone, see int4_umma.cuh)
 template <int KVT>
 cudaError_t launch_attention_partial_dtype(const AttnPartialParams& p, const CUtensorMap& map,
                                            int grid, int nt, bool pair, cudaStream_t stream) {
   switch (nt) {
     case 1:
-      if constexpr (KVT != PQKV_KV_FP16)
+      if constexpr (KVT != PQKV_KV_FP16 && KVT != PQKV_KV_INT4_GROUP)
         if (pair) return launch_attention_partial_t<KVT, 1, true>(p, map, grid, stream);
       return launch_attention_partial_t<KVT, 1>(p, map, grid, stream);
     case 2: return launch_attention_partial_t<KVT, 2>(p, map, grid, stream);
@@ -122,7 +123,7 @@ cudaError_t launch_attention_dtype(const AttnParams& p, const CUtensorMap& map, 
                                    bool pair, cudaStream_t stream) {
   switch (nt) {
     case 1:
-      if constexpr (KVT != PQKV_KV_FP16)
+      if constexpr (KVT != PQKV_KV_FP16 && KVT != PQKV_KV_INT4_GROUP)
         if (pair) return launch_attention_t<KVT, 1, true>(p, map, grid, stream);
       return launch_attention_t<KVT, 1>(p, map, grid, stream);
     case 2: return launch_attention_t<KVT, 2>(p, map, grid, stream);
@@ -136,7 +137,7 @@ template <int KVT>
 int blocks_per_sm_dtype(int nt, bool pair, int num_seqs) {
   switch (nt) {
     case 1:
-      if constexpr (KVT != PQKV_KV_FP16)
+      if constexpr (KVT != PQKV_KV_FP16 && KVT != PQKV_KV_INT4_GROUP)
         if (pair) return blocks_per_sm_t<KVT, 1, true>(num_seqs);
       return blocks_per_sm_t<KVT, 1>(num_seqs);
     case 2: return blocks_per_sm_t<KVT, 2>(num_seqs);

@@ -39,7 +39,8 @@ extern "C" int pqkv_testing_attention_wait_timeout(
   AttnLaunch L;
   rc = plan_attention_launch(a, &L);
   if (rc || num_seqs == 0) return rc;
-  if (kv_dtype != PQKV_KV_FP8_E4M3 || L.nt != 3) return PQKV_EUNSUPPORTED;
+  const bool int4 = kv_dtype == PQKV_KV_INT4_GROUP && num_splits == 0;
+  if ((kv_dtype != PQKV_KV_FP8_E4M3 && !int4) || L.nt != 3) return PQKV_EUNSUPPORTED;
   if (skip_block < 0 || skip_block >= L.grid || skip_page < 0) return PQKV_EINVAL;
   AttnWaitTestParams p;
   CUtensorMap map;
@@ -48,6 +49,10 @@ extern "C" int pqkv_testing_attention_wait_timeout(
   p.out = static_cast<uint16_t*>(out);
   p.skip_block = skip_block;
   p.skip_page = skip_page;
+  if (int4)
+    return launch_int4_umma_wait_test(p, L.grid, static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? PQKV_OK
+               : PQKV_ECUDA;
   return launch_attention_wait_test_e4m3(p, map, L.grid, L.nt,
                                          static_cast<cudaStream_t>(stream)) == cudaSuccess
              ? PQKV_OK

@@ -7,14 +7,25 @@
 //     P^T = 2^(S^T c - m)   (fp16, shared memory)
 //     O^T += V^T P^T   (128 dims x N x 128 keys, V and P in shared memory, O in TMEM)
 // so a row of the short side costs next to nothing, and the work is what 4 bits need: the
-// codes of a tile become 32768 fp16 values, two per three instructions.
+// codes of a tile become 32768 fp16 values (each exact), 11 instructions for eight.
 //
 // One CTA per SM takes a contiguous share of the tiles of all segments.  Warps: 0-3 the
 // softmax (a key per thread), 4-7 and 8-11 widen K and V (a key per thread: K's row goes
 // to the thread's TMEM lane, V's to shared memory), 12-15 bring a fragment's query rows
 // and write its O, m and l (and merge a segment's partial results, when the CTA is the
-// segment's last), 16 the copies, 17 the products, 18 the fragments of the share.  Every
-// stage is two deep, the codes four tiles, so a fragment's end overlaps the next one.
+// segment's last), 16 and 19 the copies, 17 the products, 18 the fragments of the share.
+// Every stage is two deep, the codes up to eight tiles, so a fragment's end overlaps the
+// next one.
+//
+// What bounds it: the instructions around a tile.  The 18432 bytes of a tile are 780 cycles
+// of an SM's share of the memory; a tile takes 1530 (8 x 131072 keys, 8 heads, 20 rows:
+// 350 us, 3.45 TB/s, 51 % of the measured copy; 32 rows 43 %; one row of 16 heads 50 %).  K's and
+// V's warps work all of that time: four turns of 145 cycles for 16 values a thread and
+// 130 to 180 for their store.  Tried and slower: a second group of warps each for K and V
+// (355 us), a second softmax for every other tile (460), waits by one warp of a group and a
+// barrier (400), one warp for the scores' products and one for V's (365), K and V in one loop
+// (393), and their rows unrolled in full (600): a scheduler's warps run a code each, and
+// what does not fit its instruction cache together is fetched again for every tile.
 #pragma once
 
 #include "attention_launch.cuh"
@@ -51,30 +62,35 @@ struct I4Cfg {
                 "registers of the launch");
   static constexpr int kRP = 8 * NT;                     // rows that are computed
   static constexpr int kN = NT <= 2 ? 16 : 32;           // columns of the products
-  static constexpr int kStages = 4;
+  static constexpr int kMaxStages = 8;                   // of the codes, as far as they fit
   static constexpr int kSlab = kI4Pages * kI4PageBytes;  // a tile's codes and scales
   static constexpr int kVTile = 2 * 128 * 128;           // two halves: 128 rows of 64 values
-  static constexpr int kPTile = 128 * 128;               // 128 rows of up to 64 values
-  static constexpr int kQHalf = 32 * 128;                // up to 32 rows of 64 values
+  static constexpr int kPTile = 128 * 64;                // 128 rows of up to 32 values
+  static constexpr int kQHalf = kN * 128;                // N rows of 64 values
   static constexpr int kFrags = 4;
-  static constexpr int kReaders = 18;                    // warps that read fragments
+  static constexpr int kReaders = 19;                    // warps that read fragments
   static constexpr int kVOff = 0;
   static constexpr int kPOff = kVOff + 2 * kVTile;
   static constexpr int kQOff = kPOff + 2 * kPTile;
-  static constexpr int kSlabOff = kQOff + 2 * 2 * kQHalf;
-  static constexpr int kFragOff = kSlabOff + kStages * kSlab;
-  static constexpr int kMaxOff = kFragOff + kFrags * (int)sizeof(I4Frag);   // [32][4] floats
+  static constexpr int kFragOff = kQOff + 2 * 2 * kQHalf;
+  static constexpr int kMaxOff = kFragOff + kFrags * (int)sizeof(I4Frag);   // [32][4]
   static constexpr int kMlOff = kMaxOff + 32 * 4 * 4;    // [2][5][32]: m, and l of 4 warps
   static constexpr int kBarOff = kMlOff + 2 * 5 * 32 * 4;
-  static constexpr int kBars = 2 * kStages + 2 * kFrags + 23;
+  static constexpr int kBars = 2 * kMaxStages + 2 * kFrags + 23;
   static constexpr int kMiscOff = kBarOff + ((kBars * 8 + 15) & ~15);
-  static constexpr int kPreOff = kMiscOff + 32;
-  static __host__ __device__ constexpr int smem_bytes(int num_seqs) {
-    return kPreOff + (3 * num_seqs + 1) * 4;
+  static constexpr int kSlabOff = (kMiscOff + 32 + 127) & ~127;
+  // the stages, and behind them three ints a sequence
+  static __host__ __device__ constexpr int pre_bytes(int num_seqs) { return (3 * num_seqs + 1) * 4; }
+  static __host__ __device__ constexpr int stages(int num_seqs) {
+    const int fit = (232448 - kSlabOff - pre_bytes(num_seqs)) / kSlab;
+    return fit < kMaxStages ? fit : kMaxStages;
   }
-  static_assert(smem_bytes(PQKV_MAX_SEQS) <= 232448, "shared memory of the largest launch");
+  static __host__ __device__ constexpr int smem_bytes(int num_seqs) {
+    return kSlabOff + stages(num_seqs) * kSlab + pre_bytes(num_seqs);
+  }
+  static_assert(stages(PQKV_MAX_SEQS) >= 4, "shared memory of the largest launch");
   // TMEM columns
-  static constexpr uint32_t kTmemK = 0, kTmemS = 128, kTmemO = 192, kTmemCols = 256;
+  static constexpr uint32_t kTmemK = 0, kTmemS = 128, kTmemO = 192;
   // kind::f16, fp32 D, M 128; S: A and B with their values along K; O: both along M and N
   static constexpr uint32_t kIdescS = (1u << 4) | ((uint32_t)(kN >> 3) << 17) | ((128u >> 4) << 24);
   static constexpr uint32_t kIdescO = kIdescS | (1u << 15) | (1u << 16);
@@ -122,20 +138,31 @@ __device__ __forceinline__ float warp_max(float v) {
   return r;
 }
 
+// P as B: rows of 64 bytes (32 values along N), 64-byte swizzle (a 16-byte chunk's index is
+// XORed with row / 2 & 3); the 8-row groups are 512 bytes apart, a k-step of 16 rows 1 KB.
+__device__ __forceinline__ uint64_t i4_p_desc(uint32_t addr) {
+  return (uint64_t)((addr & 0x3FFFF) >> 4) | ((uint64_t)1 << 16) | ((uint64_t)(512 >> 4) << 32) |
+         (uint64_t(1) << 46) | (uint64_t(4) << 61);
+}
+
 template <int NT, class PP>
 __global__ void __launch_bounds__(I4Cfg<NT>::kThreads, 1) int4_umma_kernel(const PP p) {
   using Cfg = I4Cfg<NT>;
   constexpr bool kPartial = IsPartial<PP>::value;
   constexpr bool kWin = IsWindow<PP>::value;
   constexpr bool kWaitTest = IsWaitTest<PP>::value;
-  constexpr uint32_t kWaitCycles = kWaitTest ? 1u << 21 : 1u << 31;   // 1.04 s at 2.07 GHz
-  constexpr int RP = Cfg::kRP, N = Cfg::kN, S = Cfg::kStages, F = Cfg::kFrags;
+  // looks of a wait: each takes some 100 ns, with the nap behind it.  (A look that finds
+  // nothing returns at once, and the warps' looks share a unit: without naps they made the
+  // satisfied waits cost 280 cycles.)
+  constexpr uint32_t kLooks = kWaitTest ? 1u << 13 : 1u << 23;
+  constexpr int RP = Cfg::kRP, N = Cfg::kN, F = Cfg::kFrags;
+  const uint32_t S = (uint32_t)Cfg::stages(p.num_seqs);
   extern __shared__ __align__(1024) uint8_t smem[];       // the swizzle's atoms are 1 KB
   const uint32_t sbase = smem_u32(smem);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Cfg::kBarOff);
   uint64_t* slab_full = bars;             // [S] a tile's codes have landed
-  uint64_t* slab_empty = bars + S;        // [S] they are in registers
-  uint64_t* k_full = bars + 2 * S;        // [2] K in TMEM
+  uint64_t* slab_empty = bars + Cfg::kMaxStages;   // [S] they are in registers
+  uint64_t* k_full = bars + 2 * Cfg::kMaxStages;        // [2] K in TMEM
   uint64_t* pv_full = k_full + 2;         // [2] V and the probabilities in shared memory
   uint64_t* s_full = k_full + 4;          // [2] scores in TMEM (K is read)
   uint64_t* pv_done = k_full + 6;         // [2] V and the probabilities are read
@@ -159,14 +186,14 @@ __global__ void __launch_bounds__(I4Cfg<NT>::kThreads, 1) int4_umma_kernel(const
   I4Frag* frags = reinterpret_cast<I4Frag*>(smem + Cfg::kFragOff);
   float* sMax = reinterpret_cast<float*>(smem + Cfg::kMaxOff);
   float* sMl = reinterpret_cast<float*>(smem + Cfg::kMlOff);
-  int* pre = reinterpret_cast<int*>(smem + Cfg::kPreOff);   // [B + 1] tiles before
+  int* pre = reinterpret_cast<int*>(smem + Cfg::kSlabOff + S * Cfg::kSlab);   // [B + 1] tiles before
   int* slen = pre + p.num_seqs + 1;                          // [B]
   int* sfp = slen + p.num_seqs;                              // [B] first page read (window)
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int B = p.num_seqs, H = p.num_kv_heads;
   if (tid == 0) {
-    for (int i = 0; i < S; ++i) {
+    for (uint32_t i = 0; i < S; ++i) {
       mbar_init(&slab_full[i], 1);
       mbar_init(&slab_empty[i], 8);
     }
@@ -248,27 +275,16 @@ __global__ void __launch_bounds__(I4Cfg<NT>::kThreads, 1) int4_umma_kernel(const
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
 
-  // Bounded wait (about 1 s); when one runs out the whole CTA stops at its next waits.
-  // Called by whole warps; every lane gets the same answer.  `nap`: nanoseconds between two
-  // looks.  (A look that finds nothing returns at once, and the warps' looks share a unit:
-  // 19 warps looking all the time made every wait cost 280 cycles, the satisfied ones too.)
+  // Bounded wait (about a second of looks; the kernel's end reports it): when one runs out the
+  // whole CTA stops at its next waits.  Called by whole warps; every lane gets the same answer.
   auto wait = [&](uint64_t* bar, uint32_t parity, uint32_t nap = 20) -> bool {
-    uint32_t t0 = 0;
 #pragma unroll 1
-    for (uint32_t n = 0;; ++n) {
-      if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    for (uint32_t n = kLooks; !__all_sync(0xffffffffu, mbar_try_wait(bar, parity)); --n) {
+      if (n == 0) *abort_flag = 1;
+      if (*abort_flag) return false;
       __nanosleep(nap);
-      if (n & 15u) continue;
-      const uint32_t now = (uint32_t)clock();
-      if (n == 0) t0 = now;
-      if (__any_sync(0xffffffffu, now - t0 > kWaitCycles || *abort_flag)) {
-        if (lane == 0) {
-          if (!*abort_flag) report(p.status, PQKV_DEV_TIMEOUT);
-          *abort_flag = 1;
-        }
-        return false;
-      }
     }
+    return true;
   };
   auto frag_at = [&](uint32_t n, I4Frag& f) -> bool {
     if (!wait(&frag_full[n % F], (n / F) & 1)) return false;
@@ -281,11 +297,8 @@ __global__ void __launch_bounds__(I4Cfg<NT>::kThreads, 1) int4_umma_kernel(const
     f.nt = __shfl_sync(0xffffffffu, f.nt, 0);      // (warp-uniform to the compiler)
     return f.nt > 0;
   };
-  // the thread's row of a tile's slab
-  const int key = tid & 127;
-  const int line = (key & 15) >> 1, odd = key & 1;
-  const uint32_t row_at = (uint32_t)((key >> 4) * kI4PageBytes + line * 128);
-  const uint32_t row_chunk = (uint32_t)((odd * 4) ^ (((line & 1) * 5) ^ (line & 2)));
+  const int key = tid & 127;                 // of a tile, where threads have one
+
   if (warp < 4) {
     // ================= softmax: a key per thread =================
     regs_up<Cfg::kRegSoftmax>();
@@ -406,10 +419,10 @@ __global__ void __launch_bounds__(I4Cfg<NT>::kThreads, 1) int4_umma_kernel(const
           ph[r / 2] = pack_half2(pr[r], pr[r + 1]);
         }
         // (P's buffer was last read for tile tl - 2, before this tile's scores were formed)
-        const uint32_t dst = sbase + Cfg::kPOff + b * Cfg::kPTile + key * 128;
+        const uint32_t dst = sbase + Cfg::kPOff + b * Cfg::kPTile + key * 64;
 #pragma unroll
         for (int k = 0; k < NT; ++k)
-          sts128(dst + ((k ^ (key & 7)) << 4), ph[4 * k], ph[4 * k + 1], ph[4 * k + 2],
+          sts128(dst + ((k ^ ((key >> 1) & 3)) << 4), ph[4 * k], ph[4 * k + 1], ph[4 * k + 2],
                  ph[4 * k + 3]);
         fence_proxy_async_smem();
         tc_fence_before();               // the scores are read, too
@@ -455,33 +468,48 @@ __global__ void __launch_bounds__(I4Cfg<NT>::kThreads, 1) int4_umma_kernel(const
     // ================= widen the codes of K, and of V =================
     regs_down<Cfg::kRegWiden>();
     const int kv = warp >= 8;
-    const uint32_t lane_sel = (uint32_t)((warp & 3) * 32) << 16;
-    uint32_t tl = 0;
+    // the thread's row of a tile's slab: chunk of its group 0, scale of its group 0
+    const int line = (key & 15) >> 1;
+    const uint32_t row = sbase + Cfg::kSlabOff + (key >> 4) * kI4PageBytes + kv * kInt4Tile;
+    const uint32_t chunk0 =
+        row + line * 128 + ((((key & 1) * 4) ^ (((line & 1) * 5) ^ (line & 2))) << 4);
+    const uint32_t scale0 = row + kInt4Codes + (key & 15) * 2;
+    const uint32_t to_k = tmem + ((uint32_t)((warp & 3) * 32) << 16) + Cfg::kTmemK;
+    const uint32_t to_v = sbase + Cfg::kVOff + key * 128 + ((key & 7) << 4);
+    uint32_t tl = 0, stage = 0, phase = 0;
     I4Frag f;
     bool ok = true;
     for (uint32_t n = 0; ok && frag_at(n, f); ++n) {
+      int pos = f.page0 * kPageSize + key;
 #pragma unroll 1
-      for (int i = 0; i < f.nt; ++i, ++tl) {
-        const uint32_t stage = tl % S, b = tl & 1, par = (tl >> 1) & 1;
-        // the codes have landed, and the buffer of tile tl - 2 is read: a barrier per lane
+      for (int i = 0; i < f.nt; ++i, ++tl, pos += kI4Keys) {
+        const uint32_t b = tl & 1;
+        // the codes have landed, and the buffer is free: a barrier per lane
         const bool second = (lane & 1) && tl >= 2;
         if (!(ok = wait(second ? (kv ? pv_done : s_full) + b : slab_full + stage,
-                        second ? par ^ 1 : (tl / S) & 1)))
+                         (second ? (tl >> 1) + 1 : phase) & 1)))
           break;
-        // The codes into registers, and the slab may be filled again.  (The fence: the
-        // loads are done before a copy may write there.)
-        const uint32_t at = sbase + Cfg::kSlabOff + stage * Cfg::kSlab + row_at + kv * kInt4Tile;
-        const uint32_t scale = sbase + Cfg::kSlabOff + stage * Cfg::kSlab +
-                               (key >> 4) * kI4PageBytes + kv * kInt4Tile + kInt4Codes +
-                               (key & 15) * 2;
+        const uint32_t from = stage * Cfg::kSlab;
+        const uint32_t at = chunk0 + from, scale = scale0 + from;
+        // tokens behind the end may be anything, and 0 times V has to be 0 there: a scale
+        // of 0 makes it so (K's scores are masked)
+        const bool live = kv == 0 || pos < f.L;
+        // the thread's TMEM lane, or chunk 0 of its 128-byte row of V's first half (chunk k
+        // is at `^ 16 k`)
+        const uint32_t to = kv == 0 ? to_k + b * 64 : to_v + b * Cfg::kVTile;
+        tc_fence_after();
+        // A group a turn, the next one's codes read ahead (the last turn's are not used).  The
+        // slab may be filled again when the turns are done: what its loads brought has been
+        // used.
         if (kv == 0) {
-          tc_fence_after();
-          uint32_t tK = tmem + lane_sel + Cfg::kTmemK + b * 64;
-#pragma unroll 1
-          for (int g = 0; g < 4; ++g, tK += 16) {
-            const uint4 x = lds128u(at + ((row_chunk ^ g) << 4));
-            const Int4Scale s(__half2half2(lds_half(scale + g * 2 * kPageSize)));
+          uint4 x = lds128u(at);
+          __half sc = lds_half(scale);
+#pragma unroll 2
+          for (int g = 0; g < 4; ++g) {
+            const Int4Scale s(__half2half2(sc));
             const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+            x = lds128u(at ^ ((g + 1) << 4 & 48));
+            sc = lds_half(scale + ((g + 1) & 3) * 2 * kPageSize);
             uint32_t o[16];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
@@ -490,41 +518,42 @@ __global__ void __launch_bounds__(I4Cfg<NT>::kThreads, 1) int4_umma_kernel(const
 #pragma unroll
               for (int j = 0; j < 4; ++j) o[4 * k + j] = v[j];
             }
-            tmem_st16(tK, o);
+            tmem_st16(to + g * 16, o);
           }
           tmem_wait_st();
           tc_fence_before();
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(&k_full[b]);
-            mbar_arrive(&slab_empty[stage]);
-          }
         } else {
-          // tokens behind the end may be anything: 0 times them has to be 0
-          // (a scale of 0 makes them so)
-          const bool live = (f.page0 + i * kI4Pages) * kPageSize + key < f.L;
-          const uint32_t dst = sbase + Cfg::kVOff + b * Cfg::kVTile + key * 128;
-#pragma unroll 1
+          uint4 x = lds128u(at);
+          __half sc = lds_half(scale);
+#pragma unroll 2
           for (int g = 0; g < 4; ++g) {
-            const uint4 x = lds128u(at + ((row_chunk ^ g) << 4));
-            const __half sc = lds_half(scale + g * 2 * kPageSize);
             const Int4Scale s(__half2half2(live ? sc : __ushort_as_half(0)));
             const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-            const uint32_t to = dst + (g >> 1) * 16384;
+            x = lds128u(at ^ ((g + 1) << 4 & 48));
+            sc = lds_half(scale + ((g + 1) & 3) * 2 * kPageSize);
+            uint32_t o[16];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               uint32_t v[4];
               int4_word(w[k], s, v);
-              sts128(to + ((((g & 1) * 4 + k) ^ (key & 7)) << 4), v[0], v[1], v[2], v[3]);
+#pragma unroll
+              for (int j = 0; j < 4; ++j) o[4 * k + j] = v[j];
             }
+            const uint32_t half = (to + (g >> 1) * 16384) ^ ((g & 1) << 6);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              sts128(half ^ (k << 4), o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
           }
           fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(&pv_full[b]);
-            mbar_arrive(&slab_empty[stage]);
-          }
+        }
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive((kv ? pv_full : k_full) + b);
+          mbar_arrive(&slab_empty[stage]);
+        }
+        if (++stage == S) {
+          stage = 0;
+          phase ^= 1;
         }
       }
     }
@@ -682,18 +711,22 @@ __global__ void __launch_bounds__(I4Cfg<NT>::kThreads, 1) int4_umma_kernel(const
     }
   } else {
   regs_down<Cfg::kRegOther>();
-  if (warp == 16) {
-    // ================= copies =================
+  if (warp == 16 || warp == 19) {
+    // ================= copies: of the even and of the odd tiles =================
     const uint64_t policy = l2_evict_first_policy();
     const uint8_t* pool = reinterpret_cast<const uint8_t*>(p.k_scale);
-    uint32_t tl = 0;
+    const int64_t page_bytes = (int64_t)H * kI4PageBytes;
+    const uint32_t turn = warp == 19;
+    uint32_t tl = 0, stage = turn, phase = 0;
     I4Frag f;
     bool ok = true;
     for (uint32_t n = 0; ok && frag_at(n, f); ++n) {
       const int32_t* row = p.block_table + (int64_t)f.s * p.bt_stride + f.page0;
-      // lane = page of four tiles, looked up four tiles ahead; -2: no page
-      auto lookup = [&](int at) -> int {
-        const int pg = at + lane;
+      const uint8_t* src = pool + (int64_t)f.h * kI4PageBytes;
+      // lane = page of the warp's next four tiles (every other one), looked up four ahead;
+      // -2: no page
+      auto lookup = [&](int i) -> int {
+        const int pg = (i + 2 * (lane >> 3)) * kI4Pages + (lane & 7);
         if (pg >= f.pages) return -2;
         const int id = __ldg(row + pg);
         if (id < 0 || (int64_t)id >= p.num_pages) {
@@ -702,44 +735,71 @@ __global__ void __launch_bounds__(I4Cfg<NT>::kThreads, 1) int4_umma_kernel(const
         }
         return id;
       };
-      int ids = lookup(0), next = lookup(32);
+      int i = (int)((turn ^ tl) & 1);
+      int ids = lookup(i), next = lookup(i + 8);
+      int at = 0;                                            // the tile's first lane
 #pragma unroll 1
-      for (int i = 0; i < f.nt; ++i, ++tl) {
-        if (i > 0 && (i & 3) == 0) {
+      for (; i < f.nt; i += 2) {
+        if (at == 32) {
+          at = 0;
           ids = next;
-          next = lookup((i + 4) * kI4Pages);
+          next = lookup(i + 8);
         }
-        const uint32_t stage = tl % S;
-        if (tl >= S && !(ok = wait(&slab_empty[stage], (tl / S + 1) & 1))) break;
+        const uint32_t me = tl + i;
+        if (me >= S && !(ok = wait(&slab_empty[stage], phase ^ 1, 40))) break;
         uint8_t* dst = smem + Cfg::kSlabOff + stage * Cfg::kSlab;
-        const int at = (i & 3) * kI4Pages;
-        const int here = min(kI4Pages, f.pages - i * kI4Pages);
-        const uint32_t bad = (__ballot_sync(0xffffffffu, ids == -1) >> at) & 0xFFu;
-        if (__builtin_expect(bad != 0, 0)) {             // outside the pool: zeros
+        const uint32_t bad = (__ballot_sync(0xffffffffu, ids < 0) >> at) & 0xFFu;
+        bool copy = true;
+        if constexpr (kWaitTest)
+          copy = (int)blockIdx.x != p.skip_block || (int)me != p.skip_page;
+        if (copy && bad == 0) {
+          int id[kI4Pages];
+#pragma unroll
+          for (int k = 0; k < kI4Pages; ++k) id[k] = __shfl_sync(0xffffffffu, ids, at + k);
+          // (issued by one elected thread: by eight lanes, a copy took 110 cycles)
+          if (elect_one()) {
+            mbar_arrive_expect_tx(&slab_full[stage], Cfg::kSlab);
+#pragma unroll
+            for (int k = 0; k < kI4Pages; ++k)
+              bulk_load(dst + k * kI4PageBytes, src + id[k] * page_bytes, kI4PageBytes,
+                        &slab_full[stage], policy);
+          }
+        } else if (copy) {
+          // a segment's last tile, or pages outside the pool, which read as zeros
+          const int here = min(kI4Pages, f.pages - i * kI4Pages);
 #pragma unroll 1
-          for (int k = 0; k < kI4Pages; ++k)
+          for (int k = 0; k < here; ++k)
             for (int z = lane; (bad >> k & 1) && z < kI4PageBytes / 16; z += 32)
               reinterpret_cast<uint4*>(dst + k * kI4PageBytes)[z] = make_uint4(0, 0, 0, 0);
           __syncwarp();
+          const uint32_t good = ~bad & ((1u << here) - 1);
+          if (lane == 0) mbar_arrive_expect_tx(&slab_full[stage], __popc(good) * kI4PageBytes);
+          __syncwarp();
+#pragma unroll 1
+          for (int k = 0; k < here; ++k) {
+            const int id = __shfl_sync(0xffffffffu, ids, at + k);
+            if (lane == 0 && (good >> k & 1))
+              bulk_load(dst + k * kI4PageBytes, src + id * page_bytes, kI4PageBytes,
+                        &slab_full[stage], policy);
+          }
         }
-        if constexpr (kWaitTest)
-          if ((int)blockIdx.x == p.skip_block && (int)tl == p.skip_page) continue;
-        if (lane == 0)
-          mbar_arrive_expect_tx(&slab_full[stage], (here - __popc(bad)) * kI4PageBytes);
         __syncwarp();
-        const int id = __shfl_sync(0xffffffffu, ids, at + (lane & 7));
-        if (lane < here && id >= 0)
-          bulk_load(dst + lane * kI4PageBytes, pool + ((int64_t)id * H + f.h) * kI4PageBytes,
-                    kI4PageBytes, &slab_full[stage], policy);
-        __syncwarp();
+        at += kI4Pages;
+        stage += 2;
+        if (stage >= S) {
+          stage -= S;
+          phase ^= 1;
+        }
       }
+      tl += ok ? f.nt : i;
     }
     // no copy may be in flight when the CTA ends, after a wait that ran out either
     if (lane == 0)
-      for (uint32_t i = tl > S ? tl - S : 0; i < tl; ++i) {
+      for (uint32_t k = tl > S ? tl - S : 0; k < tl; ++k) {
+        if ((k & 1) != turn) continue;
         if constexpr (kWaitTest)
-          if ((int)blockIdx.x == p.skip_block && (int)i == p.skip_page) continue;
-        (void)mbar_wait(&slab_full[i % S], (i / S) & 1);
+          if ((int)blockIdx.x == p.skip_block && (int)k == p.skip_page) continue;
+        (void)mbar_wait(&slab_full[k % S], (k / S) & 1);
       }
   } else if (warp == 17) {
     // ================= products =================
@@ -748,7 +808,7 @@ __global__ void __launch_bounds__(I4Cfg<NT>::kThreads, 1) int4_umma_kernel(const
     bool ok = true;
     const uint64_t q_desc = tc_desc(sbase + Cfg::kQOff, 16),
                    v_desc = tc_desc(sbase + Cfg::kVOff, 16384),
-                   p_desc = tc_desc(sbase + Cfg::kPOff, 16);
+                   p_desc = i4_p_desc(sbase + Cfg::kPOff);
     // O^T += V^T P^T on tile `at`; acc: not the fragment's first; last: its last
     auto pv = [&](uint32_t at, uint32_t n, bool acc, bool last) -> bool {
       const uint32_t b = at & 1, par = (at >> 1) & 1;
@@ -760,7 +820,7 @@ __global__ void __launch_bounds__(I4Cfg<NT>::kThreads, 1) int4_umma_kernel(const
                        pb = p_desc + (uint64_t)(b * (Cfg::kPTile >> 4));
 #pragma unroll
         for (int k = 0; k < 8; ++k)
-          tc_mma_ss(tmem + Cfg::kTmemO + (n & 1) * 32, va + k * 128, pb + k * 128, Cfg::kIdescO,
+          tc_mma_ss(tmem + Cfg::kTmemO + (n & 1) * 32, va + k * 128, pb + k * 64, Cfg::kIdescO,
                     acc || k > 0);
         tc_commit(&pv_done[b]);
         if (last) tc_commit(&o_done[n & 1]);
@@ -777,7 +837,7 @@ __global__ void __launch_bounds__(I4Cfg<NT>::kThreads, 1) int4_umma_kernel(const
 #pragma unroll 1
       for (int i = 0; i < nt; ++i, ++tl) {
         const uint32_t b = tl & 1, par = (tl >> 1) & 1;
-        // (the scores of tile tl - 2 are read: their product with V is issued)
+        // (the scores of tile tl - 2 are read: their probabilities' product is issued)
         if (!(ok = wait(&k_full[b], par))) break;
         tc_fence_after();
         if (elect_one()) {
@@ -826,19 +886,19 @@ __global__ void __launch_bounds__(I4Cfg<NT>::kThreads, 1) int4_umma_kernel(const
           const int fp = kWin ? sfp[g.s] : 0;
           f.page0 = fp + g.pg0 * kI4Pages;
           f.pages = min((f.L + kPageSize - 1) / kPageSize, fp + g.pg1 * kI4Pages) - f.page0;
-          if constexpr (kPartial) f.lim = p.q_pos[g.s];
+          // (bounded, so that positions may be added to it)
+          if constexpr (kPartial) f.lim = max(-(1 << 30), min(p.q_pos[g.s], 1 << 30));
           else f.lim = f.L - p.q_len;
           f.seg = g.seg;
           f.cnt = sp.count_fast(g.seg, g.a, g.b, f.first);
           f.slot = g.seg + (int)blockIdx.x;
         }
         if (n >= F) {
-          bool there = false;
-          const long long t0 = clock64();
-          while (!(there = mbar_try_wait(&frag_empty[n % F], (n / F + 1) & 1))) {
+          bool there;
+          uint32_t looks = kLooks;
+          while (!(there = mbar_try_wait(&frag_empty[n % F], (n / F + 1) & 1)) && looks-- > 0 &&
+                 !*abort_flag)
             __nanosleep(200);
-            if (*abort_flag || clock64() - t0 > 2ll * kWaitCycles) break;
-          }
           if (!there) break;
         }
         frags[n % F] = f;
@@ -853,6 +913,7 @@ __global__ void __launch_bounds__(I4Cfg<NT>::kThreads, 1) int4_umma_kernel(const
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  if (tid == 0 && *abort_flag) report(p.status, PQKV_DEV_TIMEOUT);
   if (warp == 17) tmem_free_256(tmem);
 }
 
@@ -861,7 +922,7 @@ cudaError_t launch_int4_umma_t(const PP& p, int grid, cudaStream_t stream) {
   using Cfg = I4Cfg<NT>;
   static std::atomic<uint64_t> done{0};
   const cudaError_t e =
-      opt_in_smem(int4_umma_kernel<NT, PP>, Cfg::smem_bytes(PQKV_MAX_SEQS), done);
+      opt_in_smem(int4_umma_kernel<NT, PP>, 232448, done);
   if (e != cudaSuccess) return e;
   // the register split counts on the registers that the launch bounds allow; a build that
   // used fewer would wait for them forever

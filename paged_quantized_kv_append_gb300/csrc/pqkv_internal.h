@@ -100,7 +100,6 @@ int attention_blocks_per_sm_fp16(int nt, bool pair, int num_seqs);
 int attention_blocks_per_sm_e4m3(int nt, bool pair, int num_seqs);
 int attention_blocks_per_sm_int8(int nt, bool pair, int num_seqs);
 int attention_blocks_per_sm_int8_row(int nt, bool pair, int num_seqs);
-int attention_blocks_per_sm_int4_group(int nt, bool pair, int num_seqs);
 
 cudaError_t launch_attention_partial_fp16(const AttnPartialParams& p, const CUtensorMap& map,
                                           int grid, int nt, bool pair,
@@ -132,6 +131,7 @@ cudaError_t launch_int4_umma_partial(const AttnPartialParams& p, int grid, int n
                                      cudaStream_t stream);
 cudaError_t launch_int4_umma_window(const AttnWindowParams& p, int grid, int nt,
                                     cudaStream_t stream);
+cudaError_t launch_int4_umma_wait_test(const AttnWaitTestParams& p, int grid, cudaStream_t stream);
 cudaError_t launch_attention_wait_test_e4m3(const AttnWaitTestParams& p, const CUtensorMap& map,
                                             int grid, int nt, cudaStream_t stream);
 cudaError_t launch_lse_merge(const float* part_o, const float* part_lse, int num_parts,
