@@ -256,13 +256,14 @@ def kv_append_quant(k, v, slot_mapping, kv_dtype, k_scale, v_scale, pages, statu
     _on_device(dev, k=k, v=v, slot_mapping=slot_mapping, k_scale=k_scale if kd in _SCALED else None,
                v_scale=v_scale if kd in _SCALED else None)
     _check_status(status, dev)
-    lib = load_library()
-    with torch.cuda.device(dev):
-        rc = lib.pqkv_kv_append_quant(
-            _ptr(k), k.stride(0), _ptr(v), v.stride(0), _ptr(slot_mapping), T, H, HEAD_DIM, kd,
-            _ptr(k_scale if kd in _SCALED else None), _ptr(v_scale if kd in _SCALED else None),
-            sph, _ptr(pages), pages.shape[0], PAGE_SIZE, _ptr(status), _stream(pages, stream))
-    _check(rc, "kv_append_quant")
+    scaled = kd in _SCALED
+    rc = _call_on(
+        dev.index, stream, load_library().pqkv_kv_append_quant, k.data_ptr(), k.stride(0),
+        v.data_ptr(), v.stride(0), slot_mapping.data_ptr(), T, H, HEAD_DIM, kd,
+        k_scale.data_ptr() if scaled else None, v_scale.data_ptr() if scaled else None, sph,
+        pages.data_ptr(), pages.shape[0], PAGE_SIZE, None if status is None else status.data_ptr())
+    if rc:
+        _check(rc, "kv_append_quant")
     return pages
 
 
@@ -310,6 +311,7 @@ def kv_read(pages, block_table, first_pos, token_offsets, kv_dtype, k_scale, v_s
     return k, v
 
 
+@functools.lru_cache(maxsize=256)
 def workspace_size(num_seqs, q_len, num_q_heads, num_kv_heads, num_splits=0) -> int:
     return int(load_library().pqkv_paged_attention_workspace_size(
         num_seqs, q_len, num_q_heads, num_kv_heads, HEAD_DIM, num_splits))
@@ -400,24 +402,21 @@ def paged_attention(q, pages, block_table, seq_lens, q_len, kv_dtype, k_scale, v
     ws = workspace.get(need, 4 * B * H) if isinstance(workspace, Workspace) else workspace
     _on_device(dev, workspace=ws)
     ws_bytes = 0 if ws is None else ws.numel() * ws.element_size()
-    lib = load_library()
     if window < 0:
         raise ValueError("window must be >= 0")
-    with torch.cuda.device(dev):
-        if window > 0:
-            rc = lib.pqkv_paged_attention_window(
-                _ptr(q), _ptr(out), _ptr(pages), pages.shape[0], _ptr(block_table),
-                block_table.shape[1], _ptr(seq_lens), B, q_len, Hq, H, HEAD_DIM, PAGE_SIZE, kd,
-                _ptr(k_scale if kd in _SCALED else None), _ptr(v_scale if kd in _SCALED else None),
-                sph, num_splits, max_seq_len, window, _ptr(ws), ws_bytes, _ptr(status),
-                _stream(q, stream))
-        else:
-            rc = lib.pqkv_paged_attention(
-                _ptr(q), _ptr(out), _ptr(pages), pages.shape[0], _ptr(block_table),
-                block_table.shape[1], _ptr(seq_lens), B, q_len, Hq, H, HEAD_DIM, PAGE_SIZE, kd,
-                _ptr(k_scale if kd in _SCALED else None), _ptr(v_scale if kd in _SCALED else None),
-                sph, num_splits, max_seq_len, _ptr(ws), ws_bytes, _ptr(status), _stream(q, stream))
-    _check(rc, "paged_attention")
+    lib, scaled = load_library(), kd in _SCALED
+    args = [q.data_ptr(), out.data_ptr(), pages.data_ptr(), pages.shape[0], block_table.data_ptr(),
+            block_table.shape[1], seq_lens.data_ptr(), B, q_len, Hq, H, HEAD_DIM, PAGE_SIZE, kd,
+            k_scale.data_ptr() if scaled else None, v_scale.data_ptr() if scaled else None, sph,
+            num_splits, max_seq_len]
+    fn = lib.pqkv_paged_attention
+    if window > 0:
+        fn = lib.pqkv_paged_attention_window
+        args.append(window)
+    rc = _call_on(dev.index, stream, fn, *args, None if ws is None else ws.data_ptr(), ws_bytes,
+                  None if status is None else status.data_ptr())
+    if rc:
+        _check(rc, "paged_attention")
     return out
 
 

@@ -188,7 +188,8 @@ extern "C" int pqkv_kv_append_quant(const void* k, int64_t k_token_stride, const
   // that: at most one wave of the blocks that fit on every SM at once
   const int per_sm = append_blocks_per_sm(kv_dtype);
   if (per_sm < 1) return PQKV_ECUDA;
-  const int64_t work = (int64_t)num_tokens * num_kv_heads * (kHeadDim / 16);
+  const int64_t work = (int64_t)num_tokens * num_kv_heads *
+                       (kHeadDim / (kv_dtype == PQKV_KV_INT4_GROUP ? 8 : 16));
   const int64_t per_block = (int64_t)kAppendThreads * kAppendUnroll;
   const int64_t blocks = (work + per_block - 1) / per_block;
   const int grid = (int)std::min<int64_t>(blocks, (int64_t)sms * per_sm);

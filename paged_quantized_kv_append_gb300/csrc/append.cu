@@ -42,9 +42,8 @@
 // stores the fp16 scale at the row's place in the scale area that follows the
 // codes.
 //
-// 4 bits with a scale per group of 32 values (PQKV_KV_INT4_GROUP): the two lanes of a
-// group exchange their maxima, and each writes the 8 bytes of its 16 codes and one of
-// the group's two scales.
+// 4 bits with a scale per group of 32 values (PQKV_KV_INT4_GROUP): a kernel of its own, see
+// append_int4_kernel.
 #include <atomic>
 
 #include <cuda_bf16.h>
@@ -227,67 +226,93 @@ __device__ __forceinline__ uint4 quantize16(const uint4& a, const uint4& b, floa
   return make_uint4(out[0], out[1], out[2], out[3]);
 }
 
-// 4 bits: the larger of the two lanes that hold a group of 32 values (an even lane and
-// the next one; their row is wholly in range, see the kernel's loop)
-__device__ __forceinline__ float group_max2(float m) {
-  return fmaxf(m, __shfl_xor_sync(3u << (threadIdx.x & 30), m, 1));
+__device__ __forceinline__ __half2 as_half2(uint32_t w) {
+  return *reinterpret_cast<const __half2*>(&w);
+}
+
+// 4 bits: the largest |x| of a group of 32 values of K and of V, eight of each in each of
+// four lanes (their row is wholly in range, see the kernel's loop); NaN drops out
+__device__ __forceinline__ float2 group_max4(const uint4& k, const uint4& v) {
+  const __half2 mk = __hmax2(__hmax2(__habs2(as_half2(k.x)), __habs2(as_half2(k.y))),
+                             __hmax2(__habs2(as_half2(k.z)), __habs2(as_half2(k.w))));
+  const __half2 mv = __hmax2(__hmax2(__habs2(as_half2(v.x)), __habs2(as_half2(v.y))),
+                             __hmax2(__habs2(as_half2(v.z)), __habs2(as_half2(v.w))));
+  __half2 m = __hmax2(__lows2half2(mk, mv), __highs2half2(mk, mv));
+  const unsigned mask = 0xFu << (threadIdx.x & 28);
+  m = __hmax2(m, __shfl_xor_sync(mask, m, 1));
+  m = __hmax2(m, __shfl_xor_sync(mask, m, 2));
+  const float2 f = __half22float2(m);
+  return make_float2(fmaxf(f.x, 0.f), fmaxf(f.y, 0.f));       // (all NaN: 0)
 }
 
 // 4 bits: the scale of a group whose largest |x| is amax: amax / 7 with 8 significant
-// bits (bfloat16's), as an fp16 value, at most 2720
+// bits (bfloat16's), as an fp16 value, at most 2720.  The quotient is the correctly rounded
+// one: its approximation by the reciprocal, corrected by the exact remainder (Markstein,
+// "Computation of elementary functions on the IBM RISC System/6000 processor", 1990).
 __device__ __forceinline__ float int4_scale(float amax) {
-  const float q = __fdiv_rn(fminf(amax, 65504.f), 7.f);
+  constexpr float kSeventh = 1.f / 7.f;
+  const float a = fminf(amax, 65504.f), q0 = __fmul_rn(a, kSeventh);
+  const float q = __fmaf_rn(__fmaf_rn(-7.f, q0, a), kSeventh, q0);
   const float s = __bfloat162float(__float2bfloat16_rn(q));
   return fminf(__half2float(__float2half_rn(s)), 2720.f);
 }
 
-// 4 bits: the codes (+ 8) of 16 values, in the fields that int4_pair reads.  The code of
-// x is x / s rounded to a whole number, ties to even, within +-7.  z = x RN(1 / s) is
-// within 2^-22.9 of x / s (for scales whose reciprocal is a normal number: all but 0, s being at
-// least 2^-24), so c = rint(z) is the code or, next to a half-integer, its neighbour.
-// There |x| is compared with s (c -+ 1/2), an exact product (8 and 4 bits); a tie goes to the
-// even code.  Infinities saturate, NaN has code 0; under a scale of 0 every code is 0.
-__device__ __forceinline__ uint2 int4_pack16(const uint4& a, const uint4& b, float s) {
-  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-  const float r = s > 0.f ? __frcp_rn(s) : 0.f;
-  constexpr float kMagic = 12582912.0f;   // 1.5 * 2^23: adding it leaves rint in the low bits
-  uint32_t out[2] = {0, 0};
+// 4 bits: the codes (+ 8) of 8 values of a group whose largest |x| is amax, in the fields
+// that int4_pair reads.  The code of x is x / s rounded to a whole number, ties to even, within
+// +-7.  With r = 1 / s to within 2^-23 of itself (s is 0 or at least 2^-24, so r is a normal
+// number), x r is within 2^-20 of x / s.  And x / s, a quotient of 11 by 8 bits, is either a
+// half-integer or 2^-12 or more away from each of those that it can lie next to: so x r
+// rounded to a multiple of 2^-13 is on its side of them, or on them, and rounds to the
+// code.  (Ties are common: about one value in a thousand.)  Where amax / s passes 7.4 (the
+// smallest scales, and values that saturate, infinities too) or a value is NaN, the 8 are done
+// one by one: |x| is compared with s (c -+ 1/2), an exact product (8 and 4 bits).  Infinities
+// saturate, NaN has code 0; under a scale of 0 every code is 0.
+__device__ __forceinline__ uint32_t int4_pack8(const uint4& a, float s, float amax) {
+  const uint32_t w[8] = {a.x, a.y, a.z, a.w, 0, 0, 0, 0};
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+  if (s == 0.f) r = 0.f;
+  constexpr float kSnap = 1536.0f;         // 1.5 * 2^10: adding it rounds to multiples of 2^-13
+  constexpr float kMagic = 12582920.0f;    // 1.5 * 2^23 + 8: leaves the code + 8 in the low bits
+  uint32_t y[8], all = 0;
 #pragma unroll
-  for (int k = 0; k < 16; ++k) {
-    const float x = half_of(w, k);
-    // (a NaN is dropped by the maximum: it becomes -7.5 and is mended below)
-    const float z = fminf(fmaxf(__fmul_rn(x, r), -7.5f), 7.5f);
-    const float y = __fadd_rn(z, kMagic);
-    const float c = __fsub_rn(y, kMagic), d = __fsub_rn(z, c);
-    uint32_t n = (__float_as_uint(y) + 8u) & 31u;       // code + 8, in 0 .. 16
-    if (!(fabsf(d) <= 0.5f - 0x1p-14f) || !(fabsf(z) < 7.5f)) {
-      const float za = fabsf(z), ca = fabsf(c);
-      const float m = za > ca ? ca + 0.5f : ca - 0.5f;  // the half-integer near za
-      const float sm = __fmul_rn(s, m), xa = fabsf(x);
-      const int lo = (int)(m - 0.5f);
-      int mag = xa > sm || (xa == sm && (lo & 1)) ? lo + 1 : lo;
-      mag = x != x || s == 0.f ? 0 : min(mag, 7);
-      n = 8u + (uint32_t)(x < 0.f ? -mag : mag);
-    }
-    constexpr int kTurn[4] = {6, 2, 10, 14};
-    const int f = (k >> 1) & 3, e = (k & 1) * 16;
-    uint32_t& o = out[k >> 3];
-    if (f < 3) o |= n << (e + kTurn[f]);
-    else o |= ((n & 3u) << (e + 14)) | ((n >> 2) << e);
+  for (int k = 0; k < 8; ++k) {
+    const float snapped = __fsub_rn(__fmaf_rn(half_of(w, k), r, kSnap), kSnap);
+    y[k] = __float_as_uint(__fadd_rn(snapped, kMagic));
+    all |= y[k];
   }
-  return make_uint2(out[0], out[1]);
+  const bool sure = (all >> 8) == (0x4B400000u >> 8) && amax * r < 7.4f;
+  if (!sure) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float x = half_of(w, k), xa = fabsf(x);
+      const float ca = rintf(fminf(__fmul_rn(xa, r), 8.f));        // (NaN: 8)
+      // the half-integers on either side, times s
+      const float up = __fmul_rn(s, ca + 0.5f), down = __fmul_rn(s, ca - 0.5f);
+      const bool odd = (int)ca & 1;
+      float mag = ca;
+      if (xa > up || (xa == up && odd)) mag = ca + 1.f;
+      if (xa < down || (xa == down && odd)) mag = ca - 1.f;
+      mag = x != x || s == 0.f ? 0.f : fminf(mag, 7.f);
+      y[k] = (uint32_t)(8 + (int)(x < 0.f ? -mag : mag));
+    }
+  }
+  // fields 0 to 3 of the word: values (0, 1), (2, 3), (4, 5), (6, 7) in its halves
+  const uint32_t f0 = __byte_perm(y[0], y[1], 0x5410) & 0x000F000Fu;
+  const uint32_t f1 = __byte_perm(y[2], y[3], 0x5410) & 0x000F000Fu;
+  const uint32_t f2 = __byte_perm(y[4], y[5], 0x5410) & 0x000F000Fu;
+  const uint32_t f3 = __byte_perm(y[6], y[7], 0x5410) & 0x000F000Fu;
+  return (f0 << 6) | (f1 << 2) | (f2 << 10) | ((f3 & 0x00030003u) << 14) | (f3 >> 2 & 0x00030003u);
 }
 
 // Six resident blocks per SM (40 registers) for the formats with one scale;
 // the row-scale format keeps its registers (it would spill under that cap).
 template <int KVT>
-__global__ void __launch_bounds__(kAppendThreads, KVT == PQKV_KV_INT8_ROW || KVT == PQKV_KV_INT4_GROUP ? 1 : 6)
+__global__ void __launch_bounds__(kAppendThreads, KVT == PQKV_KV_INT8_ROW ? 1 : 6)
     append_kernel(const AppendParams p) {
   constexpr int kVecPerRow = kHeadDim / 16;
   constexpr int kElem = (KVT == PQKV_KV_FP16) ? 2 : 1;
-  constexpr bool kInt4 = KVT == PQKV_KV_INT4_GROUP;
-  constexpr int64_t kTile =                                         // one K (or V) tile
-      kInt4 ? kInt4Tile : (int64_t)kPageSize * kHeadDim * kElem;
+  constexpr int64_t kTile = (int64_t)kPageSize * kHeadDim * kElem;  // one K (or V) tile
   constexpr int U = kAppendUnroll;
   grid_dependency_wait();
   grid_dependents_launch();
@@ -334,21 +359,9 @@ __global__ void __launch_bounds__(kAppendThreads, KVT == PQKV_KV_INT8_ROW || KVT
       const int64_t page = slot[u] / kPageSize;
       const int off = (int)(slot[u] % kPageSize);
       uint8_t* tile = p.pages + (page * p.num_kv_heads + h[u]) * 2 * kTile;
-      // (4 bits: half of the 16 bytes of a group)
-      uint8_t* kd = tile + (kInt4 ? int4_chunk(off >> 1, off & 1, c[u] >> 1) + (c[u] & 1) * 8
-                                  : off * kHeadDim * kElem + c[u] * 16 * kElem);
+      uint8_t* kd = tile + (int64_t)off * kHeadDim * kElem + c[u] * 16 * kElem;
       uint8_t* vd = kd + kTile;
-      if constexpr (kInt4) {
-        // two lanes share a group
-        const float kscale = int4_scale(group_max2(amax16(k0[u], k1[u])));
-        const float vscale = int4_scale(group_max2(amax16(v0[u], v1[u])));
-        *reinterpret_cast<uint2*>(kd) = int4_pack16(k0[u], k1[u], kscale);
-        *reinterpret_cast<uint2*>(vd) = int4_pack16(v0[u], v1[u], vscale);
-        // the lane of a group's first half writes K's scale, the other one V's
-        uint16_t* sc = reinterpret_cast<uint16_t*>(tile + ((c[u] & 1) ? kTile : 0) + kInt4Codes) +
-                       (c[u] >> 1) * kPageSize + off;
-        *sc = __half_as_ushort(__float2half_rn((c[u] & 1) ? vscale : kscale));   // exact
-      } else if (KVT == PQKV_KV_FP16) {
+      if (KVT == PQKV_KV_FP16) {
         reinterpret_cast<uint4*>(kd)[0] = k0[u];
         reinterpret_cast<uint4*>(kd)[1] = k1[u];
         reinterpret_cast<uint4*>(vd)[0] = v0[u];
@@ -388,6 +401,48 @@ __global__ void __launch_bounds__(kAppendThreads, KVT == PQKV_KV_INT8_ROW || KVT
   }
 }
 
+// 4 bits: a thread owns 8 values of a row of K and of V (16 bytes each), sixteen
+// consecutive lanes a row, four a group.  8192 tokens of 8 heads (43 MB): 11.7 us, 3.7 TB/s;
+// it issues about as long as it loads (without the codes' arithmetic 8.8 us).  With 16 values a
+// thread, as the other formats have them, it held 64 registers and 1024 threads an SM, and
+// with ties decided value by value a third of the warps had one: 20 us.
+__global__ void __launch_bounds__(kAppendThreads, 6) append_int4_kernel(const AppendParams p) {
+  constexpr int kVecPerRow = kHeadDim / 8;
+  grid_dependency_wait();
+  grid_dependents_launch();
+  const int64_t total = (int64_t)p.num_tokens * p.num_kv_heads * kVecPerRow;
+  const int64_t pool_slots = p.num_pages * kPageSize;
+  for (int64_t i = (int64_t)blockIdx.x * kAppendThreads + threadIdx.x; i < total;
+       i += (int64_t)gridDim.x * kAppendThreads) {
+    const int c = (int)(i % kVecPerRow);
+    const int64_t th = i / kVecPerRow;
+    // (a 64-bit division costs as much as the codes of four values)
+    const int64_t t = (uint64_t)th <= 0xFFFFFFFFull ? (int64_t)((uint32_t)th / (uint32_t)p.num_kv_heads)
+                                                    : th / p.num_kv_heads;
+    const int h = (int)(th - t * p.num_kv_heads);
+    const int64_t slot = __ldg(p.slots + t);
+    const uint4 k = __ldcs(reinterpret_cast<const uint4*>(p.k + t * p.k_stride + h * kHeadDim) + c);
+    const uint4 v = __ldcs(reinterpret_cast<const uint4*>(p.v + t * p.v_stride + h * kHeadDim) + c);
+    if (slot < 0) continue;
+    if (slot >= pool_slots) {
+      if (c == 0 && h == 0) report(p.status, PQKV_DEV_SLOT_RANGE);
+      continue;
+    }
+    const int off = (int)(slot % kPageSize), g = c >> 2, w = c & 3;
+    uint8_t* tile = p.pages + ((slot / kPageSize) * p.num_kv_heads + h) * 2 * kInt4Tile;
+    // word w of the group's 16 bytes
+    uint32_t* to = reinterpret_cast<uint32_t*>(tile + int4_chunk(off >> 1, off & 1, g)) + w;
+    const float2 amax = group_max4(k, v);
+    const float ks = int4_scale(amax.x), vs = int4_scale(amax.y);
+    to[0] = int4_pack8(k, ks, amax.x);
+    to[kInt4Tile / 4] = int4_pack8(v, vs, amax.y);
+    // the group's first lane writes K's scale, its second one V's (both exact in fp16)
+    if (w < 2)
+      reinterpret_cast<__half*>(tile + w * kInt4Tile + kInt4Codes)[g * kPageSize + off] =
+          __float2half_rn(w ? vs : ks);
+  }
+}
+
 // Resident blocks per SM of the append kernel for `kv_dtype` on the current
 // device (register-limited), cached per device ordinal 0..63; 0 on error.
 int append_blocks_per_sm(int kv_dtype) {
@@ -415,8 +470,7 @@ int append_blocks_per_sm(int kv_dtype) {
                                                         kAppendThreads, 0);
       break;
     case PQKV_KV_INT4_GROUP:
-      e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, append_kernel<PQKV_KV_INT4_GROUP>,
-                                                        kAppendThreads, 0);
+      e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, append_int4_kernel, kAppendThreads, 0);
       break;
     default:
       e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, append_kernel<PQKV_KV_INT8_ROW>,
@@ -439,7 +493,7 @@ cudaError_t launch_append(const AppendParams& p, int kv_dtype, int grid, cudaStr
     case PQKV_KV_INT8_ROW:
       return launch_pdl(append_kernel<PQKV_KV_INT8_ROW>, grid, kAppendThreads, 0, stream, p);
     case PQKV_KV_INT4_GROUP:
-      return launch_pdl(append_kernel<PQKV_KV_INT4_GROUP>, grid, kAppendThreads, 0, stream, p);
+      return launch_pdl(append_int4_kernel, grid, kAppendThreads, 0, stream, p);
     default:
       return cudaErrorInvalidValue;
   }
