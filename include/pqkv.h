@@ -431,7 +431,6 @@ int pqkv_paged_attention_noalloc(const void* q, void* out, const void* pages, in
  *                   nothing between calls.  Calls that share a workspace must
  *                   not overlap on the device.
  * 1 <= num_groups <= 2048.  Bitwise reproducible run to run on one device.
- * INT4_GROUP pools: PQKV_EUNSUPPORTED.
  */
 int pqkv_paged_attention_shared_prefix(
     const void* q, void* out, const void* pages, int64_t num_pages, const int32_t* block_table,

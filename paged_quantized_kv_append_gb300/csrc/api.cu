@@ -571,7 +571,6 @@ int bind_shared_prefix(AttnArgs* a, const SharedArgs& sa, const void* out, const
   if (rc) return rc;
   rc = check_attention_args(*a);
   if (rc) return rc;
-  if (a->kv_dtype == PQKV_KV_INT4_GROUP) return PQKV_EUNSUPPORTED;
   if (sa.max_prefix_len < 0) return PQKV_EINVAL;
   if (a->num_seqs == 0) return PQKV_OK;
   if (sa.num_groups < 1 || !sa.group_offsets || !sa.prefix_lens || !aligned(sa.group_offsets, 4) ||
@@ -583,6 +582,12 @@ int bind_shared_prefix(AttnArgs* a, const SharedArgs& sa, const void* out, const
   if (!workspace || !aligned(workspace, 256) || workspace_bytes < need) return PQKV_EWORKSPACE;
   rc = current_device_sms(sms);
   if (rc) return rc;
+  if (a->kv_dtype == PQKV_KV_INT4_GROUP) {   // as in the other attention calls: the pool
+    std::memset(map, 0, sizeof(*map));
+    std::memset(prefix_map, 0, sizeof(*prefix_map));
+    a->k_scale = static_cast<const float*>(a->pages);
+    return PQKV_OK;
+  }
   rc = encode_pool_map(*a, map);
   if (rc) return rc;
   rc = encode_prefix_map(*a, prefix_map);

@@ -418,6 +418,7 @@ cudaError_t launch_shared_prefix(const AttnArgs& a, const SharedArgs& sa, void* 
     case PQKV_KV_FP16: e = launch_shared_fp16(p, prefix_map, map, stream); break;
     case PQKV_KV_FP8_E4M3: e = launch_shared_e4m3(p, prefix_map, map, stream); break;
     case PQKV_KV_INT8_ROW: e = launch_shared_int8_row(p, prefix_map, map, stream); break;
+    case PQKV_KV_INT4_GROUP: e = launch_shared_int4_group(p, prefix_map, map, stream); break;
     default: e = launch_shared_int8(p, prefix_map, map, stream); break;
   }
   if (e != cudaSuccess) return e;

@@ -41,7 +41,8 @@ struct SharedParams {
   const int32_t* seq_lens;
   const int32_t* group_offsets;
   const int32_t* prefix_lens;
-  const float* k_scale;     // INT8_ROW: the fp16 row scales after the pool's codes
+  const float* k_scale;     // INT8_ROW: the fp16 row scales after the pool's codes; INT4_GROUP:
+                            // the pool
   const float* v_scale;
   int32_t* status;
   SharedPlan plan;
@@ -141,6 +142,8 @@ cudaError_t launch_shared_int8(const SharedParams& p, const CUtensorMap& prefix_
                                const CUtensorMap& map, cudaStream_t st);
 cudaError_t launch_shared_int8_row(const SharedParams& p, const CUtensorMap& prefix_map,
                                    const CUtensorMap& map, cudaStream_t st);
+cudaError_t launch_shared_int4_group(const SharedParams& p, const CUtensorMap& prefix_map,
+                                     const CUtensorMap& map, cudaStream_t st);   // (maps unused)
 
 // Blocks per SM of the private-key launch for rows padded to 8 nt: two where registers
 // and shared memory hold them (8 rows; an fp16 block's ring takes 128 KB, and a grid of

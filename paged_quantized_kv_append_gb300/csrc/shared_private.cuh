@@ -27,8 +27,10 @@ struct WarpCfg {
   static constexpr int kW = 8;
   static constexpr int kMinBlocks = private_blocks_per_sm(KVT, NT);
   static constexpr int kThreads = kW * 32;
-  static constexpr int kTileBytes = (KVT == PQKV_KV_FP16) ? 8192 : 4096;
-  static constexpr int kStages = (KVT == PQKV_KV_FP16 || NT == 1) ? 2 : 4;   // per warp
+  static constexpr bool kInt4 = (KVT == PQKV_KV_INT4_GROUP);
+  static constexpr int kTileBytes = kInt4 ? 2 * kInt4Tile : (KVT == PQKV_KV_FP16) ? 8192 : 4096;
+  static constexpr int kStages =                                              // per warp
+      (KVT == PQKV_KV_FP16 || (NT == 1 && !kInt4)) ? 2 : 4;
   static constexpr int kRP = 8 * NT;
   static constexpr bool kRowScaled = (KVT == PQKV_KV_INT8_ROW);
   static constexpr int kQOff = kW * kStages * kTileBytes;
@@ -67,7 +69,8 @@ __global__ void __launch_bounds__(WarpCfg<KVT, NT>::kThreads, WarpCfg<KVT, NT>::
     mbar_init(&bars[tid], 1);
     fence_barrier_init();
   }
-  if (tid == 0) prefetch_tensormap(&map);
+  if constexpr (!Cfg::kInt4)
+    if (tid == 0) prefetch_tensormap(&map);
   grid_dependency_wait();
   grid_dependents_launch();
   for (int i = tid; i <= N; i += Cfg::kThreads) {
@@ -180,7 +183,25 @@ __global__ void __launch_bounds__(WarpCfg<KVT, NT>::kThreads, WarpCfg<KVT, NT>::
     bool copy = true;
     if constexpr (kWaitTest)
       copy = worker != p.skip_block || p.skip_part != 2 || issued != p.skip_tile;
-    if (copy && lane == 0) {
+    if constexpr (Cfg::kInt4) {
+      // as in the attention kernel: 2304 bytes on end, zeros outside the pool
+      const int stage = issued % S;
+      uint8_t* dst = ring + stage * Cfg::kTileBytes;
+      if (copy && id >= 0 && (int64_t)id < p.num_pages) {
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&full[stage], Cfg::kTileBytes);
+          bulk_load(dst,
+                    reinterpret_cast<const uint8_t*>(p.k_scale) +
+                        ((int64_t)id * p.num_kv_heads + h) * Cfg::kTileBytes,
+                    Cfg::kTileBytes, &full[stage], policy);
+        }
+      } else if (copy) {
+        for (int k = lane; k < Cfg::kTileBytes / 16; k += 32)
+          reinterpret_cast<uint4*>(dst)[k] = make_uint4(0, 0, 0, 0);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&full[stage]);
+      }
+    } else if (copy && lane == 0) {
       const int stage = issued % S;
       const bool id_ok = id >= 0 && (int64_t)id < p.num_pages;
       if constexpr (Cfg::kRowScaled) {
@@ -223,7 +244,7 @@ __global__ void __launch_bounds__(WarpCfg<KVT, NT>::kThreads, WarpCfg<KVT, NT>::
 #pragma unroll
       for (int k2 = 0; k2 < 4; ++k2) sQ[(k2 * NT + nt) * 32 + lane] = qv[nt][k2];
     float qk_scale = p.sm_scale_log2;
-    if constexpr (KVT != PQKV_KV_FP16 && KVT != PQKV_KV_INT8_ROW) {
+    if constexpr (kScaleArgs<KVT>) {
       const int hs = p.scale_per_head ? h : 0;
       const float ks = __ldg(p.k_scale + hs), vs = __ldg(p.v_scale + hs);
       if (!(ks > 0.f && ks <= 3.4e38f && vs > 0.f && vs <= 3.4e38f))

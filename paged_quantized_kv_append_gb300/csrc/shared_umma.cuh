@@ -12,8 +12,8 @@
 // (two partial results, joined by the merge like any others).
 //
 // Warps: 0-7 and 8-15 the softmax of stream 0 and 1 (two threads per row, each
-// with 64 of a tile's 128 keys), 16-19 and 20-23 widen the 8-bit codes of K and of
-// V to fp16 (exact; TMA writes the fp16 pool's rows into place itself), 24 and
+// with 64 of a tile's 128 keys), 16-19 and 20-23 widen the 8-bit or 4-bit codes of K and
+// of V to fp16 (exact; TMA writes the fp16 pool's rows into place itself), 24 and
 // 26 issue the copies of K and V, 25 the products, 27 announces the share's
 // fragments.
 //
@@ -26,8 +26,9 @@
 // fp16, 3200 for E4M3 and INT8 (whose widening shares the softmax's issue slots) and
 // more for INT8_ROW, which scales scores and probabilities; TMEM holds no third stream (128 columns
 // of scores and 128 of O each).  1280 rows a head against 32768 keys of E4M3, 8 heads
-// (172 GFLOP): 135 us from cold caches, 1.3 PFLOP/s; 134 MB of codes are read up to
-// five times, out of L2.  A CTA's first scores begin 6 to 7 us after it does (plan,
+// (172 GFLOP): 135 us from cold caches, 1.3 PFLOP/s (at 4 bits the
+// same: the whole call 183 us, E4M3's 181); 134 MB of codes are read up to five times, out of
+// L2.  A CTA's first scores begin 6 to 7 us after it does (plan,
 // page ids, copies, widening), its second fragment's 4 us after the first one's last.
 // Slower when measured: the codes fetched by the widening warps themselves, a page
 // prefetch into L2, the products issued by a warp per stream, 64 keys a step.
@@ -175,7 +176,8 @@ struct UmmaCfg {
   static constexpr int kKOff = kQOff + 2 * kTile;         // 2 stages
   static constexpr int kVOff = kKOff + 2 * kTile;         // 2 stages
   static constexpr int kCodeOff = kVOff + 2 * kTile;      // staged codes: slabs of 128 rows
-  static constexpr int kSlab = 128 * 128;
+  static constexpr bool kInt4 = KVT == PQKV_KV_INT4_GROUP;  // its slab: 8 pages' codes and scales
+  static constexpr int kSlab = kInt4 ? kUmmaPages * kInt4Tile : 128 * 128;
   static constexpr int kSlabs = kWide ? 0 : 2;
   static constexpr int kScOff = kCodeOff + kSlabs * kSlab;  // fp16 row scales: 4 stages of K and V
   static constexpr int kScBytes = kRowScaled ? 4 * 2 * 128 * 2 : 0;
@@ -249,7 +251,8 @@ __global__ void __launch_bounds__(896, 1)
   }
   if (tid < 16) reinterpret_cast<int*>(smem + Cfg::kLeftOff)[tid] = 0;
   if (warp == 25) tmem_alloc_512(tmem_slot);
-  if (warp == 24 && lane == 0) prefetch_tensormap(&map);
+  if constexpr (!Cfg::kInt4)
+    if (warp == 24 && lane == 0) prefetch_tensormap(&map);
   // The wait is for the private keys' kernel, of which this one needs nothing but that
   // the plan, and what the caller wrote, is visible: only this wait promises that.  An
   // order of starts does not (without it, and with the merge's plan reads before its
@@ -610,6 +613,41 @@ __global__ void __launch_bounds__(896, 1)
             }
           }
           const uint32_t dst = sbase + (kv ? Cfg::kVOff : Cfg::kKOff) + stage * Cfg::kTile;
+          if constexpr (Cfg::kInt4) {
+            // A row per thread: its four groups' codes and scales, then 32 values a group
+            // (exact), a word of codes to a chunk of eight.  A phase's eight lanes hold
+            // rows of four lines at one group, and store to one chunk of eight rows: the pool's
+            // order and the swizzle each spread them over all banks.
+            const uint8_t* tile = smem + Cfg::kCodeOff + kv * Cfg::kSlab + wt / kPageSize * kInt4Tile;
+            const int rr = wt % kPageSize;
+            uint4 c[4];
+            __half s[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              c[i] = *reinterpret_cast<const uint4*>(tile + int4_chunk(rr >> 1, rr & 1, i));
+              s[i] = reinterpret_cast<const __half*>(tile + kInt4Codes)[i * kPageSize + rr];
+            }
+            fence_proxy_async_smem();        // (as below)
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&code_empty[kv]);
+            const uint32_t at = dst + wt * 128;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const Int4Scale sc(__half2half2(s[i]));
+              const uint32_t w[4] = {c[i].x, c[i].y, c[i].z, c[i].w};
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                uint32_t x[4];
+                int4_word(w[k], sc, x);
+                const int chunk = 4 * (i & 1) + k;
+                sts128(at + (i >> 1) * Cfg::kHalf + ((chunk ^ (wt & 7)) << 4), x[0], x[1], x[2], x[3]);
+              }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&full[stage]);
+            continue;
+          }
           // the slab into registers, and it may be filled again
           uint4 c[8];
           const int j = wt & 7;
@@ -695,7 +733,30 @@ __global__ void __launch_bounds__(896, 1)
         bool copy = true;
         if constexpr (kWaitTest)
           copy = (int)blockIdx.x != p.skip_block || kv != p.skip_part || (int)n_tile != p.skip_tile;
-        if (copy && elect_one()) {
+        if constexpr (Cfg::kInt4) {
+          // (uniform) pages to copy; of the others the scales are zeroed, their codes read
+          // as zeros under them whatever they are
+          const uint32_t good =
+              __ballot_sync(0xffffffffu, id >= 0 && (int64_t)id < p.num_pages) & 0xFFu;
+          if (copy && good != 0xFFu) {
+#pragma unroll 1
+            for (int i = 0; i < kUmmaPages; ++i)
+              if (!(good >> i & 1) && lane < (kInt4Tile - kInt4Codes) / 16)
+                sts128(base + i * kInt4Tile + kInt4Codes + lane * 16, 0, 0, 0, 0);
+            fence_proxy_async_smem();
+            __syncwarp();
+          }
+          if (copy && elect_one()) {
+            mbar_arrive_expect_tx(full + stage, __popc(good) * kInt4Tile);
+            const uint8_t* src =
+                reinterpret_cast<const uint8_t*>(p.k_scale) + (2 * h + kv) * kInt4Tile;
+#pragma unroll
+            for (int i = 0; i < kUmmaPages; ++i)
+              if (good >> i & 1)
+                bulk_load(base + i * kInt4Tile, src + (int64_t)ids[i] * H * (2 * kInt4Tile),
+                          kInt4Tile, full + stage);
+          }
+        } else if (copy && elect_one()) {
           mbar_arrive_expect_tx(full + stage, kBytes);
 #pragma unroll
           for (int i = 0; i < kUmmaPages; ++i)

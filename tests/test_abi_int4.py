@@ -7,6 +7,7 @@ import paged_quantized_kv_append_gb300 as pq
 import workloads as W
 from tests.test_abi import (ECUDA, EINVAL, ERANGE, EUNSUPPORTED, OK, _append, _attn, _attn_window,
                             _header_text, lib)  # noqa: F401
+from tests.test_abi_shared_prefix import _call as _shared
 
 F = 5
 
@@ -26,6 +27,9 @@ def test_format_numbers(lib):  # noqa: F811
     assert _append(lib, dt=F, kscale=None, vscale=None) == ECUDA
     assert _attn(lib, dt=F, kscale=None, vscale=None) == ECUDA
     assert _attn_window(lib, 16, dt=F, kscale=None, vscale=None) == ECUDA
+    assert _shared(lib, dt=F, ks=None, vs=None) == ECUDA
+    assert _shared(lib, dt=6) == _shared(lib, dt=F, npages=0) == EINVAL
+    assert _shared(lib, dt=F, ps=32) == EUNSUPPORTED
 
 
 def _read(lib, **kw):  # noqa: F811
