@@ -210,8 +210,9 @@ def _row_scale_view(area: torch.Tensor, num_pages: int, num_kv_heads: int) -> to
 
 def _check_pages(pages, kd):
     want = torch.float16 if kd == FP16 else torch.uint8
-    n = _row_elems(kd)
-    if pages.dtype != want or pages.dim() != 5 or pages.shape[2:] != (2, PAGE_SIZE, n):
+    n, shape = _row_elems(kd), pages.shape
+    if pages.dtype is not want or len(shape) != 5 or shape[2] != 2 or shape[3] != PAGE_SIZE \
+            or shape[4] != n:
         raise ValueError("pages must be %s [num_pages, Hkv, 2, 16, %d], got %s %s"
                          % (want, n, pages.dtype, tuple(pages.shape)))
     if not pages.is_contiguous() or not pages.is_cuda:
@@ -237,7 +238,33 @@ def kv_append_quant(k, v, slot_mapping, kv_dtype, k_scale, v_scale, pages, statu
     ``slot_mapping`` slots (int64 [T], negative = skip) of ``pages``."""
     kd = _dtype_id(kv_dtype)
     _check_pages(pages, kd)
-    H = pages.shape[1]
+    N, H = pages.shape[:2]
+    idx, shape = pages.get_device(), k.shape
+    ks, vs, scaled, sph = k.stride(), v.stride(), kd in _SCALED, 0
+    # (one expression for what the checks below say one by one: the host's time is the
+    # call's where tokens are few)
+    if scaled or not (
+            k.dtype is torch.float16 and v.dtype is torch.float16 and len(shape) == 3
+            and shape[1] == H and shape[2] == HEAD_DIM and v.shape == shape
+            and ks[1] == HEAD_DIM and ks[2] == 1 and vs[1] == HEAD_DIM and vs[2] == 1
+            and slot_mapping.dtype is torch.int64 and slot_mapping.shape == shape[:1]
+            and slot_mapping.is_contiguous() and k.get_device() == idx
+            and v.get_device() == idx and slot_mapping.get_device() == idx):
+        sph = _check_tokens(k, v, slot_mapping, kd, k_scale, v_scale, pages, H)
+    if status is not None:
+        _check_status(status, pages.device)
+    rc = _call_on(
+        idx, stream, load_library().pqkv_kv_append_quant, k.data_ptr(), ks[0], v.data_ptr(), vs[0],
+        slot_mapping.data_ptr(), shape[0], H, HEAD_DIM, kd,
+        k_scale.data_ptr() if scaled else None, v_scale.data_ptr() if scaled else None, sph,
+        pages.data_ptr(), N, PAGE_SIZE, None if status is None else status.data_ptr())
+    if rc:
+        _check(rc, "kv_append_quant")
+    return pages
+
+
+def _check_tokens(k, v, slot_mapping, kd, k_scale, v_scale, pages, H):
+    """kv_append_quant's arguments; returns its scale_per_head."""
     for name, x in (("k", k), ("v", v)):
         if x.dtype != torch.float16 or x.dim() != 3 or x.shape[1:] != (H, HEAD_DIM):
             raise ValueError("%s must be fp16 [T, %d, 128], got %s %s" % (name, H, x.dtype, tuple(x.shape)))
@@ -255,16 +282,7 @@ def kv_append_quant(k, v, slot_mapping, kv_dtype, k_scale, v_scale, pages, statu
     dev = pages.device
     _on_device(dev, k=k, v=v, slot_mapping=slot_mapping, k_scale=k_scale if kd in _SCALED else None,
                v_scale=v_scale if kd in _SCALED else None)
-    _check_status(status, dev)
-    scaled = kd in _SCALED
-    rc = _call_on(
-        dev.index, stream, load_library().pqkv_kv_append_quant, k.data_ptr(), k.stride(0),
-        v.data_ptr(), v.stride(0), slot_mapping.data_ptr(), T, H, HEAD_DIM, kd,
-        k_scale.data_ptr() if scaled else None, v_scale.data_ptr() if scaled else None, sph,
-        pages.data_ptr(), pages.shape[0], PAGE_SIZE, None if status is None else status.data_ptr())
-    if rc:
-        _check(rc, "kv_append_quant")
-    return pages
+    return sph
 
 
 def kv_read(pages, block_table, first_pos, token_offsets, kv_dtype, k_scale, v_scale, k, v,
@@ -277,19 +295,28 @@ def kv_read(pages, block_table, first_pos, token_offsets, kv_dtype, k_scale, v_s
     behind the last request's are left as they are.  Returns (k, v)."""
     kd = _dtype_id(kv_dtype)
     _check_pages(pages, kd)
-    idx = pages.get_device()
-    H, B, T = pages.shape[1], _size(block_table), _size(k)
-    ints = [("block_table", block_table, (B, _size(block_table, 1))),
-            ("token_offsets", token_offsets, (B + 1,))]
-    if first_pos is not None:
-        ints.append(("first_pos", first_pos, (B,)))
-    _check_ints(idx, torch.int32, ints)
+    idx, (N, H) = pages.get_device(), pages.shape[:2]
+    table, T = block_table.shape, _size(k)
+    B, W = table if len(table) == 2 else (-1, -1)
+    if block_table.dtype is not torch.int32 or B < 0 or not block_table.is_contiguous() \
+            or block_table.get_device() != idx:
+        _refuse("block_table", block_table, torch.int32, (B, W), idx)
+    if token_offsets.dtype is not torch.int32 or token_offsets.shape != (B + 1,) \
+            or not token_offsets.is_contiguous() or token_offsets.get_device() != idx:
+        _refuse("token_offsets", token_offsets, torch.int32, (B + 1,), idx)
+    if first_pos is not None and (
+            first_pos.dtype is not torch.int32 or first_pos.shape != (B,)
+            or not first_pos.is_contiguous() or first_pos.get_device() != idx):
+        _refuse("first_pos", first_pos, torch.int32, (B,), idx)
+    shape, step = (T, H, HEAD_DIM), []
     for name, x in (("k", k), ("v", v)):
-        if x.dtype is not torch.float16 or x.shape != (T, H, HEAD_DIM) or x.get_device() != idx \
-                or x.stride(2) != 1 or (H > 1 and x.stride(1) != HEAD_DIM):
+        st = x.stride()
+        if x.dtype is not torch.float16 or x.shape != shape or x.get_device() != idx \
+                or st[2] != 1 or (H > 1 and st[1] != HEAD_DIM):
             raise ValueError("%s must be fp16 [T, %d, 128] on cuda:%d with contiguous heads and "
                              "dims, got %s %s (strides %s) on %s" % (
-                                 name, H, idx, x.dtype, list(x.shape), list(x.stride()), x.device))
+                                 name, H, idx, x.dtype, list(x.shape), list(st), x.device))
+        step.append(st[0])
     sph, ks, vs = 0, None, None
     if kd in _SCALED:
         sph = _check_scale(k_scale, H, "k_scale")
@@ -301,10 +328,9 @@ def kv_read(pages, block_table, first_pos, token_offsets, kv_dtype, k_scale, v_s
     if status is not None:
         _check_status(status, pages.device)
     rc = _call_on(
-        idx, stream, load_library().pqkv_kv_read, pages.data_ptr(), pages.shape[0],
-        block_table.data_ptr(), _size(block_table, 1),
+        idx, stream, load_library().pqkv_kv_read, pages.data_ptr(), N, block_table.data_ptr(), W,
         None if first_pos is None else first_pos.data_ptr(), token_offsets.data_ptr(), B, T, H,
-        HEAD_DIM, PAGE_SIZE, kd, ks, vs, sph, k.data_ptr(), k.stride(0), v.data_ptr(), v.stride(0),
+        HEAD_DIM, PAGE_SIZE, kd, ks, vs, sph, k.data_ptr(), step[0], v.data_ptr(), step[1],
         None if status is None else status.data_ptr())
     if rc:
         _check(rc, "kv_read")
@@ -372,12 +398,54 @@ def paged_attention(q, pages, block_table, seq_lens, q_len, kv_dtype, k_scale, v
     """
     kd = _dtype_id(kv_dtype)
     _check_pages(pages, kd)
-    H = pages.shape[1]
+    N, H = pages.shape[:2]
+    idx, rows, table, B = pages.get_device(), q.shape, block_table.shape, seq_lens.shape[0]
+    scaled, sph = kd in _SCALED, 0
+    # (one expression, as in kv_append_quant)
+    if scaled or not (
+            q.dtype is torch.float16 and out.dtype is torch.float16 and len(rows) == 3
+            and rows[2] == HEAD_DIM and out.shape == rows and rows[0] == B * q_len
+            and q.is_contiguous() and out.is_contiguous() and seq_lens.dtype is torch.int32
+            and seq_lens.dim() == 1 and seq_lens.is_contiguous()
+            and block_table.dtype is torch.int32 and len(table) == 2 and table[0] == B
+            and block_table.is_contiguous() and q.get_device() == idx and out.get_device() == idx
+            and seq_lens.get_device() == idx and block_table.get_device() == idx):
+        sph = _check_attention(q, pages, block_table, seq_lens, q_len, kd, k_scale, v_scale, out,
+                               H, B)
+    Hq = rows[1]
+    if status is not None:
+        _check_status(status, pages.device)
+    need = workspace_size(B, q_len, Hq, H, num_splits)
+    if workspace is None:
+        workspace = _default_workspace(pages.device)
+    ws = workspace.get(need, 4 * B * H) if isinstance(workspace, Workspace) else workspace
+    if ws is not None and ws.get_device() != idx:
+        _on_device(pages.device, workspace=ws)
+    ws_bytes = 0 if ws is None else ws.numel() * ws.element_size()
+    if window < 0:
+        raise ValueError("window must be >= 0")
+    lib = load_library()
+    args = [q.data_ptr(), out.data_ptr(), pages.data_ptr(), N, block_table.data_ptr(),
+            table[1], seq_lens.data_ptr(), B, q_len, Hq, H, HEAD_DIM, PAGE_SIZE, kd,
+            k_scale.data_ptr() if scaled else None, v_scale.data_ptr() if scaled else None, sph,
+            num_splits, max_seq_len]
+    fn = lib.pqkv_paged_attention
+    if window > 0:
+        fn = lib.pqkv_paged_attention_window
+        args.append(window)
+    rc = _call_on(idx, stream, fn, *args, None if ws is None else ws.data_ptr(), ws_bytes,
+                  None if status is None else status.data_ptr())
+    if rc:
+        _check(rc, "paged_attention")
+    return out
+
+
+def _check_attention(q, pages, block_table, seq_lens, q_len, kd, k_scale, v_scale, out, H, B):
+    """paged_attention's arguments; returns its scale_per_head."""
     if q.dtype != torch.float16 or q.dim() != 3 or q.shape[2] != HEAD_DIM or not q.is_contiguous():
         raise ValueError("q must be contiguous fp16 [num_seqs*q_len, Hq, 128]")
     if out.shape != q.shape or out.dtype != torch.float16 or not out.is_contiguous():
         raise ValueError("out must be contiguous fp16 shaped like q")
-    B = seq_lens.shape[0]
     if seq_lens.dtype != torch.int32 or seq_lens.dim() != 1 or not seq_lens.is_contiguous():
         raise ValueError("seq_lens must be contiguous int32 [num_seqs]")
     if block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.shape[0] != B \
@@ -385,39 +453,15 @@ def paged_attention(q, pages, block_table, seq_lens, q_len, kv_dtype, k_scale, v
         raise ValueError("block_table must be contiguous int32 [num_seqs, max_pages_per_seq]")
     if q.shape[0] != B * q_len:
         raise ValueError("q has %d rows, expected num_seqs*q_len = %d" % (q.shape[0], B * q_len))
-    Hq = q.shape[1]
     sph = 0
     if kd in _SCALED:
         sph = _check_scale(k_scale, H, "k_scale")
         if _check_scale(v_scale, H, "v_scale") != sph:
             raise ValueError("k_scale and v_scale must have the same shape")
-    dev = pages.device
-    _on_device(dev, q=q, out=out, block_table=block_table, seq_lens=seq_lens,
+    _on_device(pages.device, q=q, out=out, block_table=block_table, seq_lens=seq_lens,
                k_scale=k_scale if kd in _SCALED else None,
                v_scale=v_scale if kd in _SCALED else None)
-    _check_status(status, dev)
-    need = workspace_size(B, q_len, Hq, H, num_splits)
-    if workspace is None:
-        workspace = _default_workspace(dev)
-    ws = workspace.get(need, 4 * B * H) if isinstance(workspace, Workspace) else workspace
-    _on_device(dev, workspace=ws)
-    ws_bytes = 0 if ws is None else ws.numel() * ws.element_size()
-    if window < 0:
-        raise ValueError("window must be >= 0")
-    lib, scaled = load_library(), kd in _SCALED
-    args = [q.data_ptr(), out.data_ptr(), pages.data_ptr(), pages.shape[0], block_table.data_ptr(),
-            block_table.shape[1], seq_lens.data_ptr(), B, q_len, Hq, H, HEAD_DIM, PAGE_SIZE, kd,
-            k_scale.data_ptr() if scaled else None, v_scale.data_ptr() if scaled else None, sph,
-            num_splits, max_seq_len]
-    fn = lib.pqkv_paged_attention
-    if window > 0:
-        fn = lib.pqkv_paged_attention_window
-        args.append(window)
-    rc = _call_on(dev.index, stream, fn, *args, None if ws is None else ws.data_ptr(), ws_bytes,
-                  None if status is None else status.data_ptr())
-    if rc:
-        _check(rc, "paged_attention")
-    return out
+    return sph
 
 
 def paged_attention_partial(q, pages, block_table, seq_lens, q_pos, q_len, kv_dtype, k_scale,
@@ -541,7 +585,7 @@ def _call_on(idx, stream, fn, *args):
         raw = torch._C._cuda_getCurrentRawStream(idx)
     else:
         raw = stream.cuda_stream
-    if torch.cuda.current_device() == idx:
+    if torch._C._cuda_getDevice() == idx:
         return fn(*args, raw)
     with torch.cuda.device(idx):
         return fn(*args, raw)
