@@ -168,3 +168,87 @@ def test_a_wait_that_runs_out_reports_timeout_and_returns(skip_block, skip_tile)
     assert int(status.item()) == 0
     assert torch.equal(out, good)
     assert _run_test_mode(pq, c, out, ws, status, 3, 0, 0) == -2       # balanced calls alone
+
+
+@pytest.mark.parametrize("q_len,window", [(1, 40), (5, 300)])
+def test_fixed_splits_in_a_window(q_len, window):
+    p = Pool(20, [8, 40, 333, 1000], 2)
+    q = p.q(2, q_len, 8)
+    ref, bound = allowance(q, p.pages, p.bt, p.lens, q_len, window=window)
+    for splits in (1, 4):
+        assert_within(_attend(_dev(p.pages), _dev(p.bt), p.lens, q, q_len, window=window,
+                              num_splits=splits), ref, bound, "%d splits" % splits)
+
+
+@pytest.mark.parametrize("q_len", [1, 5])
+def test_fixed_splits_of_shares(q_len):
+    """Two shares (the first ends on a page's border), each in fixed splits, against its own
+    softmax: off by at most what allowance() counts with A <= M = max |V|."""
+    pq = require_gpu()
+    p = Pool(21, [40, 333, 1600], 2)
+    q = p.q(3, q_len, 8)
+    M = max(np.abs(oracle.gather_kv(p.pages, p.bt[s], L, h, F, None, None)[1]).max()
+            for s, L in enumerate(p.lens) for h in range(2))
+    for lo, hi in ((0, 2), (2, 200)):
+        n = [min(L, 16 * hi) - min(L, 16 * lo) for L in p.lens]
+        bt = np.full((3, max(1, min(hi, p.bt.shape[1]) - lo)), -1, np.int32)
+        for s in range(3):
+            row = p.bt[s, lo:hi]
+            bt[s, :len(row)] = row
+        pos = [L - q_len - 16 * lo for L in p.lens]
+        ro, rl = oracle.paged_attention_partial(q, p.pages, bt, n, pos, q_len, F, None, None)
+        for splits in (1, 3):
+            o = torch.full(q.shape, float("nan"), device="cuda")
+            lse = torch.full(q.shape[:2], float("nan"), device="cuda")
+            pq.paged_attention_partial(_dev(q), _dev(p.pages), _dev(bt), _i32(n), _i32(pos), q_len,
+                                       "int4_group", None, None, o, lse, num_splits=splits)
+            assert_within(o, ro, np.full(q.shape, M * (2.0 ** -11 + 2.0 ** -13 + 1600 * 2.0 ** -25)),
+                          "share %d, %d splits" % (lo, splits))
+            assert np.array_equal(np.isinf(lse.cpu().numpy()), np.isinf(rl))
+
+
+def test_two_streams_at_once():
+    """Calls on two streams, a workspace each, do not meet."""
+    pq = require_gpu()
+    cases = []
+    for seed, lens, q_len in ((22, [3000, 70, 900], 5), (23, [5000, 16], 1)):
+        p = Pool(seed, lens, 8)
+        q = p.q(1, q_len, 32)
+        cases.append((q_len, _dev(q), _dev(p.pages), _dev(p.bt), _i32(p.lens), pq.Workspace(),
+                      torch.cuda.Stream(), _attend(_dev(p.pages), _dev(p.bt), p.lens, q, q_len)))
+    torch.cuda.synchronize()
+    outs = [[torch.full_like(c[1], float("nan")) for _ in range(20)] for c in cases]
+    torch.cuda.synchronize()
+    for k in range(20):
+        for (q_len, q, pages, bt, lens, ws, st, _), o in zip(cases, outs):
+            pq.paged_attention(q, pages, bt, lens, q_len, "int4_group", None, None, o[k], stream=st,
+                               workspace=ws)
+    torch.cuda.synchronize()
+    for c, o in zip(cases, outs):
+        for x in o:
+            assert torch.equal(x, c[-1])
+
+
+def test_two_graphs_that_share_a_workspace():
+    """Replayed in turn on one stream, neither finds what the other left: other
+    batch sizes, heads and merges."""
+    pq = require_gpu()
+    ws, made = pq.Workspace(), []
+    for seed, lens, q_len, hq, hkv in ((24, [3000, 70, 900], 5, 24, 8), (25, [9000], 1, 16, 2),
+                                       (26, [100] * 40, 1, 8, 8)):
+        p = Pool(seed, lens, hkv)
+        q = p.q(1, q_len, hq)
+        args = (_dev(q), _dev(p.pages), _dev(p.bt), _i32(p.lens), q_len, "int4_group", None, None)
+        made.append((args, torch.empty_like(args[0]), _attend(args[1], args[2], p.lens, q, q_len)))
+        pq.paged_attention(*args, made[-1][1], workspace=ws)
+    graphs = []
+    for args, out, _ in made:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            pq.paged_attention(*args, out, workspace=ws)
+        graphs.append(g)
+    for _ in range(3):
+        for g, (_, out, want) in zip(graphs, made):
+            out.fill_(float("nan"))
+            g.replay()
+            assert torch.equal(out, want)
