@@ -18,8 +18,8 @@
 // next one.
 //
 // What bounds it: the instructions around a tile.  The 18432 bytes of a tile are 780 cycles
-// of an SM's share of the memory; a tile takes 1530 (8 x 131072 keys, 8 heads, 20 rows:
-// 350 us, 3.45 TB/s, 51 % of the measured copy; 32 rows 43 %; one row of 16 heads 50 %).  K's and
+// of an SM's share of the memory; a tile takes 1500 (8 x 131072 keys, 8 heads, 20 rows:
+// 343 us, 3.52 TB/s, 52 % of the measured copy; 32 rows 45 %; one row of 16 heads 51 %).  K's and
 // V's warps work all of that time: four turns of 145 cycles for 16 values a thread and
 // 130 to 180 for their store.  Tried and slower: a second group of warps each for K and V
 // (355 us), a second softmax for every other tile (460), waits by one warp of a group and a
@@ -36,6 +36,12 @@ namespace pqkv {
 constexpr int kI4Keys = 128;                    // keys of a tile
 constexpr int kI4Pages = kI4Keys / kPageSize;
 constexpr int kI4PageBytes = 2 * kInt4Tile;
+// A row's reference is raised when a score passes it by more than this (log2), and all rows'
+// to their largest scores then: probabilities stay <= 2^15.9, within fp16's 2^16, and the
+// largest key's is 1 or more, so each is off by half a step, 2^-11 of it or, under 2^-14,
+// 2^-25 of the largest at most.  With 8 a verify of 8 x 131072 took 350 us instead of 343, one
+// of 524288 208 instead of 200: a raise costs a tile about 1500 cycles.
+constexpr float kI4Raise = 15.9f;
 
 // A fragment of the CTA's share: tiles of one segment.
 struct I4Frag {
@@ -359,7 +365,7 @@ __global__ void __launch_bounds__(I4Cfg<NT>::kThreads, 1) int4_umma_kernel(const
           const float d = fmaf(__uint_as_float(x[r + 1]), c, -ref[r + 1]);
           top[(r >> 1) & 3] = max3(top[(r >> 1) & 3], a, d);
         }
-        const bool raise = fmaxf(max3(top[0], top[1], top[2]), top[3]) > 8.f;
+        const bool raise = fmaxf(max3(top[0], top[1], top[2]), top[3]) > kI4Raise;
         // The warps agree: the note of a tile is its number + 1 (a buffer's older notes are
         // smaller, and its next one comes after a vote that this warp is still to cast).
         // The probabilities are formed under the vote, and again if it raises.
@@ -872,26 +878,41 @@ __global__ void __launch_bounds__(I4Cfg<NT>::kThreads, 1) int4_umma_kernel(const
       // (no empty shares: a segment's partial results are those of neighbouring CTAs)
       sp.C = (int)min((int64_t)gridDim.x, sp.P);
       sp.k = 0;
-      FragIterT<false> it;
-      if ((int)blockIdx.x < sp.C) it.init(sp, blockIdx.x);
-      else it.init_range(sp, blockIdx.x, 0, 0);
+      // units [x, e) of the share, and the first one's sequence (by halving: a walk over the
+      // sequences before it, and divisions in 64 bits, took 4 us of a call for 256 sequences)
+      const auto div = [](int64_t n, int64_t d) { return SplitT<false>::udiv(n, d); };
+      int64_t x = 0, e = 0;
+      int s = 0;
+      if ((int)blockIdx.x < sp.C) {
+        x = div((int64_t)blockIdx.x * sp.P, sp.C);
+        e = div((int64_t)(blockIdx.x + 1) * sp.P, sp.C);
+        for (int hi = B - 1; s < hi;) {
+          const int mid = (s + hi) >> 1;
+          if ((int64_t)pre[mid + 1] * H > x) hi = mid; else s = mid + 1;
+        }
+      }
       for (uint32_t n = 0;; ++n) {
-        Frag g;
         I4Frag f = {};
-        if (it.next(g)) {
-          f.nt = g.pg1 - g.pg0;
-          f.s = g.s;
-          f.h = g.h;
-          f.L = slen[g.s];
-          const int fp = kWin ? sfp[g.s] : 0;
-          f.page0 = fp + g.pg0 * kI4Pages;
-          f.pages = min((f.L + kPageSize - 1) / kPageSize, fp + g.pg1 * kI4Pages) - f.page0;
+        if (x < e) {
+          while ((int64_t)pre[s + 1] * H <= x) ++s;
+          const int np = pre[s + 1] - pre[s];
+          const int64_t base = (int64_t)pre[s] * H;
+          f.s = s;
+          f.h = (int)div(x - base, np);
+          f.seg = s * H + f.h;
+          const int64_t seg_a = base + (int64_t)f.h * np, seg_b = seg_a + np;
+          const int t0 = (int)(x - seg_a);
+          f.nt = (int)(min(e, seg_b) - x);
+          x += f.nt;
+          f.L = slen[s];
+          const int fp = kWin ? sfp[s] : 0;
+          f.page0 = fp + t0 * kI4Pages;
+          f.pages = min((f.L + kPageSize - 1) / kPageSize, fp + (t0 + f.nt) * kI4Pages) - f.page0;
           // (bounded, so that positions may be added to it)
-          if constexpr (kPartial) f.lim = max(-(1 << 30), min(p.q_pos[g.s], 1 << 30));
+          if constexpr (kPartial) f.lim = max(-(1 << 30), min(p.q_pos[s], 1 << 30));
           else f.lim = f.L - p.q_len;
-          f.seg = g.seg;
-          f.cnt = sp.count_fast(g.seg, g.a, g.b, f.first);
-          f.slot = g.seg + (int)blockIdx.x;
+          f.cnt = sp.count_fast(f.seg, seg_a, seg_b, f.first);
+          f.slot = f.seg + (int)blockIdx.x;
         }
         if (n >= F) {
           bool there;
