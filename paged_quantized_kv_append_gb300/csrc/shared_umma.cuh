@@ -26,10 +26,10 @@
 // fp16, 3200 for E4M3 and INT8 (whose widening shares the softmax's issue slots) and
 // more for INT8_ROW, which scales scores and probabilities; TMEM holds no third stream (128 columns
 // of scores and 128 of O each).  1280 rows a head against 32768 keys of E4M3, 8 heads
-// (172 GFLOP): 135 us from cold caches, 1.3 PFLOP/s (at 4 bits the
-// same: the whole call 183 us, E4M3's 181); 134 MB of codes are read up to five times, out of
-// L2.  A CTA's first scores begin 6 to 7 us after it does (plan,
-// page ids, copies, widening), its second fragment's 4 us after the first one's last.
+// (172 GFLOP): 135 us from cold caches, 1.3 PFLOP/s (at 4 bits the same: the whole call
+// 183 us, E4M3's 181); 134 MB of codes are read up to five times, out of L2.  A CTA's first
+// scores begin 6 to 7 us after it does (plan, page ids, copies, widening), its second
+// fragment's 4 us after the first one's last.
 // Slower when measured: the codes fetched by the widening warps themselves, a page
 // prefetch into L2, the products issued by a warp per stream, 64 keys a step.
 #pragma once
