@@ -331,8 +331,8 @@ int pqkv_paged_attention_partial(const void* q, const void* pages, int64_t num_p
  * pqkv_lse_merge -- combine partial results of the same rows (the merge step
  * of the split above): with parts p = 0 .. num_parts-1,
  *     LSE = ln sum_p e^{lse_p},   out = sum_p e^{lse_p - LSE} o_p   (fp16)
- * Parts with lse_p = -inf contribute nothing; a row with no finite lse_p
- * gets out = 0 and LSE = -inf.
+ * Parts with lse_p = -inf contribute nothing; a row whose lse_p are all -inf
+ * gets out = 0 and LSE = -inf.  A NaN lse_p makes its row NaN.
  *   part_o    fp32 [num_parts][num_rows][head_dim], 16-byte aligned;
  *   part_lse  fp32 [num_parts][num_rows];
  *   out       fp16 [num_rows][head_dim], 16-byte aligned;

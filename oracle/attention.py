@@ -298,16 +298,17 @@ def paged_attention_partial(q, pages, block_table, seq_lens, q_pos, q_len, kv_dt
 
 def merge_lse(parts_o, parts_lse):
     """Combine partial results in (O / l, lse) form over the leading axis:
-    LSE = ln sum_p e^{lse_p}, O = sum_p e^{lse_p - LSE} O_p.  Rows with no
-    finite lse_p give O = 0, LSE = -inf."""
+    LSE = ln sum_p e^{lse_p}, O = sum_p e^{lse_p - LSE} O_p.  Rows whose lse_p
+    are all -inf give O = 0, LSE = -inf; a NaN lse_p makes its row NaN."""
     po = np.asarray(parts_o, dtype=np.float64)
     pl = np.asarray(parts_lse, dtype=np.float64)
     M = pl.max(axis=0)
-    finite = np.isfinite(M)
-    w = np.where(finite[None], np.exp(pl - np.where(finite, M, 0.0)[None]), 0.0)
+    some = M != -np.inf                                # (NaN, too)
+    M = np.where(some, M, 0.0)
+    w = np.exp(pl - M[None])                           # e^-inf = 0 where there is nothing
     tot = w.sum(axis=0)
-    o = np.einsum("p...,p...d->...d", w, po) / np.where(tot > 0, tot, 1.0)[..., None]
-    lse = np.where(tot > 0, np.where(finite, M, 0.0) + np.log(np.where(tot > 0, tot, 1.0)), -np.inf)
+    o = np.einsum("p...,p...d->...d", w, po) / np.where(some, tot, 1.0)[..., None]
+    lse = np.where(some, M + np.log(np.where(some, tot, 1.0)), -np.inf)
     return o, lse
 
 

@@ -21,28 +21,26 @@ __global__ void __launch_bounds__(256) lse_merge_kernel(const float* part_o, con
   for (int q = 0; q < num_parts; ++q) M = fmaxf(M, __ldg(part_lse + (int64_t)q * rows + row));
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   float sum = 0.f;
-  if (M > -INFINITY) {
-    for (int q = 0; q < num_parts; ++q) {
-      const float lq = __ldg(part_lse + (int64_t)q * rows + row);
-      if (!(lq > -INFINITY)) continue;                 // a share with no visible key
-      const float w = expf(lq - M);
-      const float4 v = __ldg(reinterpret_cast<const float4*>(part_o + ((int64_t)q * rows + row) *
-                                                                          kHeadDim) + lane);
-      acc.x += w * v.x;
-      acc.y += w * v.y;
-      acc.z += w * v.z;
-      acc.w += w * v.w;
-      sum += w;
-    }
+  for (int q = 0; q < num_parts; ++q) {
+    const float lq = __ldg(part_lse + (int64_t)q * rows + row);
+    if (lq == -INFINITY) continue;                     // a share with no visible key
+    const float w = expf(lq - M);                      // (of a NaN share: NaN, and so the row)
+    const float4 v = __ldg(reinterpret_cast<const float4*>(part_o + ((int64_t)q * rows + row) *
+                                                                        kHeadDim) + lane);
+    acc.x += w * v.x;
+    acc.y += w * v.y;
+    acc.z += w * v.z;
+    acc.w += w * v.w;
+    sum += w;
   }
-  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
   __half2 h01 = __floats2half2_rn(acc.x * inv, acc.y * inv);
   __half2 h23 = __floats2half2_rn(acc.z * inv, acc.w * inv);
   uint2 pk;
   pk.x = *reinterpret_cast<uint32_t*>(&h01);
   pk.y = *reinterpret_cast<uint32_t*>(&h23);
   *reinterpret_cast<uint2*>(out + row * kHeadDim + 4 * lane) = pk;
-  if (out_lse && lane == 0) out_lse[row] = sum > 0.f ? M + logf(sum) : -INFINITY;
+  if (out_lse && lane == 0) out_lse[row] = sum == 0.f ? -INFINITY : M + logf(sum);
 }
 
 cudaError_t launch_lse_merge(const float* part_o, const float* part_lse, int num_parts,
