@@ -239,6 +239,9 @@ size_t pqkv_paged_attention_workspace_size(int32_t num_seqs, int32_t q_len,
  * off by at most 2^-11 of it or 2^-25 of the row's largest; INT8_ROW: their products
  * with V's row scales), and rounded to fp16.  A V that is not finite in one of the
  * q_len new tokens also reaches the rows of the queries before it, as 0 times it.
+ * A NaN among the scores of the keys that a row sees (from a NaN or an infinity in its
+ * query, or in a K) makes the row NaN, however the keys are split; a row whose scores are
+ * all -inf gets 0.
  *
  *   q, out            fp16 [num_seqs*q_len][num_q_heads][head_dim], contiguous.
  *   pages             the pool (layout above), num_pages pages, 16-byte aligned.
@@ -313,7 +316,7 @@ int pqkv_paged_attention_window(const void* q, void* out, const void* pages, int
  *              share (0 for a row that sees no key);
  *   out_lse    fp32 [num_seqs*q_len][num_q_heads]: m + ln(l), the natural-log
  *              log-sum-exp of the row's scores over the share (-inf when the
- *              row sees no key).
+ *              row sees no key; NaN with a NaN among the scores).
  * Scores are q . K_j / sqrt(head_dim) as in pqkv_paged_attention.  out_o must
  * be 16-byte aligned.
  */

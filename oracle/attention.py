@@ -288,7 +288,7 @@ def paged_attention_partial(q, pages, block_table, seq_lens, q_pos, q_len, kv_dt
                 K, V = gather_kv(pages, block_table[s], L, h, kv_dtype,
                                  _scale_of(k_scale, h), _scale_of(v_scale, h))
             O, m, l = attention_partial(_rows_of(q, s, h, q_len, G), K, V, limits, 0, L)
-            seen = l > 0
+            seen = l != 0                 # (a NaN among the scores stays one)
             O[seen] /= l[seen][:, None]
             lr = np.where(seen, m + np.log(np.where(seen, l, 1.0)), -np.inf)
             o[s * q_len:(s + 1) * q_len, h * G:(h + 1) * G] = O.reshape(q_len, G, D)

@@ -150,6 +150,14 @@ struct AttnCfg {
 constexpr float kNoScore = -1.0e30f;
 constexpr float kLn2 = 0.6931471805599453f;
 
+// num / l of a row whose probabilities (under the reference m, in log2) add up to l, and its
+// natural-log LSE.  A row that sees no key has l = 0 and gets 0 and -inf; a NaN among its
+// scores is in l and stays one.
+__device__ __forceinline__ float row_inv(float l, float num) { return l == 0.f ? 0.f : num / l; }
+__device__ __forceinline__ float row_lse(float m, float l) {
+  return l == 0.f ? -INFINITY : (m + __log2f(l)) * kLn2;
+}
+
 __device__ __forceinline__ void fence_proxy_async_smem() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
@@ -1205,10 +1213,10 @@ __global__ void __launch_bounds__(AttnCfg<KVT, NT, kPair>::kThreads,
       if (cnt == 1) {
         const int i = r / p.group, gh = r % p.group;
         const int64_t orow = (out_row0 + i) * p.num_q_heads + f_h * p.group + gh;
-        const float val = l > 0.f ? acc / l * v_mult : 0.f;
+        const float val = l == 0.f ? 0.f : acc / l * v_mult;
         if constexpr (kPartial) {
           p.out_o[orow * kHeadDim + d] = val;
-          if (d == 0) p.out_lse[orow] = l > 0.f ? (M + __log2f(l)) * kLn2 : -INFINITY;
+          if (d == 0) p.out_lse[orow] = row_lse(M, l);
         } else {
           p.out[orow * kHeadDim + d] = __half_as_ushort(__float2half_rn(val));
         }
@@ -1279,14 +1287,13 @@ __global__ void __launch_bounds__(AttnCfg<KVT, NT, kPair>::kThreads,
             acc.z += wq * v.z;
             acc.w += wq * v.w;
           }
-          const float inv = sLrow[r] > 0.f ? v_mult / sLrow[r] : 0.f;
+          const float inv = row_inv(sLrow[r], v_mult);
           const int i = r / p.group, gh = r % p.group;
           const int64_t orow = (out_row0 + i) * p.num_q_heads + f_h * p.group + gh;
           if constexpr (kPartial) {
             *reinterpret_cast<float4*>(p.out_o + orow * kHeadDim + 4 * dq) =
                 make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-            if (dq == 0)
-              p.out_lse[orow] = sLrow[r] > 0.f ? (M + __log2f(sLrow[r])) * kLn2 : -INFINITY;
+            if (dq == 0) p.out_lse[orow] = row_lse(M, sLrow[r]);
           } else {
             __half2 h01 = __floats2half2_rn(acc.x * inv, acc.y * inv);
             __half2 h23 = __floats2half2_rn(acc.z * inv, acc.w * inv);
@@ -1438,11 +1445,11 @@ __global__ void __launch_bounds__(AttnCfg<KVT, NT, kPair>::kThreads,
         const int i = r / p.group, gh = r % p.group;
         const int64_t orow = (out_row0 + i) * p.num_q_heads + f_h * p.group + gh;
         if (cnt == 1) {
-          const float f = l > 0.f ? v_mult / l : 0.f;
+          const float f = row_inv(l, v_mult);
           if constexpr (kPartial) {
             *reinterpret_cast<float4*>(p.out_o + orow * kHeadDim + 4 * dq) =
                 make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
-            if (dq == 0) p.out_lse[orow] = l > 0.f ? (M + __log2f(l)) * kLn2 : -INFINITY;
+            if (dq == 0) p.out_lse[orow] = row_lse(M, l);
           } else {
             __half2 h01 = __floats2half2_rn(acc.x * f, acc.y * f);
             __half2 h23 = __floats2half2_rn(acc.z * f, acc.w * f);
@@ -1476,14 +1483,14 @@ __global__ void __launch_bounds__(AttnCfg<KVT, NT, kPair>::kThreads,
           const int i = r / p.group, gh = r % p.group;
           const int64_t orow = (out_row0 + i) * p.num_q_heads + f_h * p.group + gh;
           if (cnt == 1) {
-            const float f = l > 0.f ? v_mult / l : 0.f;
+            const float f = row_inv(l, v_mult);
             if constexpr (kPartial) {
               float4* dst = reinterpret_cast<float4*>(p.out_o + orow * kHeadDim + 16 * g);
 #pragma unroll
               for (int k4 = 0; k4 < 4; ++k4)
                 dst[k4] = make_float4(o[2 * k4][nt][c] * f, o[2 * k4][nt][c + 2] * f,
                                       o[2 * k4 + 1][nt][c] * f, o[2 * k4 + 1][nt][c + 2] * f);
-              if (g == 0) p.out_lse[orow] = l > 0.f ? (M + __log2f(l)) * kLn2 : -INFINITY;
+              if (g == 0) p.out_lse[orow] = row_lse(M, l);
             } else {
               uint32_t hv[8];
 #pragma unroll
@@ -1583,13 +1590,13 @@ __global__ void __launch_bounds__(AttnCfg<KVT, NT, kPair>::kThreads,
             }
             M = Mn;
           }
-          const float inv = l > 0.f ? v_mult / l : 0.f;
+          const float inv = row_inv(l, v_mult);
           const int i = r / p.group, gh = r % p.group;
           const int64_t orow = (out_row0 + i) * p.num_q_heads + f_h * p.group + gh;
           if constexpr (kPartial) {
             *reinterpret_cast<float4*>(p.out_o + orow * kHeadDim + 4 * dq) =
                 make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-            if (dq == 0) p.out_lse[orow] = l > 0.f ? (M + __log2f(l)) * kLn2 : -INFINITY;
+            if (dq == 0) p.out_lse[orow] = row_lse(M, l);
           } else {
             __half2 h01 = __floats2half2_rn(acc.x * inv, acc.y * inv);
             __half2 h23 = __floats2half2_rn(acc.z * inv, acc.w * inv);
@@ -1643,13 +1650,13 @@ __global__ void __launch_bounds__(AttnCfg<KVT, NT, kPair>::kThreads,
             acc.z += w * v.z;
             acc.w += w * v.w;
           }
-          const float f = l > 0.f ? 1.f / l : 0.f;
+          const float f = row_inv(l, 1.f);
           const int i = r / p.group, gh = r % p.group;
           const int64_t orow = (int64_t)i * p.num_q_heads + gh;
           if constexpr (kPartial) {
             *reinterpret_cast<float4*>(p.out_o + orow * kHeadDim + 4 * dq) =
                 make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
-            if (dq == 0) p.out_lse[orow] = l > 0.f ? (M + __log2f(l)) * kLn2 : -INFINITY;
+            if (dq == 0) p.out_lse[orow] = row_lse(M, l);
           } else {
             __half2 h01 = __floats2half2_rn(acc.x * f, acc.y * f);
             __half2 h23 = __floats2half2_rn(acc.z * f, acc.w * f);

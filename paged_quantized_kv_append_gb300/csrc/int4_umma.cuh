@@ -619,10 +619,10 @@ __global__ void __launch_bounds__(I4Cfg<NT>::kThreads, 1) int4_umma_kernel(const
         if (cur.cnt == 1) {
           const int64_t orow =
               (out_row0 + r / p.group) * p.num_q_heads + cur.h * p.group + r % p.group;
-          const float res = l > 0.f ? val / l : 0.f;
+          const float res = l == 0.f ? 0.f : val / l;
           if constexpr (kPartial) {
             p.out_o[orow * kHeadDim + t] = res;
-            if (t == 0) p.out_lse[orow] = l > 0.f ? (ml[r] + __log2f(l)) * kLn2 : -INFINITY;
+            if (t == 0) p.out_lse[orow] = row_lse(ml[r], l);
           } else {
             p.out[orow * kHeadDim + t] = __half_as_ushort(__float2half_rn(res));
           }
@@ -695,13 +695,13 @@ __global__ void __launch_bounds__(I4Cfg<NT>::kThreads, 1) int4_umma_kernel(const
               }
               M = Mn;
             }
-            const float inv = l > 0.f ? 1.f / l : 0.f;
+            const float inv = row_inv(l, 1.f);
             const int64_t orow =
                 (out_row0 + r / p.group) * p.num_q_heads + cur.h * p.group + r % p.group;
             if constexpr (kPartial) {
               *reinterpret_cast<float4*>(p.out_o + orow * kHeadDim + 4 * dq) =
                   make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-              if (dq == 0) p.out_lse[orow] = l > 0.f ? (M + __log2f(l)) * kLn2 : -INFINITY;
+              if (dq == 0) p.out_lse[orow] = row_lse(M, l);
             } else {
               uint2 pk;
               pk.x = pack_half2(acc.x * inv, acc.y * inv);

@@ -271,7 +271,7 @@ __global__ void __launch_bounds__(256) shared_merge_kernel(const SharedParams p,
     }
   }
   if (!in) return;
-  float inv = l > 0.f ? 1.f / l : 0.f;
+  float inv = row_inv(l, 1.f);
   if (scaled) inv *= __ldg(p.v_scale + (p.scale_per_head ? row.h : 0));
   __half2 h01 = __floats2half2_rn(acc.x * inv, acc.y * inv);
   __half2 h23 = __floats2half2_rn(acc.z * inv, acc.w * inv);
