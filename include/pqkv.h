@@ -310,8 +310,8 @@ int pqkv_paged_attention_window(const void* q, void* out, const void* pages, int
  *   seq_lens   int32 [num_seqs]: keys of each sequence held here (0 allowed);
  *   q_pos      int32 [num_seqs] (device): local index of query 0's position,
  *              i.e. its global position minus the global index of this
- *              share's first key; query i sees local keys j <= q_pos + i
- *              (any value: negative hides every key from the row);
+ *              share's first key; query i sees local keys j <= q_pos + i,
+ *              j < seq_lens[s] (any value: a negative position sees none);
  *   out_o      fp32 [num_seqs*q_len][num_q_heads][head_dim]: O / l of the
  *              share (0 for a row that sees no key);
  *   out_lse    fp32 [num_seqs*q_len][num_q_heads]: m + ln(l), the natural-log

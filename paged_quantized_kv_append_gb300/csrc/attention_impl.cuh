@@ -938,19 +938,22 @@ __global__ void __launch_bounds__(AttnCfg<KVT, NT, kPair>::kThreads,
         v_mult = vs;
       }
       inv_qk_scale = 1.f / qk_scale;
-      if constexpr (kPartial) lim_min = Cfg::kTree ? qpos_e : p.q_pos[f_s];
-      else lim_min = L - p.q_len;
-      // causal limit per row: the last key position row r may see
+      // causal limit per row: the last key position row r may see, at most the last key
+      // there is.  (In a partial call the queries may lie anywhere before or behind the
+      // share's keys; the bound on q_pos lets positions be added to it.)
+      int lim0 = L - p.q_len;
+      if constexpr (kPartial) lim0 = min(Cfg::kTree ? qpos_e : p.q_pos[f_s], 1 << 30);
+      lim_min = min(lim0, L - 1);
       if constexpr (Cfg::kRowsInSmem) {
         for (int r = tid; r < RP; r += nthr)
-          sLim[r] = r < p.rows ? lim_min + r / p.group : 0x7fffffff;
+          sLim[r] = r < p.rows ? min(lim0 + r / p.group, L - 1) : 0x7fffffff;
       } else {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
             const int r = 8 * nt + 2 * t + c;
-            lim[nt][c] = r < p.rows ? lim_min + r / p.group : 0x7fffffff;
+            lim[nt][c] = r < p.rows ? min(lim0 + r / p.group, L - 1) : 0x7fffffff;
           }
       }
       cur_seg = f_seg;
