@@ -375,6 +375,25 @@ class Workspace:
         return part
 
 
+def _what(x):
+    if not isinstance(x, torch.Tensor):
+        return type(x).__name__
+    return "%s of strides %s on %s" % (list(x.shape), list(x.stride()), x.device)
+
+
+def _scratch(workspace, idx, need, counter_bytes=0):
+    """Address and bytes of a call's workspace on cuda:idx: a Workspace's part, or a tensor."""
+    if isinstance(workspace, Workspace):
+        workspace = workspace.get(need, counter_bytes)
+        if workspace is None:
+            return None, 0
+    if not isinstance(workspace, torch.Tensor) or workspace.get_device() != idx \
+            or not workspace.is_contiguous():
+        raise ValueError("workspace must be a Workspace or a contiguous CUDA tensor on cuda:%d, "
+                         "got %s" % (idx, _what(workspace)))
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
 _default_ws = {}
 
 
@@ -415,15 +434,12 @@ def paged_attention(q, pages, block_table, seq_lens, q_len, kv_dtype, k_scale, v
     Hq = rows[1]
     if status is not None:
         _check_status(status, pages.device)
+    if window < 0:
+        raise ValueError("window must be >= 0")
     need = workspace_size(B, q_len, Hq, H, num_splits)
     if workspace is None:
         workspace = _default_workspace(pages.device)
-    ws = workspace.get(need, 4 * B * H) if isinstance(workspace, Workspace) else workspace
-    if ws is not None and ws.get_device() != idx:
-        _on_device(pages.device, workspace=ws)
-    ws_bytes = 0 if ws is None else ws.numel() * ws.element_size()
-    if window < 0:
-        raise ValueError("window must be >= 0")
+    ws, ws_bytes = _scratch(workspace, idx, need, 4 * B * H)
     lib = load_library()
     args = [q.data_ptr(), out.data_ptr(), pages.data_ptr(), N, block_table.data_ptr(),
             table[1], seq_lens.data_ptr(), B, q_len, Hq, H, HEAD_DIM, PAGE_SIZE, kd,
@@ -433,8 +449,7 @@ def paged_attention(q, pages, block_table, seq_lens, q_len, kv_dtype, k_scale, v
     if window > 0:
         fn = lib.pqkv_paged_attention_window
         args.append(window)
-    rc = _call_on(idx, stream, fn, *args, None if ws is None else ws.data_ptr(), ws_bytes,
-                  None if status is None else status.data_ptr())
+    rc = _call_on(idx, stream, fn, *args, ws, ws_bytes, None if status is None else status.data_ptr())
     if rc:
         _check(rc, "paged_attention")
     return out
@@ -504,16 +519,14 @@ def paged_attention_partial(q, pages, block_table, seq_lens, q_pos, q_len, kv_dt
     need = workspace_size(B, q_len, Hq, H, num_splits)
     if workspace is None:
         workspace = _default_workspace(dev)
-    ws = workspace.get(need, 4 * B * H) if isinstance(workspace, Workspace) else workspace
-    _on_device(dev, workspace=ws)
-    ws_bytes = 0 if ws is None else ws.numel() * ws.element_size()
+    ws, ws_bytes = _scratch(workspace, dev.index, need, 4 * B * H)
     lib = load_library()
     with torch.cuda.device(dev):
         rc = lib.pqkv_paged_attention_partial(
             _ptr(q), _ptr(pages), pages.shape[0], _ptr(block_table), block_table.shape[1],
             _ptr(seq_lens), _ptr(q_pos), B, q_len, Hq, H, HEAD_DIM, PAGE_SIZE, kd,
             _ptr(k_scale if kd in _SCALED else None), _ptr(v_scale if kd in _SCALED else None),
-            sph, num_splits, max_seq_len, _ptr(out_o), _ptr(out_lse), _ptr(ws), ws_bytes,
+            sph, num_splits, max_seq_len, _ptr(out_o), _ptr(out_lse), ws, ws_bytes,
             _ptr(status), _stream(q, stream))
     _check(rc, "paged_attention_partial")
     return out_o, out_lse
@@ -635,17 +648,12 @@ def paged_attention_shared_prefix(q, pages, block_table, seq_lens, group_offsets
         else:                            # owned by the stream it is used on
             with torch.cuda.stream(stream):
                 ws = torch.empty(need, dtype=torch.uint8, device=pages.device)
-    elif isinstance(ws, Workspace):
-        ws = ws.get(shared_prefix_workspace_size(B, M, q_len, Hq, H))
-    if ws is not None and (not isinstance(ws, torch.Tensor) or ws.get_device() != idx
-                           or not ws.is_contiguous()):
-        raise ValueError("workspace must be a Workspace or a contiguous tensor on cuda:%d" % idx)
+    at, ws_bytes = _scratch(ws, idx, shared_prefix_workspace_size(B, M, q_len, Hq, H))
     rc = _call_on(
         idx, stream, load_library().pqkv_paged_attention_shared_prefix, q.data_ptr(),
         out.data_ptr(), pages.data_ptr(), N, block_table.data_ptr(), W, seq_lens.data_ptr(), B,
         group_offsets.data_ptr(), prefix_lens.data_ptr(), M, q_len, Hq, H, HEAD_DIM, PAGE_SIZE, kd,
-        ks, vs, sph, max_seq_len, max_prefix_len, None if ws is None else ws.data_ptr(),
-        0 if ws is None else ws.numel() * ws.element_size(),
+        ks, vs, sph, max_seq_len, max_prefix_len, at, ws_bytes,
         None if status is None else status.data_ptr())
     if rc:
         _check(rc, "paged_attention_shared_prefix")
