@@ -18,6 +18,7 @@ page and kv-head a 16-token K tile followed by a V tile -- of uint8 codes
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import functools
 import os
@@ -347,32 +348,89 @@ class Workspace:
     """Zero-initialised device scratch for paged_attention, grown on demand.
 
     The kernels leave the merge counters at a call's start zeroed again after
-    every call, so one workspace serves any number of calls on one stream.  How
+    every call, so one workspace serves any number of calls, and graphs that captured calls,
+    which run one after another; calls that may overlap on the GPU need one each.  How
     many counters there are depends on the call's num_seqs and num_kv_heads; the
     counters of every call end at the same byte, ``head``, so that none has its
-    counters where another has had its partial results."""
+    counters where another has had its partial results.
+
+    A buffer is allocated and zeroed on the stream of the call that needs it.  One that
+    has become too small is kept, for the kernels and graphs that still use it, and the next
+    is at least twice as large, so that all of the old ones together are smaller."""
 
     def __init__(self, device="cuda"):
         self.device = torch.device(device)
         self.head = 1 << 18
         self.buf = None
         self._parts = {}
+        self._old = []
+        self._lock = threading.Lock()
 
-    def get(self, nbytes: int, counter_bytes: int = 0):
-        """``nbytes`` of scratch, the first ``counter_bytes`` of them counters."""
+    def get(self, nbytes: int, counter_bytes: int = 0, stream=None):
+        """``nbytes`` of scratch, the first ``counter_bytes`` of them counters, for a call on
+        ``stream`` (None: the device's current one)."""
         if nbytes == 0:
             return None
         counters = -(-counter_bytes // 256) * 256
-        while self.head < counters:
-            self.head, self.buf = 2 * self.head, None
-        need = self.head - counters + nbytes
-        if self.buf is None or self.buf.numel() < need:
-            self.buf = torch.zeros(max(need, 1 << 20), dtype=torch.uint8, device=self.device)
-            self._parts.clear()
-        part = self._parts.get(counters)
-        if part is None:                     # a slice costs a call more than a microsecond
-            part = self._parts[counters] = self.buf[self.head - counters:]
-        return part
+        part = self._parts.get(counters)     # (a slice costs a call more than a microsecond)
+        if part is not None and part.numel() >= nbytes:
+            return part
+        with self._lock:
+            head, buf = self.head, self.buf
+            while head < counters:
+                head, buf = 2 * head, None
+            need = head - counters + nbytes
+            if buf is None or buf.numel() < need:
+                if self.device.type == "cuda" and _capturing(self.device.index, stream):
+                    return _captured_scratch(self.device, nbytes, counters, stream)
+                if self.buf is not None:
+                    self._old.append(self.buf)
+                    need = max(need, 2 * self.buf.numel())
+                with _stream_of(self.device, stream):
+                    buf = torch.zeros(max(need, 1 << 20), dtype=torch.uint8, device=self.device)
+                self.head, self.buf, self._parts = head, buf, {}
+            part = self._parts[counters] = buf[head - counters:]
+            return part
+
+
+def _stream_of(device, stream):
+    """The context in which tensors are made on ``stream`` (None: the device's current one)."""
+    if stream is not None:
+        return torch.cuda.stream(stream)
+    return torch.cuda.device(device) if device.type == "cuda" else contextlib.nullcontext()
+
+
+def _capturing(idx, stream):
+    """Whether ``stream`` (None: the current one of cuda:idx) is being captured.  (torch asks the
+    current stream alone; its context managers would cost a call 8 microseconds.)"""
+    dev = torch._C._cuda_getDevice()
+    if stream is None:
+        if idx is None or idx == dev:
+            return torch._C._cuda_isCurrentStreamCapturing()
+        with torch.cuda.device(idx):
+            return torch._C._cuda_isCurrentStreamCapturing()
+    if stream.device_index != dev:
+        with torch.cuda.stream(stream):
+            return torch._C._cuda_isCurrentStreamCapturing()
+    was = torch._C._cuda_getCurrentStream(dev)
+    if was[0] == stream.stream_id:
+        return torch._C._cuda_isCurrentStreamCapturing()
+    set_stream = torch._C._cuda_setStream
+    try:
+        set_stream(stream_id=stream.stream_id, device_index=dev, device_type=stream.device_type)
+        return torch._C._cuda_isCurrentStreamCapturing()
+    finally:
+        set_stream(stream_id=was[0], device_index=was[1], device_type=was[2])
+
+
+def _captured_scratch(device, nbytes, counters, stream):
+    """Scratch of one captured call: memory of its graph, whose counters every replay zeroes.
+    (What is allocated and zeroed under a capture is neither there nor zero for another graph or
+    for an eager call.)"""
+    with _stream_of(device, stream):
+        buf = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        buf[:counters].zero_()
+    return buf
 
 
 def _what(x):
@@ -381,10 +439,10 @@ def _what(x):
     return "%s of strides %s on %s" % (list(x.shape), list(x.stride()), x.device)
 
 
-def _scratch(workspace, idx, need, counter_bytes=0):
+def _scratch(workspace, idx, stream, need, counter_bytes=0):
     """Address and bytes of a call's workspace on cuda:idx: a Workspace's part, or a tensor."""
     if isinstance(workspace, Workspace):
-        workspace = workspace.get(need, counter_bytes)
+        workspace = workspace.get(need, counter_bytes, stream)
         if workspace is None:
             return None, 0
     if not isinstance(workspace, torch.Tensor) or workspace.get_device() != idx \
@@ -439,7 +497,7 @@ def paged_attention(q, pages, block_table, seq_lens, q_len, kv_dtype, k_scale, v
     need = workspace_size(B, q_len, Hq, H, num_splits)
     if workspace is None:
         workspace = _default_workspace(pages.device)
-    ws, ws_bytes = _scratch(workspace, idx, need, 4 * B * H)
+    ws, ws_bytes = _scratch(workspace, idx, stream, need, 4 * B * H)
     lib = load_library()
     args = [q.data_ptr(), out.data_ptr(), pages.data_ptr(), N, block_table.data_ptr(),
             table[1], seq_lens.data_ptr(), B, q_len, Hq, H, HEAD_DIM, PAGE_SIZE, kd,
@@ -519,7 +577,7 @@ def paged_attention_partial(q, pages, block_table, seq_lens, q_pos, q_len, kv_dt
     need = workspace_size(B, q_len, Hq, H, num_splits)
     if workspace is None:
         workspace = _default_workspace(dev)
-    ws, ws_bytes = _scratch(workspace, dev.index, need, 4 * B * H)
+    ws, ws_bytes = _scratch(workspace, dev.index, stream, need, 4 * B * H)
     lib = load_library()
     with torch.cuda.device(dev):
         rc = lib.pqkv_paged_attention_partial(
@@ -648,7 +706,7 @@ def paged_attention_shared_prefix(q, pages, block_table, seq_lens, group_offsets
         else:                            # owned by the stream it is used on
             with torch.cuda.stream(stream):
                 ws = torch.empty(need, dtype=torch.uint8, device=pages.device)
-    at, ws_bytes = _scratch(ws, idx, shared_prefix_workspace_size(B, M, q_len, Hq, H))
+    at, ws_bytes = _scratch(ws, idx, stream, shared_prefix_workspace_size(B, M, q_len, Hq, H))
     rc = _call_on(
         idx, stream, load_library().pqkv_paged_attention_shared_prefix, q.data_ptr(),
         out.data_ptr(), pages.data_ptr(), N, block_table.data_ptr(), W, seq_lens.data_ptr(), B,
