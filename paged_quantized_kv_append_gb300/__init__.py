@@ -455,11 +455,21 @@ def _scratch(workspace, idx, stream, need, counter_bytes=0):
 _default_ws = {}
 
 
-def _default_workspace(device):
-    key = torch.device(device).index
-    if key not in _default_ws:
-        _default_ws[key] = Workspace(device)
-    return _default_ws[key]
+def _default_scratch(idx, stream, need, counter_bytes):
+    """_scratch of a call that was given no workspace: one per stream, whose calls run one after
+    another; a captured call's own, as its graph may be replayed beside any other."""
+    if not need:
+        return None, 0
+    if _capturing(idx, stream):
+        part = _captured_scratch(torch.device("cuda", idx), need, -(-counter_bytes // 256) * 256,
+                                 stream)
+    else:
+        raw = torch._C._cuda_getCurrentRawStream(idx) if stream is None else stream.cuda_stream
+        ws = _default_ws.get((idx, raw))
+        if ws is None:
+            ws = _default_ws.setdefault((idx, raw), Workspace(torch.device("cuda", idx)))
+        part = ws.get(need, counter_bytes, stream)
+    return part.data_ptr(), part.numel()
 
 
 def paged_attention(q, pages, block_table, seq_lens, q_len, kv_dtype, k_scale, v_scale, out,
@@ -496,8 +506,9 @@ def paged_attention(q, pages, block_table, seq_lens, q_len, kv_dtype, k_scale, v
         raise ValueError("window must be >= 0")
     need = workspace_size(B, q_len, Hq, H, num_splits)
     if workspace is None:
-        workspace = _default_workspace(pages.device)
-    ws, ws_bytes = _scratch(workspace, idx, stream, need, 4 * B * H)
+        ws, ws_bytes = _default_scratch(idx, stream, need, 4 * B * H)
+    else:
+        ws, ws_bytes = _scratch(workspace, idx, stream, need, 4 * B * H)
     lib = load_library()
     args = [q.data_ptr(), out.data_ptr(), pages.data_ptr(), N, block_table.data_ptr(),
             table[1], seq_lens.data_ptr(), B, q_len, Hq, H, HEAD_DIM, PAGE_SIZE, kd,
@@ -576,8 +587,9 @@ def paged_attention_partial(q, pages, block_table, seq_lens, q_pos, q_len, kv_dt
     _check_status(status, dev)
     need = workspace_size(B, q_len, Hq, H, num_splits)
     if workspace is None:
-        workspace = _default_workspace(dev)
-    ws, ws_bytes = _scratch(workspace, dev.index, stream, need, 4 * B * H)
+        ws, ws_bytes = _default_scratch(dev.index, stream, need, 4 * B * H)
+    else:
+        ws, ws_bytes = _scratch(workspace, dev.index, stream, need, 4 * B * H)
     lib = load_library()
     with torch.cuda.device(dev):
         rc = lib.pqkv_paged_attention_partial(

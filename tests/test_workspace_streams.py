@@ -1,5 +1,5 @@
 """Workspaces on the streams that use them: zeroed in the call's own order, kept while an earlier
-call or graph may use them."""
+call or graph may use them, one per stream where the caller gave none."""
 import contextlib
 
 import pytest
@@ -98,6 +98,25 @@ def test_first_and_growing_calls_on_a_side_stream():
             assert torch.equal(o, c.want)
 
 
+@pytest.mark.gpu
+def test_streams_without_a_workspace_do_not_meet():
+    require_gpu()
+    cases = [Call(3, [3000, 70, 900]), Call(4, [5000, 16]), Call(5, [900] * 8)]
+    streams = [torch.cuda.Stream() for _ in cases]
+    outs = [[torch.full_like(c.args[0], float("nan")) for _ in range(20)] for c in cases]
+    torch.cuda.synchronize()
+    for k in range(20):
+        for c, st, o in zip(cases, streams, outs):
+            if k % 2:
+                c.into(o[k], stream=st)
+            else:
+                with torch.cuda.stream(st):
+                    c.into(o[k])
+    torch.cuda.synchronize()
+    for c, o in zip(cases, outs):
+        assert all(torch.equal(x, c.want) for x in o)
+
+
 def _captured(call, **kw):
     out = torch.empty_like(call.args[0])
     g = torch.cuda.CUDAGraph()
@@ -105,6 +124,28 @@ def _captured(call, **kw):
         call.into(out, **kw)
         torch.empty(1 << 22, dtype=torch.uint8, device="cuda").fill_(255)   # of the graph's memory
     return g, out
+
+
+@pytest.mark.gpu
+def test_graphs_without_a_workspace_replay_side_by_side():
+    """Captured on one stream, replayed on two at once, beside an eager call."""
+    require_gpu()
+    a, b, c = Call(6, [3000, 70, 900]), Call(7, [5000, 16]), Call(8, [900] * 8)
+    graphs = [_captured(x) for x in (a, b)]
+    streams = [torch.cuda.Stream() for _ in graphs]
+    for _ in range(10):
+        for _, out in graphs:
+            out.fill_(float("nan"))
+        torch.cuda.synchronize()
+        for _ in range(5):
+            for (g, _), st in zip(graphs, streams):
+                with torch.cuda.stream(st):
+                    g.replay()
+            got = c()
+        torch.cuda.synchronize()
+        assert torch.equal(got, c.want)
+        for (_, out), x in zip(graphs, (a, b)):
+            assert torch.equal(out, x.want)
 
 
 @pytest.mark.gpu
@@ -126,3 +167,32 @@ def test_a_workspace_that_is_first_used_in_a_capture():
             g.replay()
             assert torch.equal(out, x.want)
         assert torch.equal(a(workspace=ws), a.want)
+
+
+@pytest.mark.gpu
+def test_a_call_on_a_given_stream_that_is_captured():
+    """Begun and ended on that stream, which is not the current one when the call is made; the
+    current stream stays what it was."""
+    require_gpu()
+    a, other = Call(12, [3000, 70, 900]), torch.cuda.Stream()
+    out, st, g = torch.empty_like(a.args[0]), torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    a.into(out, stream=st)                       # st has an eager workspace of its own
+    torch.cuda.synchronize()
+    before = set(pq._default_ws)
+    with torch.cuda.stream(st):
+        g.capture_begin()
+    try:
+        with torch.cuda.stream(other):
+            a.into(out, stream=st)
+            assert torch.cuda.current_stream() == other
+    finally:
+        with torch.cuda.stream(st):
+            g.capture_end()
+    assert set(pq._default_ws) == before
+    for _ in range(3):
+        out.fill_(float("nan"))
+        torch.cuda.synchronize()
+        g.replay()
+        eager = [a(stream=st) for _ in range(3)]
+        torch.cuda.synchronize()
+        assert torch.equal(out, a.want) and all(torch.equal(x, a.want) for x in eager)
