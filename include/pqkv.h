@@ -146,6 +146,9 @@ enum {
  * fp32(x)/s rounded half to even and clamped to [-7, 7] (NaN -> 0; all 0 for s = 0).
  * A scale has 8 significant bits, so every value code * s is an fp16 value.
  * Values beyond +-19040 saturate.  k_scale / v_scale are ignored (may be NULL).
+ * How exact: rows of N(0, 1) values are off by 9.7 % (rms, of their rms), where
+ * E4M3 under one scale is off by 2.6 %, INT8 1.1 % and INT8_ROW 0.7 %; with 1 %
+ * of the values twenty times as large 15.7 % (E4M3 2.6, INT8 8.0, INT8_ROW 2.1).
  *
  *   k, v            fp16 [num_tokens][num_kv_heads][head_dim]; heads and dims
  *                   contiguous, tokens `k_token_stride` / `v_token_stride`
@@ -207,8 +210,8 @@ int pqkv_kv_read(const void* pages, int64_t num_pages, const int32_t* block_tabl
 /*
  * pqkv_paged_attention_workspace_size -- bytes of device workspace that
  * pqkv_paged_attention needs for these sizes and split mode (0 if none).
- * num_splits as in pqkv_paged_attention.  Pure host function; it queries the
- * current device's SM count.  The first PQKV_COUNTER_BYTES(num_seqs,
+ * num_splits as in pqkv_paged_attention.  Pure host function; for balanced
+ * calls the size is that of the largest grid on any device.  The first PQKV_COUNTER_BYTES(num_seqs,
  * num_kv_heads) bytes of the workspace are merge counters: they must be zero
  * before the first call, and every call that returns with *status clean
  * leaves them zero again.  Zero the whole workspace once after allocating it

@@ -482,6 +482,11 @@ def paged_attention(q, pages, block_table, seq_lens, q_len, kv_dtype, k_scale, v
     the q_len new ones included).  num_splits 0 balances key pages over the
     GPU; k >= 1 cuts each (sequence, kv-head) into k partitions.  window > 0:
     query position p sees only keys p - window + 1 .. p (sliding window).
+
+    workspace: a Workspace, or a zeroed tensor of workspace_size() bytes, that no other call
+    uses at the same time.  None: one that is kept for the stream, or, in a capture by
+    torch.cuda.graph, memory of that graph; under another kind of capture, and where calls go on
+    after a reported timeout (which leaves the workspace to be zeroed), give one.
     """
     kd = _dtype_id(kv_dtype)
     _check_pages(pages, kd)

@@ -372,13 +372,13 @@ __device__ __forceinline__ uint4 lds128(const uint8_t* base, int line, int chunk
   return *reinterpret_cast<const uint4*>(base + line * 128 + ((chunk ^ (line & 7)) << 4));
 }
 
-// The Q^T B-fragments live in a shared table [4][NT][32] of 16-byte entries:
-// a lane's fragments of k-steps 2*k2 and 2*k2 + 1 of one row tile side by
-// side, so one 16-byte load serves two k-steps.
 // the formats whose k_scale / v_scale arguments are read
 template <int KVT>
 constexpr bool kScaleArgs = KVT == PQKV_KV_FP8_E4M3 || KVT == PQKV_KV_INT8;
 
+// The Q^T B-fragments live in a shared table [4][NT][32] of 16-byte entries:
+// a lane's fragments of k-steps 2*k2 and 2*k2 + 1 of one row tile side by
+// side, so one 16-byte load serves two k-steps.
 template <int NT>
 struct QFrags {
   const uint4* tab;

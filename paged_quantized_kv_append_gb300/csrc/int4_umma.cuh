@@ -14,14 +14,19 @@
 // to the thread's TMEM lane, V's to shared memory), 12-15 bring a fragment's query rows
 // and write its O, m and l (and merge a segment's partial results, when the CTA is the
 // segment's last), 16 and 19 the copies, 17 the products, 18 the fragments of the share.
-// Every stage is two deep, the codes up to eight tiles, so a fragment's end overlaps the
+// Every stage is two deep, the codes five to seven tiles, so a fragment's end overlaps the
 // next one.
 //
-// What bounds it: the instructions around a tile.  The 18432 bytes of a tile are 780 cycles
-// of an SM's share of the memory; a tile takes 1500 (8 x 131072 keys, 8 heads, 20 rows:
-// 343 us, 3.52 TB/s, 52 % of the measured copy; 32 rows 45 %; one row of 16 heads 51 %).  K's and
-// V's warps work all of that time: four turns of 145 cycles for 16 values a thread and
-// 130 to 180 for their store.  Tried and slower: a second group of warps each for K and V
+// What bounds it: the instructions around a tile, in two chains.  The 18432 bytes of a tile
+// are 780 cycles of an SM's share of the memory; a tile takes 1500 (8 x 131072 keys, 8 heads,
+// 20 rows: 343 us, 3.52 TB/s, 52 % of the measured copy; 32 rows 45 %; one row of 16 heads
+// 51 %).  K's and V's warps work all of that time: four turns, each of 145 cycles for a group's
+// 32 values a thread and 130 to 180 for their store.  And a kernel without any widening still
+// took 250 us, 1090 cycles a tile: a tile's scores landed, their load out of TMEM, the vote of
+// the four softmax warps, the probabilities' store and V's product follow one another.
+// The register split below was measured with 24 rows alone.  It leaves the softmax warps of
+// 8 and 16 rows registers to spare, and the 32-row kernels spill 88 to 112 bytes a thread.
+// Tried and slower: a second group of warps each for K and V
 // (355 us), a second softmax for every other tile (460), waits by one warp of a group and a
 // barrier (400), one warp for the scores' products and one for V's (365), K and V in one loop
 // (393), and their rows unrolled in full (600): a scheduler's warps run a code each, and
@@ -68,7 +73,7 @@ struct I4Cfg {
                 "registers of the launch");
   static constexpr int kRP = 8 * NT;                     // rows that are computed
   static constexpr int kN = NT <= 2 ? 16 : 32;           // columns of the products
-  static constexpr int kMaxStages = 8;                   // of the codes, as far as they fit
+  static constexpr int kMaxStages = 7;                   // of the codes, as far as they fit
   static constexpr int kSlab = kI4Pages * kI4PageBytes;  // a tile's codes and scales
   static constexpr int kVTile = 2 * 128 * 128;           // two halves: 128 rows of 64 values
   static constexpr int kPTile = 128 * 64;                // 128 rows of up to 32 values
@@ -94,7 +99,10 @@ struct I4Cfg {
   static __host__ __device__ constexpr int smem_bytes(int num_seqs) {
     return kSlabOff + stages(num_seqs) * kSlab + pre_bytes(num_seqs);
   }
-  static_assert(stages(PQKV_MAX_SEQS) >= 4, "shared memory of the largest launch");
+  // (odd numbers too: each of the two copying warps steps over every other stage, and comes to
+  // the rest of them when it wraps)
+  static_assert(stages(1) == kMaxStages && stages(PQKV_MAX_SEQS) == (kN == 16 ? 6 : 5),
+                "shared memory of the smallest and of the largest launch");
   // TMEM columns
   static constexpr uint32_t kTmemK = 0, kTmemS = 128, kTmemO = 192;
   // kind::f16, fp32 D, M 128; S: A and B with their values along K; O: both along M and N

@@ -11,8 +11,9 @@ extern "C" {
 
 /*
  * pqkv_testing_attention_wait_timeout -- pqkv_paged_attention (same
- * arguments, E4M3 and balanced INT4_GROUP pools with 17..24 query rows per kv-head only; for
- * the latter skip_page counts tiles of 128 keys) in a test mode of its bounded waits: block `skip_block` never issues the tile copy of
+ * arguments, E4M3 and balanced INT4_GROUP pools with 17..24 query rows per
+ * kv-head only; for the latter skip_page counts tiles of 128 keys) in a test
+ * mode of its bounded waits: block `skip_block` never issues the tile copy of
  * page `skip_page` of its share, so the warp that owns that page waits for a
  * tile that never arrives.  Waits give up after 1 ms (instead of 1 s); the
  * kernel then sets PQKV_DEV_TIMEOUT in *status, waits for every copy it did

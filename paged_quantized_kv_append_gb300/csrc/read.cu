@@ -9,10 +9,11 @@
 // E4M3's and INT8's product with an fp32 scale is rounded to fp32 first).
 //
 // A copy that widens: per (token, kv-head) 512 bytes are written and 144 to 512 read, so
-// DRAM bounds it (131072 E4M3 tokens of 8 heads: 5.7 TB/s, 83 % of the measured copy; 178000 at
-// 4 bits: 6.0, 89 %; tiny calls 2.7 us).  A thread takes 16 values (4 bits: 32, a group): a block's threads lie along
-// a token's K heads, then its V heads, then the next token, so that stores run over whole
-// rows (32 or 64 bytes a lane) and the request and page are looked up for neighbouring tokens.
+// DRAM bounds it (131072 E4M3 tokens of 8 heads: 5.7 TB/s, 84 % of the measured copy; 178000
+// at 4 bits: 6.0, 89 %; tiny calls 2.7 us).  A thread takes 16 values (4 bits: 32, a group):
+// a block's threads lie along a token's K heads, then its V heads, then the next token, so
+// that stores run over whole rows (32 or 64 bytes a lane) and the request and page are looked
+// up for neighbouring tokens.
 #include "block_scan.cuh"
 #include "pqkv_common.cuh"
 
