@@ -943,17 +943,20 @@ __global__ void __launch_bounds__(AttnCfg<KVT, NT, kPair>::kThreads,
       // share's keys; the bound on q_pos lets positions be added to it.)
       int lim0 = L - p.q_len;
       if constexpr (kPartial) lim0 = min(Cfg::kTree ? qpos_e : p.q_pos[f_s], 1 << 30);
-      lim_min = min(lim0, L - 1);
+      // (elsewhere no row's limit is behind the last key; taken there too, the
+      // minimum made an E4M3 verify of 2 x 512K tokens 510 -> 515 us)
+      const int last = kPartial ? L - 1 : 0x7fffffff;
+      lim_min = min(lim0, last);
       if constexpr (Cfg::kRowsInSmem) {
         for (int r = tid; r < RP; r += nthr)
-          sLim[r] = r < p.rows ? min(lim0 + r / p.group, L - 1) : 0x7fffffff;
+          sLim[r] = r < p.rows ? min(lim0 + r / p.group, last) : 0x7fffffff;
       } else {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
             const int r = 8 * nt + 2 * t + c;
-            lim[nt][c] = r < p.rows ? min(lim0 + r / p.group, L - 1) : 0x7fffffff;
+            lim[nt][c] = r < p.rows ? min(lim0 + r / p.group, last) : 0x7fffffff;
           }
       }
       cur_seg = f_seg;
