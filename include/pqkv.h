@@ -245,6 +245,8 @@ size_t pqkv_paged_attention_workspace_size(int32_t num_seqs, int32_t q_len,
  * A NaN among the scores of the keys that a row sees (from a NaN or an infinity in its
  * query, or in a K) makes the row NaN, however the keys are split; a row whose scores are
  * all -inf gets 0.
+ * Scores may be up to 2^26 in size: from 2^28 on an fp32 step of a score is a factor that
+ * fp16 probabilities do not hold.
  *
  *   q, out            fp16 [num_seqs*q_len][num_q_heads][head_dim], contiguous.
  *   pages             the pool (layout above), num_pages pages, 16-byte aligned.
